@@ -11,6 +11,9 @@
  *   gs_project_fwd    the EWA projection of 3D Gaussians that feeds the intersection step,
  *   gs_bin_tiles      fixed-capacity per-tile bins (the alternative to the first three steps), composited by
  *                     gs_rasterize_fwd_bins.
+ * The last group trains a layer of experts that predicts the splats' attributes (gs_rasterize_bwd gives the
+ * gradient it starts from): gs_layer_norm_fwd and _bwd, gs_expert_plan, gs_expert_dispatch, gs_expert_combine and
+ * _bwd, gs_orthogonalize.
  *
  * Definitions follow these pages:
  *   [gsplat]     gsplat 1.0.0 Ruby gem, native C extension, intersections.c (gs_tile_bits, gs_bounds,
@@ -343,6 +346,105 @@ gs_status gs_rasterize_bwd(const float *means2d, const float *conics, const floa
                            const float *grad_render_alphas, float *grad_means2d, float *grad_conics,
                            float *grad_colors, float *grad_opacities, float *grad_backgrounds,
                            float *grad_means2d_abs, void *stream);
+
+/* ------------------------------------------------------------------------------------------------------------
+ * Training operators of a layer of experts. Their arrays hold one of three element types, named by a gs_dtype;
+ * sums, statistics and products are formed in float32 or wider and rounded once where they are stored. The order of
+ * every sum depends on the sizes alone: the same inputs give the same bits on every run. Rows may start at any
+ * multiple of the element's size.
+ */
+typedef enum gs_dtype {
+    GS_F32 = 0,
+    GS_BF16 = 1,
+    GS_F16 = 2
+} gs_dtype;
+
+/* Layer norm over the last axis.
+ *
+ * For each row x of `rows` rows of `dim` elements: mean = sum(x) / dim, rstd = 1 / sqrt(sum((x - mean)^2) / dim +
+ * eps), y = (x - mean) * rstd * weight + bias.
+ * x, y              [rows, dim] of dtype; may not overlap
+ * weight, bias      [dim] of weight_dtype (dtype or GS_F32); bias may be NULL: no bias
+ * mean, rstd        [rows] float32, the backward's inputs; both may be NULL (inference)
+ * Limits: 0 <= rows < 2^31, 1 <= dim < 2^31, eps >= 0. rows = 0 launches nothing. Asynchronous.
+ */
+gs_status gs_layer_norm_fwd(const void *x, const void *weight, const void *bias, int64_t rows, int64_t dim, float eps,
+                            int dtype, int weight_dtype, void *y, float *mean, float *rstd, void *stream);
+
+/* Backward of gs_layer_norm_fwd for L = sum(grad_y * y), with xh = (x - mean) * rstd and g = grad_y * weight:
+ *   grad_x = rstd * (g - sum(g) / dim - xh * sum(g * xh) / dim)   (per row)
+ *   grad_weight = sum over rows of grad_y * xh,   grad_bias = sum over rows of grad_y.
+ * grad_x has x's type, grad_weight and grad_bias the weight's. grad_bias may be NULL (not computed). With rows = 0
+ * the two sums are zeros. All outputs are overwritten. workspace: gs_layer_norm_bwd_workspace_bytes(rows, dim)
+ * bytes (0 for sizes out of range), float32 partial sums. Limits as the forward's. Asynchronous.
+ */
+size_t gs_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+
+gs_status gs_layer_norm_bwd(const void *x, const void *weight, const float *mean, const float *rstd,
+                            const void *grad_y, int64_t rows, int64_t dim, int dtype, int weight_dtype, void *grad_x,
+                            void *grad_weight, void *grad_bias, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/* Tokens sorted by expert.
+ *
+ * ids [tokens, choices] int32: the expert of each (token, choice) pair; a value outside [0, experts) drops the pair.
+ * With pair number p = token * choices + choice, the kept pairs take rows 0, 1, ... in ascending order of
+ * (expert, p). Writes
+ * offsets [experts + 1] int32: expert e has rows [offsets[e], offsets[e + 1]); offsets[experts] pairs are kept
+ * rows    [tokens, choices] int32: each pair's row, -1 if dropped
+ * pairs   [tokens * choices] int32: each row's pair, -1 in the rows past the last kept one
+ * Limits: 0 <= tokens, 1 <= choices, tokens * choices < 2^31, 1 <= experts <= 4096. Asynchronous.
+ * workspace: gs_expert_plan_workspace_bytes(tokens, choices, experts) bytes (0 for sizes out of range).
+ */
+size_t gs_expert_plan_workspace_bytes(int64_t tokens, int64_t choices, int experts);
+
+gs_status gs_expert_plan(const int32_t *ids, int64_t tokens, int64_t choices, int experts, int32_t *offsets,
+                         int32_t *rows, int32_t *pairs, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Each token's row copied to the rows of its kept pairs: sent[rows[t, k]] = x[t]; the rows from offsets[experts]
+ * on become zeros. x [tokens, dim], sent [tokens * choices, dim] of dtype. offsets and rows as gs_expert_plan wrote
+ * them (a row number outside the output is skipped). Its gradient is gs_expert_combine without weights.
+ * Limits of gs_expert_plan, 1 <= dim < 2^31. Asynchronous.
+ */
+gs_status gs_expert_dispatch(const void *x, const int32_t *offsets, const int32_t *rows, int64_t tokens,
+                             int64_t choices, int experts, int64_t dim, int dtype, void *sent, void *stream);
+
+/* Each token's sum over its kept pairs, in ascending choice order and float32: y[t] = sum_k weights[t, k] *
+ * source[rows[t, k]]; a token with no kept pair gets zeros. Dropped pairs' weights and the rows past the kept ones
+ * are not read. source [tokens * choices, dim], y [tokens, dim] of dtype; weights [tokens, choices] float32, or
+ * NULL: ones. Limits as gs_expert_dispatch. Asynchronous.
+ */
+gs_status gs_expert_combine(const void *source, const int32_t *rows, const float *weights, int64_t tokens,
+                            int64_t choices, int64_t dim, int dtype, void *y, void *stream);
+
+/* Backward of the weighted gs_expert_combine for L = sum(grad_y * y):
+ *   grad_source[rows[t, k]] = weights[t, k] * grad_y[t],  zeros in the rows from offsets[experts] on
+ *   grad_weights[t, k] = sum(grad_y[t] * source[rows[t, k]]),  0 for a dropped pair (float32).
+ * Limits as gs_expert_dispatch. Asynchronous.
+ */
+gs_status gs_expert_combine_bwd(const void *source, const int32_t *offsets, const int32_t *rows,
+                                const float *weights, const void *grad_y, int64_t tokens, int64_t choices,
+                                int experts, int64_t dim, int dtype, void *grad_source, float *grad_weights,
+                                void *stream);
+
+/* Orthogonalised update of each matrix of a batch by Newton-Schulz steps (an odd matrix polynomial that moves every
+ * singular value towards 1).
+ *
+ * X = update / (|update| + eps) with the Frobenius norm of each matrix; `steps` times A = X X^T, X = a X +
+ * (b A + c A A) X, with (a, b, c) = coefficients (X transposed around the steps where m > n, which gives the same
+ * result with the smaller products). out = X, in update's type.
+ * update, out [batch, m, n] of dtype; out may be update. The norm's sums are float64. X, A and b A + c A A are held
+ * as pairs of float16 (high and low part, 22 bits together, scaled by a power of two). Every singular value must
+ * stay below 16 and every entry of b A + c A A below 64 in magnitude, as they do for coefficients that converge.
+ * A matrix that holds an infinity or NaN gives NaN; others in the batch are not affected.
+ * Limits: 0 <= batch <= 65535, 1 <= m, n <= 65536, batch * m * n < 2^40, 0 <= steps <= 100. Asynchronous.
+ * workspace: gs_orthogonalize_workspace_bytes(batch, m, n) bytes (0 for sizes out of range).
+ */
+size_t gs_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n);
+
+gs_status gs_orthogonalize(const void *update, int64_t batch, int64_t m, int64_t n, int steps, float a, float b,
+                           float c, float eps, int dtype, void *out, void *workspace, size_t workspace_bytes,
+                           void *stream);
 
 #ifdef __cplusplus
 }

@@ -24,7 +24,11 @@ EXPORTS = ("gs_last_error", "gs_isect_workspace_bytes", "gs_isect_tiles", "gs_so
            "gs_sort_keys", "gs_tile_ranges_workspace_bytes", "gs_tile_ranges", "gs_rasterize_workspace_bytes",
            "gs_rasterize_fwd", "gs_rasterize_fwd_hwexp", "gs_rasterize_fwd_traced", "gs_rasterize_bwd",
            "gs_project_fwd", "gs_bin_tiles", "gs_rasterize_fwd_bins", "gs_set_spin_limit", "gs_device_check",
-           "gs_sort_keys_static")
+           "gs_sort_keys_static", "gs_layer_norm_fwd", "gs_layer_norm_bwd_workspace_bytes", "gs_layer_norm_bwd",
+           "gs_expert_plan_workspace_bytes", "gs_expert_plan", "gs_expert_dispatch", "gs_expert_combine",
+           "gs_expert_combine_bwd", "gs_orthogonalize_workspace_bytes", "gs_orthogonalize")
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # gs_dtype
 
 
 class GsError(RuntimeError):
@@ -79,6 +83,21 @@ def load_library(path: str = LIB_PATH):
     lib.gs_sort_keys_static.argtypes, lib.gs_sort_keys_static.restype = [P, P, I64, I32, P], I32
     lib.gs_set_spin_limit.argtypes, lib.gs_set_spin_limit.restype = [ctypes.c_uint32], ctypes.c_uint32
     lib.gs_device_check.argtypes, lib.gs_device_check.restype = [P], I32
+    lib.gs_layer_norm_fwd.argtypes = [P, P, P, I64, I64, F, I32, I32, P, P, P, P]
+    lib.gs_layer_norm_fwd.restype = I32
+    lib.gs_layer_norm_bwd_workspace_bytes.argtypes, lib.gs_layer_norm_bwd_workspace_bytes.restype = [I64, I64], SZ
+    lib.gs_layer_norm_bwd.argtypes = [P, P, P, P, P, I64, I64, I32, I32, P, P, P, P, SZ, P]
+    lib.gs_layer_norm_bwd.restype = I32
+    lib.gs_expert_plan_workspace_bytes.argtypes, lib.gs_expert_plan_workspace_bytes.restype = [I64, I64, I32], SZ
+    lib.gs_expert_plan.argtypes, lib.gs_expert_plan.restype = [P, I64, I64, I32, P, P, P, P, SZ, P], I32
+    lib.gs_expert_dispatch.argtypes = [P, P, P, I64, I64, I32, I64, I32, P, P]
+    lib.gs_expert_dispatch.restype = I32
+    lib.gs_expert_combine.argtypes, lib.gs_expert_combine.restype = [P, P, P, I64, I64, I64, I32, P, P], I32
+    lib.gs_expert_combine_bwd.argtypes = [P, P, P, P, P, I64, I64, I32, I64, I32, P, P, P]
+    lib.gs_expert_combine_bwd.restype = I32
+    lib.gs_orthogonalize_workspace_bytes.argtypes, lib.gs_orthogonalize_workspace_bytes.restype = [I64, I64, I64], SZ
+    lib.gs_orthogonalize.argtypes = [P, I64, I64, I64, I32, F, F, F, F, I32, P, P, SZ, P]
+    lib.gs_orthogonalize.restype = I32
     _lib = lib
     return lib
 
@@ -558,4 +577,237 @@ def gs_project_fwd(means, covars, viewmats, Ks, width, height, eps2d=0.3, near_p
                               float(eps2d), float(near_plane), float(far_plane), float(radius_clip),
                               int(bool(orthographic)), _ptr(out.radii), _ptr(out.means2d), _ptr(out.depths),
                               _ptr(out.conics), _ptr(out.compensations), _stream(stream)))
+    return out
+
+
+# ----------------------------------------------------------------------------------------------------------------
+# Training operators of a layer of experts
+
+
+def _element(t, name):
+    """The gs_dtype code of a tensor of one of the three element types."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
+    return code
+
+
+def _norm_inputs(x, weight):
+    code, wcode = _element(x, "x"), _element(weight, "weight")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., dim]")
+    dim = x.shape[-1]
+    if dim < 1:
+        raise ValueError("x must have at least one column")
+    if wcode not in (code, 0):
+        raise TypeError(f"weight must be {x.dtype} or torch.float32 (got {weight.dtype})")
+    dev = x.device
+    _req(x, "x", x.dtype, dev)
+    _req(weight, "weight", weight.dtype, dev, (dim,))
+    return code, wcode, dev, x.numel() // dim, dim
+
+
+@dataclass
+class LayerNorm:
+    y: torch.Tensor  # x's shape and type
+    mean: torch.Tensor | None  # [...] float32
+    rstd: torch.Tensor | None  # [...] float32
+
+
+@_stream_scoped
+def gs_layer_norm_fwd(x, weight, bias=None, eps=1e-5, stats=True, out=None, stream=None) -> LayerNorm:
+    """Layer norm over the last axis: y = (x - mean) * rstd * weight + bias with the rows' mean and rstd = 1 /
+    sqrt(variance + eps) in float32 (stats=False: not returned).
+
+    x [..., dim] of float32, bfloat16 or float16; weight and bias [dim] of x's type or float32."""
+    lib = load_library()
+    code, wcode, dev, rows, dim = _norm_inputs(x, weight)
+    if bias is not None:
+        _req(bias, "bias", weight.dtype, dev, (dim,))
+    if out is None:
+        shape = x.shape[:-1]
+        out = LayerNorm(torch.empty_like(x),
+                        torch.empty(shape, dtype=torch.float32, device=dev) if stats else None,
+                        torch.empty(shape, dtype=torch.float32, device=dev) if stats else None)
+    else:
+        _req(out.y, "y", x.dtype, dev, x.shape)
+        if (out.mean is None) != (out.rstd is None):
+            raise ValueError("mean and rstd go together")
+        if out.mean is not None:
+            _req(out.mean, "mean", torch.float32, dev, x.shape[:-1])
+            _req(out.rstd, "rstd", torch.float32, dev, x.shape[:-1])
+    _check(lib.gs_layer_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), rows, dim, float(eps), code, wcode, _ptr(out.y),
+                                 _ptr(out.mean), _ptr(out.rstd), _stream(stream)))
+    return out
+
+
+@dataclass
+class LayerNormGrad:
+    x: torch.Tensor  # x's shape and type
+    weight: torch.Tensor  # [dim] of the weight's type
+    bias: torch.Tensor | None  # [dim] of the weight's type
+
+
+@_stream_scoped
+def gs_layer_norm_bwd(x, weight, mean, rstd, grad_y, grad_bias=True, out=None, stream=None,
+                      workspace=None) -> LayerNormGrad:
+    """Gradients of sum(grad_y * y) of gs_layer_norm_fwd, from its inputs and statistics (grad_bias=False: the bias's
+    is not computed)."""
+    lib = load_library()
+    code, wcode, dev, rows, dim = _norm_inputs(x, weight)
+    _req(mean, "mean", torch.float32, dev, x.shape[:-1])
+    _req(rstd, "rstd", torch.float32, dev, x.shape[:-1])
+    _req(grad_y, "grad_y", x.dtype, dev, x.shape)
+    if out is None:
+        out = LayerNormGrad(torch.empty_like(x), torch.empty_like(weight),
+                            torch.empty_like(weight) if grad_bias else None)
+    else:
+        _req(out.x, "grad_x", x.dtype, dev, x.shape)
+        _req(out.weight, "grad_weight", weight.dtype, dev, (dim,))
+        if out.bias is not None:
+            _req(out.bias, "grad_bias", weight.dtype, dev, (dim,))
+    ws = workspace if workspace is not None else _workspace(lib.gs_layer_norm_bwd_workspace_bytes(rows, dim), dev)
+    _check(lib.gs_layer_norm_bwd(_ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(grad_y), rows, dim, code, wcode,
+                                 _ptr(out.x), _ptr(out.weight), _ptr(out.bias), _ptr(ws), ws.numel(),
+                                 _stream(stream)))
+    return out
+
+
+@dataclass
+class ExpertPlan:
+    offsets: torch.Tensor  # [experts + 1] int32: expert e has rows [offsets[e], offsets[e + 1])
+    rows: torch.Tensor  # [tokens, choices] int32: each pair's row, -1 if dropped
+    pairs: torch.Tensor  # [tokens * choices] int32: each row's pair, -1 past the kept ones
+
+
+def _plan_sizes(plan, dev):
+    _req(plan.offsets, "offsets", torch.int32, dev)
+    _req(plan.rows, "rows", torch.int32, dev)
+    if plan.rows.dim() != 2 or plan.rows.shape[1] < 1:
+        raise ValueError("rows must be [tokens, choices]")
+    if plan.offsets.dim() != 1 or plan.offsets.shape[0] < 2:
+        raise ValueError("offsets must be [experts + 1]")
+    return plan.rows.shape[0], plan.rows.shape[1], plan.offsets.shape[0] - 1
+
+
+@_stream_scoped
+def gs_expert_plan(ids, experts, out=None, stream=None, workspace=None) -> ExpertPlan:
+    """The (token, choice) pairs of ids [tokens, choices] int32 in stable order of their expert; an id outside
+    [0, experts) drops its pair."""
+    lib = load_library()
+    _req(ids, "ids", torch.int32)
+    if ids.dim() != 2 or ids.shape[1] < 1:
+        raise ValueError("ids must be [tokens, choices]")
+    dev = ids.device
+    T, K, E = ids.shape[0], ids.shape[1], int(experts)
+    if E < 1:
+        raise ValueError("experts must be >= 1")
+    if out is None:
+        out = ExpertPlan(torch.empty(E + 1, dtype=torch.int32, device=dev), torch.empty_like(ids),
+                         torch.empty(T * K, dtype=torch.int32, device=dev))
+    else:
+        _req(out.offsets, "offsets", torch.int32, dev, (E + 1,))
+        _req(out.rows, "rows", torch.int32, dev, (T, K))
+        _req(out.pairs, "pairs", torch.int32, dev, (T * K,))
+    ws = workspace if workspace is not None else _workspace(lib.gs_expert_plan_workspace_bytes(T, K, E), dev)
+    _check(lib.gs_expert_plan(_ptr(ids), T, K, E, _ptr(out.offsets), _ptr(out.rows), _ptr(out.pairs), _ptr(ws),
+                              ws.numel(), _stream(stream)))
+    return out
+
+
+@_stream_scoped
+def gs_expert_dispatch(x, plan, out=None, stream=None):
+    """Each token's row of x [tokens, dim] copied to its pairs' rows: [tokens * choices, dim], zeros in the rows past
+    the kept ones. The gradient of x is gs_expert_combine(gradient of the result, plan)."""
+    lib = load_library()
+    code, dev = _element(x, "x"), x.device
+    T, K, E = _plan_sizes(plan, dev)
+    if x.dim() != 2 or x.shape[0] != T or x.shape[1] < 1:
+        raise ValueError(f"x must be [{T}, dim] (got {tuple(x.shape)})")
+    _req(x, "x", x.dtype, dev)
+    D = x.shape[1]
+    if out is None:
+        out = torch.empty((T * K, D), dtype=x.dtype, device=dev)
+    else:
+        _req(out, "sent", x.dtype, dev, (T * K, D))
+    _check(lib.gs_expert_dispatch(_ptr(x), _ptr(plan.offsets), _ptr(plan.rows), T, K, E, D, code, _ptr(out),
+                                  _stream(stream)))
+    return out
+
+
+def _sorted_rows(t, name, T, K):
+    if t.dim() != 2 or t.shape[0] != T * K or t.shape[1] < 1:
+        raise ValueError(f"{name} must be [{T * K}, dim] (got {tuple(t.shape)})")
+    return t.shape[1]
+
+
+@_stream_scoped
+def gs_expert_combine(source, plan, weights=None, out=None, stream=None):
+    """Each token's sum of weights [tokens, choices] (float32; None: ones) times its kept pairs' rows of source
+    [tokens * choices, dim]: [tokens, dim], summed in float32."""
+    lib = load_library()
+    code, dev = _element(source, "source"), source.device
+    T, K, _ = _plan_sizes(plan, dev)
+    D = _sorted_rows(source, "source", T, K)
+    _req(source, "source", source.dtype, dev)
+    if weights is not None:
+        _req(weights, "weights", torch.float32, dev, (T, K))
+    if out is None:
+        out = torch.empty((T, D), dtype=source.dtype, device=dev)
+    else:
+        _req(out, "y", source.dtype, dev, (T, D))
+    _check(lib.gs_expert_combine(_ptr(source), _ptr(plan.rows), _ptr(weights), T, K, D, code, _ptr(out),
+                                 _stream(stream)))
+    return out
+
+
+@dataclass
+class ExpertCombineGrad:
+    rows: torch.Tensor  # [tokens * choices, dim], source's type
+    weights: torch.Tensor  # [tokens, choices] float32
+
+
+@_stream_scoped
+def gs_expert_combine_bwd(source, plan, weights, grad_y, out=None, stream=None) -> ExpertCombineGrad:
+    """Gradients of sum(grad_y * gs_expert_combine(source, plan, weights)) for source (zeros in the rows past the
+    kept ones) and weights (0 for a dropped pair)."""
+    lib = load_library()
+    code, dev = _element(source, "source"), source.device
+    T, K, E = _plan_sizes(plan, dev)
+    D = _sorted_rows(source, "source", T, K)
+    _req(source, "source", source.dtype, dev)
+    _req(weights, "weights", torch.float32, dev, (T, K))
+    _req(grad_y, "grad_y", source.dtype, dev, (T, D))
+    if out is None:
+        out = ExpertCombineGrad(torch.empty_like(source), torch.empty_like(weights))
+    else:
+        _req(out.rows, "grad_rows", source.dtype, dev, (T * K, D))
+        _req(out.weights, "grad_weights", torch.float32, dev, (T, K))
+    _check(lib.gs_expert_combine_bwd(_ptr(source), _ptr(plan.offsets), _ptr(plan.rows), _ptr(weights), _ptr(grad_y),
+                                     T, K, E, D, code, _ptr(out.rows), _ptr(out.weights), _stream(stream)))
+    return out
+
+
+@_stream_scoped
+def gs_orthogonalize(update, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, out=None, stream=None,
+                     workspace=None):
+    """The orthogonalised update of each matrix of update [m, n] or [batch, m, n]: X = update / (|update| + eps), then
+    `steps` times X = a X + (b A + c A A) X with A = X X^T and (a, b, c) = coefficients. out may be update."""
+    lib = load_library()
+    code, dev = _element(update, "update"), update.device
+    if update.dim() not in (2, 3) or update.shape[-1] < 1 or update.shape[-2] < 1:
+        raise ValueError(f"update must be [m, n] or [batch, m, n] (got {tuple(update.shape)})")
+    _req(update, "update", update.dtype, dev)
+    m, n = update.shape[-2], update.shape[-1]
+    B = update.shape[0] if update.dim() == 3 else 1
+    a, b, c = (float(v) for v in coefficients)
+    if out is None:
+        out = torch.empty_like(update)
+    else:
+        _req(out, "out", update.dtype, dev, update.shape)
+    ws = workspace if workspace is not None else _workspace(lib.gs_orthogonalize_workspace_bytes(B, m, n), dev)
+    _check(lib.gs_orthogonalize(_ptr(update), B, m, n, int(steps), a, b, c, float(eps), code, _ptr(out), _ptr(ws),
+                                ws.numel(), _stream(stream)))
     return out

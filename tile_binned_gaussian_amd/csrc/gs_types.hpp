@@ -1,0 +1,69 @@
+// Element types of the training operators (layer norm, experts, orthogonalised updates): 16-byte loads and stores
+// of rows that start at any element, and conversions to and from float32.
+#pragma once
+
+#include "gs_internal.hpp"
+
+namespace gs {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Pack {
+    static constexpr int kN = 16 / sizeof(T);  // elements of one 16-byte load
+    typedef T V __attribute__((ext_vector_type(kN)));
+    // Rows of an odd width start at any multiple of the element's size, and gfx950's vector memory takes a
+    // 16-byte access at any address, so one path serves every alignment.
+    typedef V VU __attribute__((aligned(sizeof(T))));
+};
+
+// Columns [col, col + kN) of a row of `dim` elements, those past the end 0.
+template <typename T>
+__device__ __forceinline__ typename Pack<T>::V load_pack(const T *__restrict__ row, int64_t col, int64_t dim) {
+    if (col + Pack<T>::kN <= dim) return *reinterpret_cast<const typename Pack<T>::VU *>(row + col);
+    typename Pack<T>::V v;
+#pragma unroll
+    for (int j = 0; j < Pack<T>::kN; ++j) v[j] = col + j < dim ? row[col + j] : static_cast<T>(0.0f);
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_pack(T *__restrict__ row, int64_t col, int64_t dim, typename Pack<T>::V v) {
+    if (col + Pack<T>::kN <= dim) {
+        *reinterpret_cast<typename Pack<T>::VU *>(row + col) = v;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < Pack<T>::kN; ++j)
+        if (col + j < dim) row[col + j] = v[j];
+}
+
+// N consecutive float32 values of an array of T at col (0 past the end), N a multiple or divisor of Pack<T>::kN.
+template <int N, typename T>
+__device__ __forceinline__ void load_floats(const T *__restrict__ row, int64_t col, int64_t dim, float *out) {
+    constexpr int P = Pack<T>::kN;
+    if constexpr (N >= P) {
+#pragma unroll
+        for (int i = 0; i < N / P; ++i) {
+            const typename Pack<T>::V v = load_pack(row, col + i * P, dim);
+#pragma unroll
+            for (int j = 0; j < P; ++j) out[i * P + j] = static_cast<float>(v[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) out[j] = col + j < dim ? static_cast<float>(row[col + j]) : 0.0f;
+    }
+}
+
+// Sum over the lanes of a group of G consecutive lanes (G a power of two up to 64), in every lane.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int d = G / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, kWave);
+    return v;
+}
+
+inline bool known_dtype(int dtype) { return dtype == GS_F32 || dtype == GS_BF16 || dtype == GS_F16; }
+inline size_t dtype_size(int dtype) { return dtype == GS_F32 ? 4 : 2; }
+
+}  // namespace gs

@@ -1,0 +1,447 @@
+// Layer norm over the last axis and its backward on gfx950.
+//
+// A group of G lanes holds one row in registers (V packs of 16 bytes a lane), so the mean, the centred sum of squares
+// and the output come from one read of the row; the two passes over registers keep the variance exact for rows far
+// from zero. The backward forms both row sums from one read of x and grad_y, and every lane keeps the column sums of
+// its columns (weight and bias gradient) over all rows that its workgroup visits; the workgroups' sums go to a
+// workspace and a second kernel adds them in a fixed order. Wider rows than the registers hold take the kernels that
+// read the row again from L2.
+#include "gs_types.hpp"
+
+namespace gs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kFwdBlocks = 2048;    // 8 workgroups a CU; each visits several rows with its weights in registers
+constexpr int kBwdBlocks = 512;     // 2 a CU: each adds one row of column sums to the workspace
+constexpr int kReduceThreads = 1024;
+
+// Sum over the G lanes that share a row; slot: LDS words of this sum alone when G spans waves. A row's two sums take
+// different slots, so one barrier between writing and reading a slot is enough.
+template <int G>
+__device__ __forceinline__ float row_sum(float v, float *slot) {
+    if constexpr (G <= kWave) {
+        return group_sum<G>(v);
+    } else {
+        v = group_sum<kWave>(v);
+        if (threadIdx.x % kWave == 0) slot[threadIdx.x / kWave] = v;
+        __syncthreads();
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < G / kWave; ++i) s += slot[i];
+        return s;
+    }
+}
+
+template <typename T, typename W, int G, int V>
+__global__ __launch_bounds__(kThreads) void norm_fwd_kernel(const T *__restrict__ x, const W *__restrict__ weight,
+                                                            const W *__restrict__ bias, int64_t rows, int64_t dim,
+                                                            float eps, T *__restrict__ y, float *__restrict__ mean,
+                                                            float *__restrict__ rstd) {
+    constexpr int N = Pack<T>::kN, kRows = kThreads / G;
+    __shared__ float s_sum[2][kThreads / kWave];
+    const int lane = threadIdx.x % G;
+    const float n = static_cast<float>(dim);
+    float w[V * N], b[V * N];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int64_t col = (static_cast<int64_t>(v) * G + lane) * N;
+        load_floats<N>(weight, col, dim, w + v * N);
+#pragma unroll
+        for (int j = 0; j < N; ++j) b[v * N + j] = 0.0f;
+        if (bias) load_floats<N>(bias, col, dim, b + v * N);
+    }
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G; r < rows;
+         r += static_cast<int64_t>(gridDim.x) * kRows) {
+        float c[V * N];
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            load_floats<N>(x + r * dim, (static_cast<int64_t>(v) * G + lane) * N, dim, c + v * N);
+#pragma unroll
+            for (int j = 0; j < N; ++j) s += c[v * N + j];
+        }
+        const float m = row_sum<G>(s, s_sum[0]) / n;
+        float q = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                float &e = c[v * N + j];
+                e = (static_cast<int64_t>(v) * G + lane) * N + j < dim ? e - m : 0.0f;
+                q = __builtin_fmaf(e, e, q);
+            }
+        const float rs = 1.0f / sqrtf(row_sum<G>(q, s_sum[1]) / n + eps);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            typename Pack<T>::V o;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                o[j] = static_cast<T>(__builtin_fmaf(c[v * N + j] * rs, w[v * N + j], b[v * N + j]));
+            store_pack(y + r * dim, (static_cast<int64_t>(v) * G + lane) * N, dim, o);
+        }
+        if (mean && lane == 0) {
+            mean[r] = m;
+            rstd[r] = rs;
+        }
+    }
+}
+
+// Rows wider than the registers hold: one workgroup a row, three reads (the last two from L2).
+template <typename T, typename W>
+__global__ __launch_bounds__(kThreads) void norm_fwd_wide_kernel(const T *__restrict__ x, const W *__restrict__ weight,
+                                                                 const W *__restrict__ bias, int64_t rows, int64_t dim,
+                                                                 float eps, T *__restrict__ y,
+                                                                 float *__restrict__ mean, float *__restrict__ rstd) {
+    constexpr int N = Pack<T>::kN;
+    __shared__ float s_sum[2][kThreads / kWave];
+    const float n = static_cast<float>(dim);
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const T *row = x + r * dim;
+        float s = 0.0f;
+        for (int64_t col = threadIdx.x * N; col < dim; col += kThreads * N) {
+            float c[N];
+            load_floats<N>(row, col, dim, c);
+#pragma unroll
+            for (int j = 0; j < N; ++j) s += c[j];
+        }
+        const float m = row_sum<kThreads>(s, s_sum[0]) / n;
+        float q = 0.0f;
+        for (int64_t col = threadIdx.x * N; col < dim; col += kThreads * N) {
+            float c[N];
+            load_floats<N>(row, col, dim, c);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float e = col + j < dim ? c[j] - m : 0.0f;
+                q = __builtin_fmaf(e, e, q);
+            }
+        }
+        const float rs = 1.0f / sqrtf(row_sum<kThreads>(q, s_sum[1]) / n + eps);
+        for (int64_t col = threadIdx.x * N; col < dim; col += kThreads * N) {
+            float c[N], w[N], b[N] = {};
+            load_floats<N>(row, col, dim, c);
+            load_floats<N>(weight, col, dim, w);
+            if (bias) load_floats<N>(bias, col, dim, b);
+            typename Pack<T>::V o;
+#pragma unroll
+            for (int j = 0; j < N; ++j) o[j] = static_cast<T>(__builtin_fmaf((c[j] - m) * rs, w[j], b[j]));
+            store_pack(y + r * dim, col, dim, o);
+        }
+        if (mean && threadIdx.x == 0) {
+            mean[r] = m;
+            rstd[r] = rs;
+        }
+    }
+}
+
+template <typename T, typename W, int G, int V>
+__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(const T *__restrict__ x, const W *__restrict__ weight,
+                                                            const float *__restrict__ mean,
+                                                            const float *__restrict__ rstd,
+                                                            const T *__restrict__ grad_y, int64_t rows, int64_t dim,
+                                                            T *__restrict__ grad_x, float *__restrict__ partial) {
+    constexpr int N = Pack<T>::kN, kRows = kThreads / G;
+    __shared__ float s_sum[2][2][kThreads / kWave];
+    __shared__ float s_cols[kRows > 1 ? kThreads * (N + 1) : 1];
+    const int lane = threadIdx.x % G, group = threadIdx.x / G;
+    const float n = static_cast<float>(dim);
+    float w[V * N], dw[V * N], db[V * N];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        load_floats<N>(weight, (static_cast<int64_t>(v) * G + lane) * N, dim, w + v * N);
+#pragma unroll
+        for (int j = 0; j < N; ++j) dw[v * N + j] = db[v * N + j] = 0.0f;
+    }
+    int turn = 0;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + group; r < rows;
+         r += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
+        const float m = mean[r], rs = rstd[r];
+        float xh[V * N], g[V * N];
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int64_t col = (static_cast<int64_t>(v) * G + lane) * N;
+            load_floats<N>(x + r * dim, col, dim, xh + v * N);
+            load_floats<N>(grad_y + r * dim, col, dim, g + v * N);
+#pragma unroll
+            for (int j = v * N; j < v * N + N; ++j) {
+                xh[j] = (xh[j] - m) * rs;
+                dw[j] = __builtin_fmaf(g[j], xh[j], dw[j]);
+                db[j] += g[j];
+                g[j] *= w[j];  // zero past the row's end, as weight and grad_y are
+                s1 += g[j];
+                s2 = __builtin_fmaf(g[j], xh[j], s2);
+            }
+        }
+        s1 = row_sum<G>(s1, s_sum[turn][0]) / n;
+        s2 = row_sum<G>(s2, s_sum[turn][1]) / n;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            typename Pack<T>::V o;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                o[j] = static_cast<T>(rs * (g[v * N + j] - s1 - xh[v * N + j] * s2));
+            store_pack(grad_x + r * dim, (static_cast<int64_t>(v) * G + lane) * N, dim, o);
+        }
+    }
+    // the workgroup's column sums: its groups' added in order
+    float *out = partial + static_cast<int64_t>(blockIdx.x) * 2 * dim;
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float *acc = (which ? db : dw) + v * N;
+            if constexpr (kRows > 1) {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < N; ++j) s_cols[threadIdx.x * (N + 1) + j] = acc[j];
+                __syncthreads();
+                if (group == 0)
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        for (int k = 1; k < kRows; ++k) acc[j] += s_cols[(k * G + lane) * (N + 1) + j];
+            }
+            if (group == 0) {
+                const int64_t col = (static_cast<int64_t>(v) * G + lane) * N;
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (col + j < dim) out[which * dim + col + j] = acc[j];
+            }
+        }
+}
+
+// Rows wider than the registers hold: grad_x by one workgroup a row (two reads), and the column sums by a thread a
+// column over the rows of one slice (a third).
+template <typename T, typename W>
+__global__ __launch_bounds__(kThreads) void norm_bwd_wide_kernel(const T *__restrict__ x, const W *__restrict__ weight,
+                                                                 const float *__restrict__ mean,
+                                                                 const float *__restrict__ rstd,
+                                                                 const T *__restrict__ grad_y, int64_t rows,
+                                                                 int64_t dim, T *__restrict__ grad_x) {
+    constexpr int N = Pack<T>::kN;
+    __shared__ float s_sum[2][2][kThreads / kWave];
+    const float n = static_cast<float>(dim);
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
+        const float m = mean[r], rs = rstd[r];
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int pass = 0; pass < 2; ++pass) {
+            for (int64_t col = threadIdx.x * N; col < dim; col += kThreads * N) {
+                float xh[N], g[N], w[N];
+                load_floats<N>(x + r * dim, col, dim, xh);
+                load_floats<N>(grad_y + r * dim, col, dim, g);
+                load_floats<N>(weight, col, dim, w);
+                typename Pack<T>::V o;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    xh[j] = (xh[j] - m) * rs;
+                    g[j] *= w[j];
+                    if (pass == 0) {
+                        s1 += g[j];
+                        s2 = __builtin_fmaf(g[j], xh[j], s2);
+                    } else {
+                        o[j] = static_cast<T>(rs * (g[j] - s1 - xh[j] * s2));
+                    }
+                }
+                if (pass) store_pack(grad_x + r * dim, col, dim, o);
+            }
+            if (pass == 0) {
+                s1 = row_sum<kThreads>(s1, s_sum[turn][0]) / n;
+                s2 = row_sum<kThreads>(s2, s_sum[turn][1]) / n;
+            }
+        }
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_columns_kernel(const T *__restrict__ x, const float *__restrict__ mean,
+                                                                const float *__restrict__ rstd,
+                                                                const T *__restrict__ grad_y, int64_t rows,
+                                                                int64_t dim, float *__restrict__ partial) {
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (col >= dim) return;
+    float dw = 0.0f, db = 0.0f;
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+        const float g = static_cast<float>(grad_y[r * dim + col]);
+        dw = __builtin_fmaf(g, (static_cast<float>(x[r * dim + col]) - mean[r]) * rstd[r], dw);
+        db += g;
+    }
+    float *out = partial + static_cast<int64_t>(blockIdx.y) * 2 * dim;
+    out[col] = dw;
+    out[dim + col] = db;
+}
+
+// grad_weight (y = 0) and grad_bias (y = 1): 64 columns a workgroup, its 16 waves take the partial sums in turn.
+template <typename W>
+__global__ __launch_bounds__(kReduceThreads) void norm_reduce_kernel(const float *__restrict__ partial, int parts,
+                                                                     int64_t dim, W *__restrict__ grad_weight,
+                                                                     W *__restrict__ grad_bias) {
+    constexpr int kWaves = kReduceThreads / kWave;
+    __shared__ float s_part[kWaves][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * kWave + lane;
+    float s = 0.0f;
+    if (col < dim) {
+        const float *p = partial + blockIdx.y * dim + col;
+#pragma unroll 8
+        for (int i = wave; i < parts; i += kWaves) s += p[static_cast<int64_t>(i) * 2 * dim];
+    }
+    s_part[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && col < dim) {
+        for (int i = 1; i < kWaves; ++i) s += s_part[i][lane];
+        (blockIdx.y ? grad_bias : grad_weight)[col] = static_cast<W>(s);
+    }
+}
+
+// How a row is held: the lanes that share it and the packs of a lane; wide: more than 256 lanes' 4 packs.
+struct RowShape {
+    int lanes, packs;
+};
+
+inline RowShape row_shape(int64_t dim, int pack) {
+    const int64_t packs = (dim + pack - 1) / pack;
+    if (packs <= 16) return {16, 1};
+    if (packs <= 64) return {64, 1};
+    if (packs <= 128) return {64, 2};
+    if (packs <= 256) return {256, 1};
+    if (packs <= 512) return {256, 2};
+    if (packs <= 1024) return {256, 4};
+    return {0, 0};
+}
+
+int64_t bwd_blocks(int64_t rows) { return rows < kBwdBlocks ? rows : kBwdBlocks; }
+
+template <typename T, typename W>
+gs_status run_fwd(const void *x, const void *weight, const void *bias, int64_t rows, int64_t dim, float eps, void *y,
+                  float *mean, float *rstd, hipStream_t stream) {
+    const RowShape shape = row_shape(dim, Pack<T>::kN);
+#define GS_NORM_FWD(G, V)                                                                                             \
+    if (shape.lanes == G && shape.packs == V) {                                                                       \
+        const int64_t blocks = (rows + kThreads / G - 1) / (kThreads / G);                                            \
+        hipLaunchKernelGGL((norm_fwd_kernel<T, W, G, V>),                                                             \
+                           dim3(static_cast<unsigned>(blocks < kFwdBlocks ? blocks : kFwdBlocks)), dim3(kThreads), 0, \
+                           stream, static_cast<const T *>(x), static_cast<const W *>(weight),                         \
+                           static_cast<const W *>(bias), rows, dim, eps, static_cast<T *>(y), mean, rstd);            \
+        GS_LAUNCH_TRY("norm_fwd_kernel");                                                                             \
+        return ok();                                                                                                  \
+    }
+    GS_NORM_FWD(16, 1)
+    GS_NORM_FWD(64, 1)
+    GS_NORM_FWD(64, 2)
+    GS_NORM_FWD(256, 1)
+    GS_NORM_FWD(256, 2)
+    GS_NORM_FWD(256, 4)
+#undef GS_NORM_FWD
+    hipLaunchKernelGGL((norm_fwd_wide_kernel<T, W>),
+                       dim3(static_cast<unsigned>(rows < kFwdBlocks ? rows : kFwdBlocks)), dim3(kThreads), 0, stream,
+                       static_cast<const T *>(x), static_cast<const W *>(weight), static_cast<const W *>(bias), rows,
+                       dim, eps, static_cast<T *>(y), mean, rstd);
+    GS_LAUNCH_TRY("norm_fwd_wide_kernel");
+    return ok();
+}
+
+template <typename T, typename W>
+gs_status run_bwd(const void *x, const void *weight, const float *mean, const float *rstd, const void *grad_y,
+                  int64_t rows, int64_t dim, void *grad_x, void *grad_weight, void *grad_bias, float *partial,
+                  hipStream_t stream) {
+    const RowShape shape = row_shape(dim, Pack<T>::kN);
+    const T *tx = static_cast<const T *>(x), *tg = static_cast<const T *>(grad_y);
+    const W *tw = static_cast<const W *>(weight);
+    T *to = static_cast<T *>(grad_x);
+    int64_t parts = bwd_blocks(rows);
+#define GS_NORM_BWD(G, V)                                                                                          \
+    if (shape.lanes == G && shape.packs == V) {                                                                    \
+        parts = (rows + kThreads / G - 1) / (kThreads / G);                                                        \
+        if (parts > kBwdBlocks) parts = kBwdBlocks;                                                                \
+        if (rows > 0)                                                                                              \
+            hipLaunchKernelGGL((norm_bwd_kernel<T, W, G, V>), dim3(static_cast<unsigned>(parts)), dim3(kThreads),  \
+                               0, stream, tx, tw, mean, rstd, tg, rows, dim, to, partial);                         \
+    }
+    GS_NORM_BWD(16, 1)
+    GS_NORM_BWD(64, 1)
+    GS_NORM_BWD(64, 2)
+    GS_NORM_BWD(256, 1)
+    GS_NORM_BWD(256, 2)
+    GS_NORM_BWD(256, 4)
+#undef GS_NORM_BWD
+    GS_LAUNCH_TRY("norm_bwd_kernel");
+    if (shape.lanes == 0 && rows > 0) {
+        hipLaunchKernelGGL((norm_bwd_wide_kernel<T, W>),
+                           dim3(static_cast<unsigned>(rows < kFwdBlocks ? rows : kFwdBlocks)), dim3(kThreads), 0,
+                           stream, tx, tw, mean, rstd, tg, rows, dim, to);
+        GS_LAUNCH_TRY("norm_bwd_wide_kernel");
+        if (parts > 64) parts = 64;
+        hipLaunchKernelGGL((norm_columns_kernel<T>),
+                           dim3(static_cast<unsigned>((dim + kThreads - 1) / kThreads), static_cast<unsigned>(parts)),
+                           dim3(kThreads), 0, stream, tx, mean, rstd, tg, rows, dim, partial);
+        GS_LAUNCH_TRY("norm_columns_kernel");
+    }
+    hipLaunchKernelGGL((norm_reduce_kernel<W>),
+                       dim3(static_cast<unsigned>((dim + kWave - 1) / kWave), grad_bias ? 2u : 1u),
+                       dim3(kReduceThreads), 0, stream, partial, static_cast<int>(parts), dim,
+                       static_cast<W *>(grad_weight), static_cast<W *>(grad_bias));
+    GS_LAUNCH_TRY("norm_reduce_kernel");
+    return ok();
+}
+
+constexpr int64_t kLimit = int64_t(1) << 31;
+
+gs_status check_norm(const char *name, int64_t rows, int64_t dim, int dtype, int weight_dtype) {
+    if (rows < 0 || rows >= kLimit) return fail(GS_ERR_INVALID_ARG, "%s: need 0 <= rows < 2^31", name);
+    if (dim < 1 || dim >= kLimit) return fail(GS_ERR_INVALID_ARG, "%s: need 1 <= dim < 2^31", name);
+    if (!known_dtype(dtype)) return fail(GS_ERR_INVALID_ARG, "%s: dtype = %d is no gs_dtype", name, dtype);
+    if (weight_dtype != dtype && weight_dtype != GS_F32)
+        return fail(GS_ERR_INVALID_ARG, "%s: weight_dtype = %d is neither dtype nor GS_F32", name, weight_dtype);
+    return GS_OK;
+}
+
+}  // namespace
+}  // namespace gs
+
+using namespace gs;
+
+// One call of fn<element type, weight type>(...) for the two type codes.
+#define GS_NORM_TYPES(fn, ...)                                                                          \
+    do {                                                                                                \
+        if (dtype == GS_F32) return fn<float, float>(__VA_ARGS__);                                      \
+        if (dtype == GS_BF16)                                                                           \
+            return weight_dtype == GS_F32 ? fn<__bf16, float>(__VA_ARGS__) : fn<__bf16, __bf16>(__VA_ARGS__); \
+        return weight_dtype == GS_F32 ? fn<_Float16, float>(__VA_ARGS__) : fn<_Float16, _Float16>(__VA_ARGS__); \
+    } while (0)
+
+extern "C" gs_status gs_layer_norm_fwd(const void *x, const void *weight, const void *bias, int64_t rows, int64_t dim,
+                                       float eps, int dtype, int weight_dtype, void *y, float *mean, float *rstd,
+                                       void *stream_handle) {
+    const gs_status bad = check_norm("gs_layer_norm_fwd", rows, dim, dtype, weight_dtype);
+    if (bad != GS_OK) return bad;
+    if (!(eps >= 0.0f)) return fail(GS_ERR_INVALID_ARG, "gs_layer_norm_fwd: eps must be >= 0");
+    if ((mean == nullptr) != (rstd == nullptr))
+        return fail(GS_ERR_INVALID_ARG, "gs_layer_norm_fwd: mean and rstd go together");
+    if (rows == 0) return ok();
+    if (!x || !weight || !y) return fail(GS_ERR_INVALID_ARG, "gs_layer_norm_fwd: a required pointer is NULL");
+    hipStream_t stream = static_cast<hipStream_t>(stream_handle);
+    GS_NORM_TYPES(run_fwd, x, weight, bias, rows, dim, eps, y, mean, rstd, stream);
+}
+
+extern "C" size_t gs_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
+    if (rows < 0 || rows >= kLimit || dim < 1 || dim >= kLimit) return 0;
+    return static_cast<size_t>(bwd_blocks(rows)) * 2 * static_cast<size_t>(dim) * sizeof(float);
+}
+
+extern "C" gs_status gs_layer_norm_bwd(const void *x, const void *weight, const float *mean, const float *rstd,
+                                       const void *grad_y, int64_t rows, int64_t dim, int dtype, int weight_dtype,
+                                       void *grad_x, void *grad_weight, void *grad_bias, void *workspace,
+                                       size_t workspace_bytes, void *stream_handle) {
+    const gs_status bad = check_norm("gs_layer_norm_bwd", rows, dim, dtype, weight_dtype);
+    if (bad != GS_OK) return bad;
+    if (!weight || !grad_weight || (rows > 0 && (!x || !mean || !rstd || !grad_y || !grad_x)))
+        return fail(GS_ERR_INVALID_ARG, "gs_layer_norm_bwd: a required pointer is NULL");
+    const size_t need = gs_layer_norm_bwd_workspace_bytes(rows, dim);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(GS_ERR_WORKSPACE, "gs_layer_norm_bwd: need %zu workspace bytes, got %zu", need,
+                    workspace ? workspace_bytes : 0);
+    hipStream_t stream = static_cast<hipStream_t>(stream_handle);
+    GS_NORM_TYPES(run_bwd, x, weight, mean, rstd, grad_y, rows, dim, grad_x, grad_weight, grad_bias,
+                  static_cast<float *>(workspace), stream);
+}
