@@ -5,45 +5,70 @@
 // high high + high low + low high, summed in float32. The term left out is 2^-22 of the product.
 // X holds values scaled by 2^12 and the Gram side by 2^10: entries of X are at most its largest singular value, and
 // the scale keeps the low parts of the smallest ones out of float16's subnormals.
+#include <type_traits>
+
 #include "gs_types.hpp"
 
 namespace gs {
 namespace {
 
 typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kScaleX = 4096.0f;
 constexpr float kScaleA = 1024.0f;
-constexpr int kTile = 64;  // output tile of a workgroup; planes are padded to it with zeros
-constexpr int kStep = 32;  // columns of both operands staged at a time
 constexpr int kThreads = 256;
 constexpr int kNormBlocks = 64;
+constexpr int kPanel = 32;   // rows of a panel; planes are padded to it with zeros both ways
+constexpr int kDepth = 16;   // columns of a block
+constexpr int kBlock = kPanel * kDepth;  // elements of a block: 1 KB
+constexpr int kStages = 4;
 
+// A plane holds a matrix [rows][depth] as blocks of 32 rows and 16 columns, [rows / 32][depth / 16][512], each in the
+// order in which a wave's lanes hold a matrix-core operand: lane l has row l % 32 and the eight columns from
+// l / 32 * 8 on. A block goes from memory to LDS and from LDS to registers as 1 KB in a row: no bank is hit twice,
+// whatever the tile.
 struct Planes {
     _Float16 *hi, *lo;
 };
 
-__device__ __forceinline__ void store_pair(const Planes &p, size_t i, float v) {
-    const _Float16 h = static_cast<_Float16>(v);
-    p.hi[i] = h;
-    p.lo[i] = static_cast<_Float16>(v - static_cast<float>(h));
+__device__ __forceinline__ size_t block_at(int panel, int block, int depth) {
+    return (static_cast<size_t>(panel) * (depth / kDepth) + block) * kBlock;
 }
-__device__ __forceinline__ float load_pair(const Planes &p, size_t i) {
-    return static_cast<float>(p.hi[i]) + static_cast<float>(p.lo[i]);
+
+// Element offset of the eight columns from col (a multiple of 8) on of a row.
+__device__ __forceinline__ size_t eight_at(int row, int col, int depth) {
+    return block_at(row / kPanel, col / kDepth, depth) + (col / 8 % 2 * kPanel + row % kPanel) * 8;
+}
+
+template <int N, typename H>
+__device__ __forceinline__ void split(const float *v, H &hi, H &lo) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        hi[j] = static_cast<_Float16>(v[j]);
+        lo[j] = static_cast<_Float16>(v[j] - static_cast<float>(hi[j]));
+    }
 }
 
 // Partial sums of squares of matrix blockIdx.y in float64.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_norm_kernel(const T *__restrict__ update, int64_t count,
                                                               double *__restrict__ partial) {
+    constexpr int N = Pack<T>::kN;
     __shared__ double s_part[kThreads];
     const T *u = update + blockIdx.y * count;
     double s = 0.0;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < count;
-         i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const double v = static_cast<double>(static_cast<float>(u[i]));
-        s = __builtin_fma(v, v, s);
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * N; i < count;
+         i += static_cast<int64_t>(gridDim.x) * kThreads * N) {
+        const typename Pack<T>::V v = load_pack(u, i, count);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const double d = static_cast<double>(static_cast<float>(v[j]));
+            s = __builtin_fma(d, d, s);
+        }
     }
     s_part[threadIdx.x] = s;
     __syncthreads();
@@ -54,13 +79,14 @@ __global__ __launch_bounds__(kThreads) void ortho_norm_kernel(const T *__restric
     if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = s_part[0];
 }
 
-// X = update / (norm + eps) in both orders: `direct` laid out as the update, `turned` transposed; 64 x 64 tiles,
-// zeros in the padding. direct [batch][pm][pn], turned [batch][pn][pm].
+// X = update / (norm + eps) in both orders: `direct` holds the update's rows, `turned` its columns; 64 x 64 elements
+// a workgroup, zeros in the padding.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restrict__ update,
                                                                const double *__restrict__ partial, int parts, int m,
                                                                int n, int pm, int pn, float eps, Planes direct,
                                                                Planes turned) {
+    constexpr int kTile = 64;
     __shared__ float s_tile[kTile][kTile + 1];
     __shared__ double s_scale;
     if (threadIdx.x == 0) {
@@ -70,7 +96,7 @@ __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restri
     }
     __syncthreads();
     const double scale = s_scale;
-    const size_t plane = static_cast<size_t>(pm) * pn;
+    const size_t plane = blockIdx.z * static_cast<size_t>(pm) * pn;
     const int r0 = blockIdx.y * kTile, c0 = blockIdx.x * kTile;
     const int tc = threadIdx.x % kTile;
     for (int tr = threadIdx.x / kTile; tr < kTile; tr += kThreads / kTile) {
@@ -81,88 +107,248 @@ __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restri
                 static_cast<double>(static_cast<float>(update[(static_cast<size_t>(blockIdx.z) * m + r) * n + c])) *
                 scale);
         s_tile[tr][tc] = v;
-        store_pair(direct, blockIdx.z * plane + static_cast<size_t>(r) * pn + c, v);
     }
     __syncthreads();
-    for (int tr = threadIdx.x / kTile; tr < kTile; tr += kThreads / kTile)
-        store_pair(turned, blockIdx.z * plane + static_cast<size_t>(c0 + tr) * pm + r0 + tc, s_tile[tc][tr]);
+    for (int i = threadIdx.x; i < kTile * kTile / 8; i += kThreads) {
+        const int row = i % kTile, col = i / kTile * 8;
+        float v[8];
+        h16x8 hi, lo;
+        if (r0 + row < pm && c0 + col < pn) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = s_tile[row][col + j];
+            split<8>(v, hi, lo);
+            const size_t at = plane + eight_at(r0 + row, c0 + col, pn);
+            *reinterpret_cast<h16x8 *>(direct.hi + at) = hi;
+            *reinterpret_cast<h16x8 *>(direct.lo + at) = lo;
+        }
+        if (c0 + row < pn && r0 + col < pm) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = s_tile[col + j][row];
+            split<8>(v, hi, lo);
+            const size_t at = plane + eight_at(c0 + row, r0 + col, pm);
+            *reinterpret_cast<h16x8 *>(turned.hi + at) = hi;
+            *reinterpret_cast<h16x8 *>(turned.lo + at) = lo;
+        }
+    }
 }
 
-enum Product {
-    kGram,        // out = P Q^T scaled: A from X
-    kPolynomial,  // out = b A + c (P Q^T): the step's matrix from A
-    kApply,       // out = a X + P Q^T, and out_t its transpose
-};
-
+// out = scale_acc P Q^T + scale_add add, P [rows][depth], Q [cols][depth].
 struct ProductArgs {
-    Planes p, q;     // [rows][depth], [cols][depth]
-    Planes add;      // [rows][cols]: what the epilogue adds
-    Planes out;      // [rows][cols]
-    Planes out_t;    // [cols][rows]
-    int rows, cols, depth;
+    Planes p, q;
+    Planes add;       // [cols][rows], as `turned`; hi NULL: nothing is added
+    Planes straight;  // [rows][cols]; lo NULL: only the high parts are written
+    Planes turned;    // [cols][rows]
+    int rows, cols, depth;  // multiples of 32
+    int tile_rows, tile_cols;
+    int symmetric;    // P = Q and the result is symmetric: tiles of the lower triangle, written to both sides
     float scale_acc, scale_add;
 };
 
-// One 64 x 64 tile of P Q^T a workgroup, a 32 x 32 quarter a wave.
-template <int KIND>
-__global__ __launch_bounds__(kThreads) void ortho_product_kernel(ProductArgs a) {
-    __shared__ _Float16 s_op[2][2][kTile][kStep + 8];  // [P, Q][hi, lo]
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    const size_t b = blockIdx.z;
-    const size_t p0 = (b * a.rows + blockIdx.y * kTile) * a.depth, q0 = (b * a.cols + blockIdx.x * kTile) * a.depth;
-    const int wr = (wave / 2) * 32, wc = (wave % 2) * 32;
-    f32x16 acc = {};
-    const int sr = threadIdx.x / 4, sc = threadIdx.x % 4 * 8;  // staging: 64 rows of 4 eights
-    for (int k0 = 0; k0 < a.depth; k0 += kStep) {
-        const size_t off = static_cast<size_t>(sr) * a.depth + k0 + sc;
-        const h16x8 v0 = *reinterpret_cast<const h16x8 *>(a.p.hi + p0 + off);
-        const h16x8 v1 = *reinterpret_cast<const h16x8 *>(a.p.lo + p0 + off);
-        const h16x8 v2 = *reinterpret_cast<const h16x8 *>(a.q.hi + q0 + off);
-        const h16x8 v3 = *reinterpret_cast<const h16x8 *>(a.q.lo + q0 + off);
-        __syncthreads();
-        *reinterpret_cast<h16x8 *>(&s_op[0][0][sr][sc]) = v0;
-        *reinterpret_cast<h16x8 *>(&s_op[0][1][sr][sc]) = v1;
-        *reinterpret_cast<h16x8 *>(&s_op[1][0][sr][sc]) = v2;
-        *reinterpret_cast<h16x8 *>(&s_op[1][1][sr][sc]) = v3;
-        __syncthreads();
+// One block from memory to LDS, 16 bytes a lane, without registers in between. lds: byte address, the same in the
+// whole wave. The load counts in vmcnt; only LDS is written, so no register waits for it.
+__device__ __forceinline__ void load_block(const _Float16 *src, uint32_t lane_bytes, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(lane_bytes), "s"(src)
+                 : "memory");
+}
+
+// Until at most OUTSTANDING of this wave's loads are under way and its reads of LDS are done, and until every wave of the
+// workgroup is here.
+template <int OUTSTANDING>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(OUTSTANDING) : "memory");
+}
+
+// 4 x 4 transpose of float16 within each quad of lanes: lane q gives its values for rows 0..3 and gets row q's values
+// of lanes 0..3.
+__device__ __forceinline__ h16x4 quad_transpose(h16x4 v) {
+    u32x2 p = __builtin_bit_cast(u32x2, v);
+    const int q = threadIdx.x % 4;
+    // with the neighbour: lane pairs exchange so that the even one has rows 0 and 2, the odd one rows 1 and 3
+    const uint32_t pick = q % 2 ? 0x07060302u : 0x01000504u;
+    p.x = __builtin_amdgcn_perm(p.x, __builtin_amdgcn_mov_dpp(p.x, 0xB1, 0xF, 0xF, true), pick);
+    p.y = __builtin_amdgcn_perm(p.y, __builtin_amdgcn_mov_dpp(p.y, 0xB1, 0xF, 0xF, true), pick);
+    // with the lane two on
+    const uint32_t give = q < 2 ? p.y : p.x;
+    const uint32_t got = __builtin_amdgcn_mov_dpp(give, 0x4E, 0xF, 0xF, true);
+    const u32x2 r = {q < 2 ? p.x : got, q < 2 ? got : p.y};
+    return __builtin_bit_cast(h16x4, r);
+}
+
+// A workgroup of four waves makes a T x T tile, each wave a quarter of it. PRODUCTS = 3: both halves of the operands
+// (high high + high low + low high); 1: the high halves alone. A stage of the LDS ring holds 32 columns of the high
+// halves, or 16 of both; while one is multiplied the next is there already (its first operands are read ahead of the
+// barrier) and two more are on their way.
+template <int T, int PRODUCTS>
+__global__ __launch_bounds__(kThreads, T <= 128 ? 2 : 1) void ortho_product_kernel(ProductArgs a) {
+    constexpr int F = T / 64;                   // 32 x 32 results of a wave, each way
+    constexpr int kPanels = T / kPanel;
+    constexpr int PL = PRODUCTS == 1 ? 1 : 2;   // planes staged
+    constexpr int S = PRODUCTS == 1 ? 2 : 1;    // blocks of 16 columns in a stage
+    constexpr int kBlocks = 2 * PL * kPanels * S;
+    constexpr int L = kBlocks / 4;              // blocks a wave loads for a stage
+    constexpr uint32_t kStageBytes = kBlocks * kBlock * sizeof(_Float16);
+    __shared__ __attribute__((aligned(1024))) _Float16 s_ring[kStages * kBlocks * kBlock];
+
+    // tiles in order on each of the 8 dies, whose L2 then holds the panels that neighbours share
+    const int tiles = gridDim.x, die = blockIdx.x % 8;
+    const int t = die * (tiles / 8) + (die < tiles % 8 ? die : tiles % 8) + blockIdx.x / 8;
+    int ti, tj;
+    if (a.symmetric) {
+        ti = static_cast<int>((sqrtf(8.0f * static_cast<float>(t) + 1.0f) - 1.0f) * 0.5f);
+        while (ti * (ti + 1) / 2 > t) --ti;
+        while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
+        tj = t - ti * (ti + 1) / 2;
+    } else {  // bands of four tile rows
+        const int band = t / (4 * a.tile_cols), in = t % (4 * a.tile_cols);
+        const int height = a.tile_rows - band * 4 < 4 ? a.tile_rows - band * 4 : 4;
+        ti = band * 4 + in % height;
+        tj = in / height;
+    }
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+    const size_t batch = blockIdx.y;
+    const int row_panels = a.rows / kPanel, col_panels = a.cols / kPanel, blocks = a.depth / kDepth;
+
+    // where this wave's blocks of a stage come from; panels past the edge repeat the last one and are not stored
+    const _Float16 *src[L];
 #pragma unroll
-        for (int k = 0; k < kStep; k += 16) {
-            const int kc = k + lane / 32 * 8;
-            const h16x8 ph = *reinterpret_cast<const h16x8 *>(&s_op[0][0][wr + lane % 32][kc]);
-            const h16x8 pl = *reinterpret_cast<const h16x8 *>(&s_op[0][1][wr + lane % 32][kc]);
-            const h16x8 qh = *reinterpret_cast<const h16x8 *>(&s_op[1][0][wc + lane % 32][kc]);
-            const h16x8 ql = *reinterpret_cast<const h16x8 *>(&s_op[1][1][wc + lane % 32][kc]);
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, acc, 0, 0, 0);
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, acc, 0, 0, 0);
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc, 0, 0, 0);
+    for (int i = 0; i < L; ++i) {
+        const int b = wave * L + i;
+        const int s = b % S, panel = b / S % kPanels, plane = b / (S * kPanels) % PL, op = b / (S * kPanels * PL);
+        int at = (op ? tj : ti) * kPanels + panel;
+        const int last = (op ? col_panels : row_panels) - 1;
+        at = at < last ? at : last;
+        const Planes &from = op ? a.q : a.p;
+        src[i] = (plane ? from.lo : from.hi) + batch * (static_cast<size_t>(op ? a.cols : a.rows) * a.depth) +
+                 block_at(at, s, a.depth);
+    }
+    const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) _Float16 *)s_ring));
+    const uint32_t lane_bytes = lane * 16;
+    const int stages = blocks / S;
+    int issued = 0;
+    const auto issue = [&](int i) {  // block i of this wave's share of stage `issued`
+        load_block(src[i], lane_bytes, ring + (issued % kStages) * kStageBytes + (wave * L + i) * 1024);
+        if (issued + 1 < stages) src[i] += S * kBlock;  // past the end the last stage is loaded again, unused
+    };
+    const int wr = wave / 2, wc = wave % 2;
+    constexpr int R = 2 * PL * F;  // operands of a wave for one block of 16 columns
+    h16x8 frag[2][R];
+    const auto fetch = [&](const _Float16 *stage_at, int s, int turn, int r) {
+        const int op = r / (PL * F), plane = r / F % PL, f = r % F;
+        frag[turn][r] = *reinterpret_cast<const h16x8 *>(
+            stage_at + (((op * PL + plane) * kPanels + (op ? wc : wr) * F + f) * S + s) * kBlock);
+    };
+    const auto stage_at = [&](int stage) { return s_ring + (stage % kStages) * (kBlocks * kBlock) + lane * 8; };
+    f32x16 acc[F][F] = {};
+    // The products of one block of 16 columns with, in between and in this order, the reads of the next block's
+    // operands and FIRST..LAST of the stage's loads.
+    const auto multiply = [&](int turn, const _Float16 *next, int next_s, auto first, auto last) {
+        constexpr int M = PRODUCTS * F * F, kFirst = decltype(first)::value, kLoads = decltype(last)::value - kFirst;
+        constexpr int kReads = M > R ? M - M / 4 : M;  // the reads end early enough to be done at the next barrier
+#pragma unroll
+        for (int x = 0; x < M; ++x) {
+#pragma unroll
+            for (int r = x * R / kReads; r < (x + 1) * R / kReads && r < R; ++r) fetch(next, next_s, 1 - turn, r);
+#pragma unroll
+            for (int i = x * kLoads / M; i < (x + 1) * kLoads / M; ++i) issue(kFirst + i);
+            const int term = PRODUCTS == 1 ? 2 : x / (F * F), i = x / F % F, j = x % F;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag[turn][(term == 0 ? PL - 1 : 0) * F + i],
+                                                               frag[turn][(PL + (term == 1 ? PL - 1 : 0)) * F + j],
+                                                               acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    for (; issued < kStages - 1; ++issued)
+#pragma unroll
+        for (int i = 0; i < L; ++i) issue(i);
+    wait_and_meet<2 * L>();
+#pragma unroll
+    for (int r = 0; r < R; ++r) fetch(stage_at(0), 0, 0, r);
+    using Zero = std::integral_constant<int, 0>;
+    using Half = std::integral_constant<int, L / 2>;
+    using All = std::integral_constant<int, L>;
+    for (int i = 0; i < blocks / 2; ++i) {
+        // two blocks of 16 columns; depth is a multiple of 32. At each meeting the next stage is there and all waves
+        // are done with the one before this, whose place the loads then take.
+        wait_and_meet<L>();
+        if constexpr (S == 2) {
+            multiply(0, stage_at(i), 1, Zero(), Half());
+            multiply(1, stage_at(i + 1), 0, Half(), All());
+            ++issued;
+        } else {
+            multiply(0, stage_at(2 * i + 1), 0, Zero(), All());
+            ++issued;
+            wait_and_meet<L>();
+            multiply(1, stage_at(2 * i + 2), 0, Zero(), All());
+            ++issued;
         }
     }
-    const int col = blockIdx.x * kTile + wc + lane % 32;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+    const bool both = !a.symmetric || ti != tj;  // a tile on the diagonal is its own mirror
+    const size_t out_plane = batch * (static_cast<size_t>(a.rows) * a.cols);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int row = blockIdx.y * kTile + wr + i / 4 * 8 + lane / 32 * 4 + i % 4;
-        const size_t at = (b * a.rows + row) * a.cols + col;
-        float v = acc[i] * a.scale_acc;
-        if constexpr (KIND != kGram) v = __builtin_fmaf(a.scale_add, load_pair(a.add, at), v);
-        store_pair(a.out, at, v);
-        if constexpr (KIND == kApply) store_pair(a.out_t, (b * a.cols + col) * a.rows + row, v);
+    for (int i = 0; i < F; ++i) {
+        const int mp = ti * kPanels + wr * F + i;
+        if (mp >= row_panels) continue;
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const int np = tj * kPanels + wc * F + j;
+            if (np >= col_panels) continue;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                // this lane: column lane % 32, rows g * 8 + lane / 32 * 4 + 0..3
+                const size_t at = out_plane + block_at(np, mp * 2 + g / 2, a.rows) +
+                                  (g % 2 * kPanel + lane % 32) * 8 + lane / 32 * 4;
+                float v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = acc[i][j][g * 4 + k] * a.scale_acc;
+                if (a.add.hi) {
+                    const h16x4 h = *reinterpret_cast<const h16x4 *>(a.add.hi + at);
+                    const h16x4 l = *reinterpret_cast<const h16x4 *>(a.add.lo + at);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = __builtin_fmaf(a.scale_add, static_cast<float>(h[k]) + static_cast<float>(l[k]), v[k]);
+                }
+                h16x4 h, l;
+                split<4>(v, h, l);
+                if (both) {
+                    *reinterpret_cast<h16x4 *>(a.turned.hi + at) = h;
+                    if (a.turned.lo) *reinterpret_cast<h16x4 *>(a.turned.lo + at) = l;
+                }
+                // after the transpose this lane: row g * 8 + lane / 32 * 4 + lane % 4, columns from lane % 32 / 4 * 4
+                const size_t to = out_plane + block_at(mp, np * 2 + lane % 32 / 16, a.cols) +
+                                  (lane % 16 / 8 * kPanel + g * 8 + lane / 32 * 4 + lane % 4) * 8 + lane % 8 / 4 * 4;
+                *reinterpret_cast<h16x4 *>(a.straight.hi + to) = quad_transpose(h);
+                if (a.straight.lo) *reinterpret_cast<h16x4 *>(a.straight.lo + to) = quad_transpose(l);
+            }
+        }
     }
 }
 
-// out [batch][m][n] from the planes that are laid out as it is, [batch][pm][pn].
+// out [batch][m][n] from the planes that hold its rows.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, int m, int n, int pm, int pn,
                                                                 T *__restrict__ out) {
-    const int64_t count = static_cast<int64_t>(m) * n;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < count;
-         i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t r = i / n, c = i % n;
-        out[blockIdx.y * count + i] = static_cast<T>(
-            load_pair(x, blockIdx.y * static_cast<size_t>(pm) * pn + static_cast<size_t>(r) * pn + c) / kScaleX);
+    // a wave: 8 rows, 64 columns
+    const int lane = threadIdx.x % kWave;
+    const int row = blockIdx.y * 32 + threadIdx.x / kWave * 8 + lane % 8, col = blockIdx.x * 64 + lane / 8 * 8;
+    if (row >= m || col >= n) return;
+    const size_t at = blockIdx.z * (static_cast<size_t>(pm) * pn) + eight_at(row, col, pn);
+    const h16x8 h = *reinterpret_cast<const h16x8 *>(x.hi + at), l = *reinterpret_cast<const h16x8 *>(x.lo + at);
+    T *to = out + (static_cast<size_t>(blockIdx.z) * m + row) * n;
+    constexpr int N = Pack<T>::kN;
+#pragma unroll
+    for (int i = 0; i < 8 / N; ++i) {
+        typename Pack<T>::V v;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            v[j] = static_cast<T>((static_cast<float>(h[i * N + j]) + static_cast<float>(l[i * N + j])) / kScaleX);
+        if (col + i * N < n) store_pack(to, col + i * N, n, v);
     }
 }
 
-inline int64_t padded(int64_t v) { return (v + kTile - 1) / kTile * kTile; }
+inline int64_t padded(int64_t v) { return (v + kPanel - 1) / kPanel * kPanel; }
 
 struct Layout {
     double *partial;
@@ -200,6 +386,52 @@ gs_status check_sizes(int64_t batch, int64_t m, int64_t n) {
     return GS_OK;
 }
 
+constexpr int kUnits = 256;  // compute units
+
+// The tile edge of a product: least rounds of workgroups over the chip, times a tile's work, times what a tile of
+// that edge takes of the matrix cores' time next to the largest (its operands come through LDS more often).
+int tile_edge(int64_t batch, int rows, int cols, bool symmetric) {
+    int best = 0;
+    double least = 0.0;
+    const struct {
+        int edge;
+        double cost;
+    } edges[] = {{256, 1.0}, {192, 1.05}, {128, 1.25}, {64, 2.0}};
+    for (const auto &e : edges) {
+        const int64_t r = (rows + e.edge - 1) / e.edge, c = (cols + e.edge - 1) / e.edge;
+        const int64_t tiles = batch * (symmetric ? r * (r + 1) / 2 : r * c);
+        const double t = static_cast<double>((tiles + kUnits - 1) / kUnits) * e.edge * e.edge * e.cost;
+        if (best == 0 || t < least) {
+            best = e.edge;
+            least = t;
+        }
+    }
+    return best;
+}
+
+gs_status product(ProductArgs g, int64_t batch, int products, hipStream_t stream) {
+    const int edge = tile_edge(batch, g.rows, g.cols, g.symmetric != 0);
+    g.tile_rows = (g.rows + edge - 1) / edge;
+    g.tile_cols = (g.cols + edge - 1) / edge;
+    const dim3 grid(static_cast<unsigned>(g.symmetric ? g.tile_rows * (g.tile_rows + 1) / 2
+                                                      : g.tile_rows * g.tile_cols),
+                    static_cast<unsigned>(batch));
+#define GS_PRODUCT(T, P)                                                                                  \
+    if (edge == T && products == P)                                                                       \
+    hipLaunchKernelGGL((ortho_product_kernel<T, P>), grid, dim3(kThreads), 0, stream, g)
+    GS_PRODUCT(64, 1);
+    GS_PRODUCT(64, 3);
+    GS_PRODUCT(128, 1);
+    GS_PRODUCT(128, 3);
+    GS_PRODUCT(192, 1);
+    GS_PRODUCT(192, 3);
+    GS_PRODUCT(256, 1);
+    GS_PRODUCT(256, 3);
+#undef GS_PRODUCT
+    GS_LAUNCH_TRY("ortho_product_kernel");
+    return GS_OK;
+}
+
 template <typename T>
 gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps, float a, float b, float c, float eps,
               void *out, void *workspace, hipStream_t stream) {
@@ -215,24 +447,23 @@ gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps
                        m * n, l.partial);
     GS_LAUNCH_TRY("ortho_norm_kernel");
     int at = 0;  // which transposed copy is current
-    hipLaunchKernelGGL((ortho_split_kernel<T>), dim3(pn / kTile, pm / kTile, z), dim3(kThreads), 0, stream, u,
+    hipLaunchKernelGGL((ortho_split_kernel<T>), dim3((pn + 63) / 64, (pm + 63) / 64, z), dim3(kThreads), 0, stream, u,
                        l.partial, static_cast<int>(parts), static_cast<int>(m), static_cast<int>(n), pm, pn, eps,
                        tall ? l.xt[at] : l.x, tall ? l.x : l.xt[at]);
     GS_LAUNCH_TRY("ortho_split_kernel");
     for (int s = 0; s < steps; ++s) {
-        const dim3 square(M / kTile, M / kTile, z), wide(N / kTile, M / kTile, z);
-        ProductArgs g{l.x, l.x, {}, l.gram, {}, M, M, N, kScaleA / (kScaleX * kScaleX), 0.0f};
-        hipLaunchKernelGGL((ortho_product_kernel<kGram>), square, dim3(kThreads), 0, stream, g);
-        ProductArgs p{l.gram, l.gram, l.gram, l.poly, {}, M, M, M, c / kScaleA, b};
-        hipLaunchKernelGGL((ortho_product_kernel<kPolynomial>), square, dim3(kThreads), 0, stream, p);
-        ProductArgs y{l.poly, l.xt[at], l.x, l.x, l.xt[1 - at], M, N, M, 1.0f / kScaleA, a};
-        hipLaunchKernelGGL((ortho_product_kernel<kApply>), wide, dim3(kThreads), 0, stream, y);
-        GS_LAUNCH_TRY("ortho_product_kernel");
+        const int products = 3;
+        const ProductArgs ops[3] = {
+            {l.x, l.x, {}, l.gram, l.gram, M, M, N, 0, 0, 1, kScaleA / (kScaleX * kScaleX), 0.0f},
+            {l.gram, l.gram, l.gram, l.poly, l.poly, M, M, M, 0, 0, 1, c / kScaleA, b},
+            {l.poly, l.xt[at], l.xt[at], l.x, l.xt[1 - at], M, N, M, 0, 0, 0, 1.0f / kScaleA, a}};
+        for (const ProductArgs &g : ops) {
+            const gs_status bad = product(g, batch, products, stream);
+            if (bad != GS_OK) return bad;
+        }
         at = 1 - at;
     }
-    int64_t blocks = (m * n + kThreads * 4 - 1) / (kThreads * 4);
-    if (blocks > 4096) blocks = 4096;
-    hipLaunchKernelGGL((ortho_finish_kernel<T>), dim3(static_cast<unsigned>(blocks), z), dim3(kThreads), 0, stream,
+    hipLaunchKernelGGL((ortho_finish_kernel<T>), dim3((pn + 63) / 64, pm / 32, z), dim3(kThreads), 0, stream,
                        tall ? l.xt[at] : l.x, static_cast<int>(m), static_cast<int>(n), pm, pn,
                        static_cast<T *>(out));
     GS_LAUNCH_TRY("ortho_finish_kernel");
