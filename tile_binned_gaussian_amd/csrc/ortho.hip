@@ -21,27 +21,28 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr float kScaleX = 4096.0f;
 constexpr float kScaleA = 1024.0f;
 constexpr int kThreads = 256;
-constexpr int kNormBlocks = 64;
+constexpr int kNormBlocks = 512;  // workgroups that share a matrix's norm, at most
 constexpr int kPanel = 32;   // rows of a panel; planes are padded to it with zeros both ways
 constexpr int kDepth = 16;   // columns of a block
 constexpr int kBlock = kPanel * kDepth;  // elements of a block: 1 KB
 constexpr int kStages = 4;
 
-// A plane holds a matrix [rows][depth] as blocks of 32 rows and 16 columns, [rows / 32][depth / 16][512], each in the
+// A plane holds a matrix [rows][depth] as blocks of 32 rows and 16 columns, [depth / 16][rows / 32][512], each in the
 // order in which a wave's lanes hold a matrix-core operand: lane l has row l % 32 and the eight columns from
 // l / 32 * 8 on. A block goes from memory to LDS and from LDS to registers as 1 KB in a row: no bank is hit twice,
-// whatever the tile.
+// whatever the tile. A tile's blocks of the same columns are neighbours in memory, so the workgroups, which go
+// through the columns together, spread over all memory channels.
 struct Planes {
     _Float16 *hi, *lo;
 };
 
-__device__ __forceinline__ size_t block_at(int panel, int block, int depth) {
-    return (static_cast<size_t>(panel) * (depth / kDepth) + block) * kBlock;
+__device__ __forceinline__ size_t block_at(int panel, int block, int rows) {
+    return (static_cast<size_t>(block) * (rows / kPanel) + panel) * kBlock;
 }
 
 // Element offset of the eight columns from col (a multiple of 8) on of a row.
-__device__ __forceinline__ size_t eight_at(int row, int col, int depth) {
-    return block_at(row / kPanel, col / kDepth, depth) + (col / 8 % 2 * kPanel + row % kPanel) * 8;
+__device__ __forceinline__ size_t eight_at(int row, int col, int rows) {
+    return block_at(row / kPanel, col / kDepth, rows) + (col / 8 % 2 * kPanel + row % kPanel) * 8;
 }
 
 template <int N, typename H>
@@ -51,6 +52,17 @@ __device__ __forceinline__ void split(const float *v, H &hi, H &lo) {
         hi[j] = static_cast<_Float16>(v[j]);
         lo[j] = static_cast<_Float16>(v[j] - static_cast<float>(hi[j]));
     }
+}
+
+// The sum over the workgroup's threads, in every thread.
+__device__ __forceinline__ double workgroup_sum(double v, double *s_part) {
+    s_part[threadIdx.x] = v;
+    __syncthreads();
+    for (int d = kThreads / 2; d > 0; d >>= 1) {
+        if (static_cast<int>(threadIdx.x) < d) s_part[threadIdx.x] += s_part[threadIdx.x + d];
+        __syncthreads();
+    }
+    return s_part[0];
 }
 
 // Partial sums of squares of matrix blockIdx.y in float64.
@@ -70,13 +82,8 @@ __global__ __launch_bounds__(kThreads) void ortho_norm_kernel(const T *__restric
             s = __builtin_fma(d, d, s);
         }
     }
-    s_part[threadIdx.x] = s;
-    __syncthreads();
-    for (int d = kThreads / 2; d > 0; d >>= 1) {
-        if (static_cast<int>(threadIdx.x) < d) s_part[threadIdx.x] += s_part[threadIdx.x + d];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = s_part[0];
+    s = workgroup_sum(s, s_part);
+    if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
 // X = update / (norm + eps) in both orders: `direct` holds the update's rows, `turned` its columns; 64 x 64 elements
@@ -88,14 +95,11 @@ __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restri
                                                                Planes turned) {
     constexpr int kTile = 64;
     __shared__ float s_tile[kTile][kTile + 1];
-    __shared__ double s_scale;
-    if (threadIdx.x == 0) {
-        double s = 0.0;
-        for (int i = 0; i < parts; ++i) s += partial[blockIdx.z * parts + i];
-        s_scale = static_cast<double>(kScaleX) / (sqrt(s) + static_cast<double>(eps));
-    }
-    __syncthreads();
-    const double scale = s_scale;
+    __shared__ double s_part[kThreads];
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kThreads) sum += partial[blockIdx.z * parts + i];
+    const double scale =
+        static_cast<double>(kScaleX) / (sqrt(workgroup_sum(sum, s_part)) + static_cast<double>(eps));
     const size_t plane = blockIdx.z * static_cast<size_t>(pm) * pn;
     const int r0 = blockIdx.y * kTile, c0 = blockIdx.x * kTile;
     const int tc = threadIdx.x % kTile;
@@ -117,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restri
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = s_tile[row][col + j];
             split<8>(v, hi, lo);
-            const size_t at = plane + eight_at(r0 + row, c0 + col, pn);
+            const size_t at = plane + eight_at(r0 + row, c0 + col, pm);
             *reinterpret_cast<h16x8 *>(direct.hi + at) = hi;
             *reinterpret_cast<h16x8 *>(direct.lo + at) = lo;
         }
@@ -125,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restri
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = s_tile[col + j][row];
             split<8>(v, hi, lo);
-            const size_t at = plane + eight_at(c0 + row, r0 + col, pm);
+            const size_t at = plane + eight_at(c0 + row, r0 + col, pn);
             *reinterpret_cast<h16x8 *>(turned.hi + at) = hi;
             *reinterpret_cast<h16x8 *>(turned.lo + at) = lo;
         }
@@ -219,16 +223,19 @@ __global__ __launch_bounds__(kThreads, T <= 128 ? 2 : 1) void ortho_product_kern
         at = at < last ? at : last;
         const Planes &from = op ? a.q : a.p;
         src[i] = (plane ? from.lo : from.hi) + batch * (static_cast<size_t>(op ? a.cols : a.rows) * a.depth) +
-                 block_at(at, s, a.depth);
+                 block_at(at, s, op ? a.cols : a.rows);
     }
     const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) _Float16 *)s_ring));
     const uint32_t lane_bytes = lane * 16;
     const int stages = blocks / S;
+    const size_t row_step = static_cast<size_t>(S) * row_panels * kBlock;
+    const size_t col_step = static_cast<size_t>(S) * col_panels * kBlock;
     int issued = 0;
     const auto issue = [&](int i) {  // block i of this wave's share of stage `issued`
         load_block(src[i], lane_bytes, ring + (issued % kStages) * kStageBytes + (wave * L + i) * 1024);
-        if (issued + 1 < stages) src[i] += S * kBlock;  // past the end the last stage is loaded again, unused
+        // past the end the last stage is loaded again, unused
+        if (issued + 1 < stages) src[i] += wave * L + i < kBlocks / 2 ? row_step : col_step;
     };
     const int wr = wave / 2, wc = wave % 2;
     constexpr int R = 2 * PL * F;  // operands of a wave for one block of 16 columns
@@ -298,7 +305,7 @@ __global__ __launch_bounds__(kThreads, T <= 128 ? 2 : 1) void ortho_product_kern
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 // this lane: column lane % 32, rows g * 8 + lane / 32 * 4 + 0..3
-                const size_t at = out_plane + block_at(np, mp * 2 + g / 2, a.rows) +
+                const size_t at = out_plane + block_at(np, mp * 2 + g / 2, a.cols) +
                                   (g % 2 * kPanel + lane % 32) * 8 + lane / 32 * 4;
                 float v[4];
 #pragma unroll
@@ -317,7 +324,7 @@ __global__ __launch_bounds__(kThreads, T <= 128 ? 2 : 1) void ortho_product_kern
                     if (a.turned.lo) *reinterpret_cast<h16x4 *>(a.turned.lo + at) = l;
                 }
                 // after the transpose this lane: row g * 8 + lane / 32 * 4 + lane % 4, columns from lane % 32 / 4 * 4
-                const size_t to = out_plane + block_at(mp, np * 2 + lane % 32 / 16, a.cols) +
+                const size_t to = out_plane + block_at(mp, np * 2 + lane % 32 / 16, a.rows) +
                                   (lane % 16 / 8 * kPanel + g * 8 + lane / 32 * 4 + lane % 4) * 8 + lane % 8 / 4 * 4;
                 *reinterpret_cast<h16x4 *>(a.straight.hi + to) = quad_transpose(h);
                 if (a.straight.lo) *reinterpret_cast<h16x4 *>(a.straight.lo + to) = quad_transpose(l);
@@ -334,7 +341,7 @@ __global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, int m,
     const int lane = threadIdx.x % kWave;
     const int row = blockIdx.y * 32 + threadIdx.x / kWave * 8 + lane % 8, col = blockIdx.x * 64 + lane / 8 * 8;
     if (row >= m || col >= n) return;
-    const size_t at = blockIdx.z * (static_cast<size_t>(pm) * pn) + eight_at(row, col, pn);
+    const size_t at = blockIdx.z * (static_cast<size_t>(pm) * pn) + eight_at(row, col, pm);
     const h16x8 h = *reinterpret_cast<const h16x8 *>(x.hi + at), l = *reinterpret_cast<const h16x8 *>(x.lo + at);
     T *to = out + (static_cast<size_t>(blockIdx.z) * m + row) * n;
     constexpr int N = Pack<T>::kN;
@@ -432,6 +439,17 @@ gs_status product(ProductArgs g, int64_t batch, int products, hipStream_t stream
     return GS_OK;
 }
 
+// The last steps, whose products take both halves of the operands. The earlier ones of a result with fewer than 24
+// bits take the high halves: 2^-12 of an operand is less than the update's own rounding (equal to it for float16),
+// and a step damps the error that reaches it, so what the last steps add counts most. Measured against 64 bits on
+// momentum-like matrices of 32 to 2000 rows (2-norm, next to the result's own rounding): bfloat16 with two full steps
+// of five 1.00 to 1.14 times that rounding, float16 with three 1.00 to 1.12 (with two up to 4.8). X itself, A in b A,
+// and the sums keep both halves throughout.
+template <typename T>
+constexpr int full_steps() {
+    return std::is_same<T, float>::value ? 1 << 30 : std::is_same<T, _Float16>::value ? 3 : 2;
+}
+
 template <typename T>
 gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps, float a, float b, float c, float eps,
               void *out, void *workspace, hipStream_t stream) {
@@ -452,11 +470,14 @@ gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps
                        tall ? l.xt[at] : l.x, tall ? l.x : l.xt[at]);
     GS_LAUNCH_TRY("ortho_split_kernel");
     for (int s = 0; s < steps; ++s) {
-        const int products = 3;
+        // the low parts that nothing reads are not written
+        const int products = steps - s <= full_steps<T>() ? 3 : 1;
+        const Planes poly = products == 3 ? l.poly : Planes{l.poly.hi, nullptr};
+        const Planes next = steps - s - 1 <= full_steps<T>() ? l.x : Planes{l.x.hi, nullptr};
         const ProductArgs ops[3] = {
             {l.x, l.x, {}, l.gram, l.gram, M, M, N, 0, 0, 1, kScaleA / (kScaleX * kScaleX), 0.0f},
-            {l.gram, l.gram, l.gram, l.poly, l.poly, M, M, M, 0, 0, 1, c / kScaleA, b},
-            {l.poly, l.xt[at], l.xt[at], l.x, l.xt[1 - at], M, N, M, 0, 0, 0, 1.0f / kScaleA, a}};
+            {l.gram, l.gram, l.gram, poly, poly, M, M, M, 0, 0, 1, c / kScaleA, b},
+            {l.poly, l.xt[at], l.xt[at], next, l.xt[1 - at], M, N, M, 0, 0, 0, 1.0f / kScaleA, a}};
         for (const ProductArgs &g : ops) {
             const gs_status bad = product(g, batch, products, stream);
             if (bad != GS_OK) return bad;
