@@ -116,11 +116,11 @@ def _stream_scoped(fn):
     call allocates - workspaces, outputs, a grown workspace and the copy into it - belongs to the stream its
     kernels run on: torch's caching allocator then never hands such a buffer to another stream while work queued
     on this one may still use it, and the copy is ordered after the work that produced its source."""
-    sig = inspect.signature(fn)
+    at = list(inspect.signature(fn).parameters).index("stream")
 
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
-        stream = sig.bind_partial(*args, **kwargs).arguments.get("stream")
+        stream = args[at] if len(args) > at else kwargs.get("stream")
         if stream is None:
             return fn(*args, **kwargs)
         with torch.cuda.stream(stream):
@@ -594,6 +594,36 @@ def _element(t, name):
     return code
 
 
+# These operators run on a handful of tokens too, where a call's cost is its host work: one look at an argument that is
+# as it should be, and plain integers for ctypes. What is not as it should be goes to _req, which says why.
+
+
+def _arg(t, name, dtype, device, shape):
+    """The address of a tensor argument of this type, device and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda
+            and t.device == device):
+        _req(t, name, dtype, device, shape)
+    return t.data_ptr()
+
+
+def _stream_int(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
+
+
+def _room(nbytes, device):
+    """(workspace or None, its address, its size)."""
+    if nbytes == 0:
+        return None, None, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), nbytes
+
+
+def _given_room(workspace):
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
 def _norm_inputs(x, weight):
     code, wcode = _element(x, "x"), _element(weight, "weight")
     if x.dim() < 1:
@@ -604,9 +634,8 @@ def _norm_inputs(x, weight):
     if wcode not in (code, 0):
         raise TypeError(f"weight must be {x.dtype} or torch.float32 (got {weight.dtype})")
     dev = x.device
-    _req(x, "x", x.dtype, dev)
-    _req(weight, "weight", weight.dtype, dev, (dim,))
-    return code, wcode, dev, x.numel() // dim, dim
+    return code, wcode, dev, x.numel() // dim, dim, _arg(x, "x", x.dtype, dev, x.shape), \
+        _arg(weight, "weight", weight.dtype, dev, (dim,))
 
 
 @dataclass
@@ -623,23 +652,23 @@ def gs_layer_norm_fwd(x, weight, bias=None, eps=1e-5, stats=True, out=None, stre
 
     x [..., dim] of float32, bfloat16 or float16; weight and bias [dim] of x's type or float32."""
     lib = load_library()
-    code, wcode, dev, rows, dim = _norm_inputs(x, weight)
-    if bias is not None:
-        _req(bias, "bias", weight.dtype, dev, (dim,))
+    code, wcode, dev, rows, dim, px, pw = _norm_inputs(x, weight)
+    pb = None if bias is None else _arg(bias, "bias", weight.dtype, dev, (dim,))
+    shape = x.shape[:-1]
     if out is None:
-        shape = x.shape[:-1]
         out = LayerNorm(torch.empty_like(x),
                         torch.empty(shape, dtype=torch.float32, device=dev) if stats else None,
                         torch.empty(shape, dtype=torch.float32, device=dev) if stats else None)
+        py = out.y.data_ptr()
+        pm, pr = (out.mean.data_ptr(), out.rstd.data_ptr()) if stats else (None, None)
     else:
-        _req(out.y, "y", x.dtype, dev, x.shape)
+        py, pm, pr = _arg(out.y, "y", x.dtype, dev, x.shape), None, None
         if (out.mean is None) != (out.rstd is None):
             raise ValueError("mean and rstd go together")
         if out.mean is not None:
-            _req(out.mean, "mean", torch.float32, dev, x.shape[:-1])
-            _req(out.rstd, "rstd", torch.float32, dev, x.shape[:-1])
-    _check(lib.gs_layer_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), rows, dim, float(eps), code, wcode, _ptr(out.y),
-                                 _ptr(out.mean), _ptr(out.rstd), _stream(stream)))
+            pm = _arg(out.mean, "mean", torch.float32, dev, shape)
+            pr = _arg(out.rstd, "rstd", torch.float32, dev, shape)
+    _check(lib.gs_layer_norm_fwd(px, pw, pb, rows, dim, eps, code, wcode, py, pm, pr, _stream_int(stream)))
     return out
 
 
@@ -656,22 +685,22 @@ def gs_layer_norm_bwd(x, weight, mean, rstd, grad_y, grad_bias=True, out=None, s
     """Gradients of sum(grad_y * y) of gs_layer_norm_fwd, from its inputs and statistics (grad_bias=False: the bias's
     is not computed)."""
     lib = load_library()
-    code, wcode, dev, rows, dim = _norm_inputs(x, weight)
-    _req(mean, "mean", torch.float32, dev, x.shape[:-1])
-    _req(rstd, "rstd", torch.float32, dev, x.shape[:-1])
-    _req(grad_y, "grad_y", x.dtype, dev, x.shape)
+    code, wcode, dev, rows, dim, px, pw = _norm_inputs(x, weight)
+    pm = _arg(mean, "mean", torch.float32, dev, x.shape[:-1])
+    pr = _arg(rstd, "rstd", torch.float32, dev, x.shape[:-1])
+    pg = _arg(grad_y, "grad_y", x.dtype, dev, x.shape)
     if out is None:
         out = LayerNormGrad(torch.empty_like(x), torch.empty_like(weight),
                             torch.empty_like(weight) if grad_bias else None)
+        ox, ow, ob = out.x.data_ptr(), out.weight.data_ptr(), out.bias.data_ptr() if grad_bias else None
     else:
-        _req(out.x, "grad_x", x.dtype, dev, x.shape)
-        _req(out.weight, "grad_weight", weight.dtype, dev, (dim,))
-        if out.bias is not None:
-            _req(out.bias, "grad_bias", weight.dtype, dev, (dim,))
-    ws = workspace if workspace is not None else _workspace(lib.gs_layer_norm_bwd_workspace_bytes(rows, dim), dev)
-    _check(lib.gs_layer_norm_bwd(_ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(grad_y), rows, dim, code, wcode,
-                                 _ptr(out.x), _ptr(out.weight), _ptr(out.bias), _ptr(ws), ws.numel(),
-                                 _stream(stream)))
+        ox = _arg(out.x, "grad_x", x.dtype, dev, x.shape)
+        ow = _arg(out.weight, "grad_weight", weight.dtype, dev, (dim,))
+        ob = None if out.bias is None else _arg(out.bias, "grad_bias", weight.dtype, dev, (dim,))
+    ws, pws, room = _room(lib.gs_layer_norm_bwd_workspace_bytes(rows, dim), dev) if workspace is None \
+        else _given_room(workspace)
+    _check(lib.gs_layer_norm_bwd(px, pw, pm, pr, pg, rows, dim, code, wcode, ox, ow, ob, pws, room,
+                                 _stream_int(stream)))
     return out
 
 
@@ -682,14 +711,16 @@ class ExpertPlan:
     pairs: torch.Tensor  # [tokens * choices] int32: each row's pair, -1 past the kept ones
 
 
-def _plan_sizes(plan, dev):
-    _req(plan.offsets, "offsets", torch.int32, dev)
-    _req(plan.rows, "rows", torch.int32, dev)
-    if plan.rows.dim() != 2 or plan.rows.shape[1] < 1:
+def _plan_inputs(plan, device):
+    """(tokens, choices, experts, address of offsets, address of rows)."""
+    rows, offsets = plan.rows, plan.offsets
+    po, pr = _arg(offsets, "offsets", torch.int32, device, offsets.shape), _arg(rows, "rows", torch.int32, device,
+                                                                                 rows.shape)
+    if rows.dim() != 2 or rows.shape[1] < 1:
         raise ValueError("rows must be [tokens, choices]")
-    if plan.offsets.dim() != 1 or plan.offsets.shape[0] < 2:
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError("offsets must be [experts + 1]")
-    return plan.rows.shape[0], plan.rows.shape[1], plan.offsets.shape[0] - 1
+    return rows.shape[0], rows.shape[1], offsets.shape[0] - 1, po, pr
 
 
 @_stream_scoped
@@ -701,19 +732,19 @@ def gs_expert_plan(ids, experts, out=None, stream=None, workspace=None) -> Exper
     if ids.dim() != 2 or ids.shape[1] < 1:
         raise ValueError("ids must be [tokens, choices]")
     dev = ids.device
-    T, K, E = ids.shape[0], ids.shape[1], int(experts)
+    (T, K), E = ids.shape, int(experts)
     if E < 1:
         raise ValueError("experts must be >= 1")
     if out is None:
         out = ExpertPlan(torch.empty(E + 1, dtype=torch.int32, device=dev), torch.empty_like(ids),
                          torch.empty(T * K, dtype=torch.int32, device=dev))
+        po, pr, pp = out.offsets.data_ptr(), out.rows.data_ptr(), out.pairs.data_ptr()
     else:
-        _req(out.offsets, "offsets", torch.int32, dev, (E + 1,))
-        _req(out.rows, "rows", torch.int32, dev, (T, K))
-        _req(out.pairs, "pairs", torch.int32, dev, (T * K,))
-    ws = workspace if workspace is not None else _workspace(lib.gs_expert_plan_workspace_bytes(T, K, E), dev)
-    _check(lib.gs_expert_plan(_ptr(ids), T, K, E, _ptr(out.offsets), _ptr(out.rows), _ptr(out.pairs), _ptr(ws),
-                              ws.numel(), _stream(stream)))
+        po = _arg(out.offsets, "offsets", torch.int32, dev, (E + 1,))
+        pr, pp = _arg(out.rows, "rows", torch.int32, dev, (T, K)), _arg(out.pairs, "pairs", torch.int32, dev, (T * K,))
+    ws, pws, room = _room(lib.gs_expert_plan_workspace_bytes(T, K, E), dev) if workspace is None \
+        else _given_room(workspace)
+    _check(lib.gs_expert_plan(ids.data_ptr(), T, K, E, po, pr, pp, pws, room, _stream_int(stream)))
     return out
 
 
@@ -723,17 +754,15 @@ def gs_expert_dispatch(x, plan, out=None, stream=None):
     the kept ones. The gradient of x is gs_expert_combine(gradient of the result, plan)."""
     lib = load_library()
     code, dev = _element(x, "x"), x.device
-    T, K, E = _plan_sizes(plan, dev)
+    T, K, E, po, pr = _plan_inputs(plan, dev)
     if x.dim() != 2 or x.shape[0] != T or x.shape[1] < 1:
         raise ValueError(f"x must be [{T}, dim] (got {tuple(x.shape)})")
-    _req(x, "x", x.dtype, dev)
-    D = x.shape[1]
+    px, D = _arg(x, "x", x.dtype, dev, x.shape), x.shape[1]
     if out is None:
         out = torch.empty((T * K, D), dtype=x.dtype, device=dev)
     else:
-        _req(out, "sent", x.dtype, dev, (T * K, D))
-    _check(lib.gs_expert_dispatch(_ptr(x), _ptr(plan.offsets), _ptr(plan.rows), T, K, E, D, code, _ptr(out),
-                                  _stream(stream)))
+        _arg(out, "sent", x.dtype, dev, (T * K, D))
+    _check(lib.gs_expert_dispatch(px, po, pr, T, K, E, D, code, out.data_ptr(), _stream_int(stream)))
     return out
 
 
@@ -749,17 +778,15 @@ def gs_expert_combine(source, plan, weights=None, out=None, stream=None):
     [tokens * choices, dim]: [tokens, dim], summed in float32."""
     lib = load_library()
     code, dev = _element(source, "source"), source.device
-    T, K, _ = _plan_sizes(plan, dev)
+    T, K, _, _, pr = _plan_inputs(plan, dev)
     D = _sorted_rows(source, "source", T, K)
-    _req(source, "source", source.dtype, dev)
-    if weights is not None:
-        _req(weights, "weights", torch.float32, dev, (T, K))
+    ps = _arg(source, "source", source.dtype, dev, source.shape)
+    pw = None if weights is None else _arg(weights, "weights", torch.float32, dev, (T, K))
     if out is None:
         out = torch.empty((T, D), dtype=source.dtype, device=dev)
     else:
-        _req(out, "y", source.dtype, dev, (T, D))
-    _check(lib.gs_expert_combine(_ptr(source), _ptr(plan.rows), _ptr(weights), T, K, D, code, _ptr(out),
-                                 _stream(stream)))
+        _arg(out, "y", source.dtype, dev, (T, D))
+    _check(lib.gs_expert_combine(ps, pr, pw, T, K, D, code, out.data_ptr(), _stream_int(stream)))
     return out
 
 
@@ -775,18 +802,18 @@ def gs_expert_combine_bwd(source, plan, weights, grad_y, out=None, stream=None) 
     kept ones) and weights (0 for a dropped pair)."""
     lib = load_library()
     code, dev = _element(source, "source"), source.device
-    T, K, E = _plan_sizes(plan, dev)
+    T, K, E, po, pr = _plan_inputs(plan, dev)
     D = _sorted_rows(source, "source", T, K)
-    _req(source, "source", source.dtype, dev)
-    _req(weights, "weights", torch.float32, dev, (T, K))
-    _req(grad_y, "grad_y", source.dtype, dev, (T, D))
+    ps = _arg(source, "source", source.dtype, dev, source.shape)
+    pw = _arg(weights, "weights", torch.float32, dev, (T, K))
+    pg = _arg(grad_y, "grad_y", source.dtype, dev, (T, D))
     if out is None:
         out = ExpertCombineGrad(torch.empty_like(source), torch.empty_like(weights))
     else:
-        _req(out.rows, "grad_rows", source.dtype, dev, (T * K, D))
-        _req(out.weights, "grad_weights", torch.float32, dev, (T, K))
-    _check(lib.gs_expert_combine_bwd(_ptr(source), _ptr(plan.offsets), _ptr(plan.rows), _ptr(weights), _ptr(grad_y),
-                                     T, K, E, D, code, _ptr(out.rows), _ptr(out.weights), _stream(stream)))
+        _arg(out.rows, "grad_rows", source.dtype, dev, (T * K, D))
+        _arg(out.weights, "grad_weights", torch.float32, dev, (T, K))
+    _check(lib.gs_expert_combine_bwd(ps, po, pr, pw, pg, T, K, E, D, code, out.rows.data_ptr(),
+                                     out.weights.data_ptr(), _stream_int(stream)))
     return out
 
 
@@ -799,15 +826,16 @@ def gs_orthogonalize(update, steps=5, coefficients=(3.4445, -4.7750, 2.0315), ep
     code, dev = _element(update, "update"), update.device
     if update.dim() not in (2, 3) or update.shape[-1] < 1 or update.shape[-2] < 1:
         raise ValueError(f"update must be [m, n] or [batch, m, n] (got {tuple(update.shape)})")
-    _req(update, "update", update.dtype, dev)
+    pu = _arg(update, "update", update.dtype, dev, update.shape)
     m, n = update.shape[-2], update.shape[-1]
     B = update.shape[0] if update.dim() == 3 else 1
-    a, b, c = (float(v) for v in coefficients)
+    a, b, c = coefficients
     if out is None:
         out = torch.empty_like(update)
     else:
-        _req(out, "out", update.dtype, dev, update.shape)
-    ws = workspace if workspace is not None else _workspace(lib.gs_orthogonalize_workspace_bytes(B, m, n), dev)
-    _check(lib.gs_orthogonalize(_ptr(update), B, m, n, int(steps), a, b, c, float(eps), code, _ptr(out), _ptr(ws),
-                                ws.numel(), _stream(stream)))
+        _arg(out, "out", update.dtype, dev, update.shape)
+    ws, pws, room = _room(lib.gs_orthogonalize_workspace_bytes(B, m, n), dev) if workspace is None \
+        else _given_room(workspace)
+    _check(lib.gs_orthogonalize(pu, B, m, n, int(steps), a, b, c, eps, code, out.data_ptr(), pws, room,
+                                _stream_int(stream)))
     return out
