@@ -438,7 +438,8 @@ gs_status gs_expert_combine_bwd(const void *source, const int32_t *offsets, cons
  * stay below 16 and every entry of b A + c A A below 64 in magnitude, as they do for coefficients that converge.
  * A matrix that holds an infinity or NaN gives NaN; others in the batch are not affected.
  * Limits: 0 <= batch <= 65535, 1 <= m, n <= 65536, batch * m * n < 2^40, 0 <= steps <= 100. Asynchronous.
- * workspace: gs_orthogonalize_workspace_bytes(batch, m, n) bytes (0 for sizes out of range).
+ * workspace: gs_orthogonalize_workspace_bytes(batch, m, n) bytes (0 for sizes out of range, and for matrices small
+ * enough for a compute unit's own memory, which need none).
  */
 size_t gs_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n);
 

@@ -89,10 +89,11 @@ def test_orthogonalize_refusals(lib):
                      (dict(dt=3), "dtype"), (dict(eps=-1.0), "eps"), (dict(eps=float("nan")), "eps"),
                      (dict(u=None), "NULL")):
         refused(lib, ortho(**kw), bad, word)
-    need = lib.gs_orthogonalize_workspace_bytes(3, 100, 200)
+    need = lib.gs_orthogonalize_workspace_bytes(3, 300, 200)
     assert need > 0
-    refused(lib, ortho(B=3, m=100, n=200, wsb=need - 1), space, "workspace")
-    refused(lib, ortho(ws=None), space, "workspace")
+    refused(lib, ortho(B=3, m=300, n=200, wsb=need - 1), space, "workspace")
+    refused(lib, ortho(B=3, m=300, n=200, ws=None), space, "workspace")
+    assert lib.gs_orthogonalize_workspace_bytes(3, 100, 60) == 0  # the chip's own memory holds a small matrix
     assert ortho(B=0, u=None) == binding.GS_OK
     for sizes in ((1, 0, 8), (1, 8, 65537), (0, 8, 8), (65535, 65536, 65536)):
         assert lib.gs_orthogonalize_workspace_bytes(*sizes) == 0

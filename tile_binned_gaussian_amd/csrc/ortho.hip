@@ -355,6 +355,277 @@ __global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, int m,
     }
 }
 
+// ------------------------------------------------------------------------------------------------------------
+// small matrices: one workgroup a matrix, all steps in one launch
+//
+// Wave w owns the 32 columns of X of blocks w, w + 8, ...: all of their rows, in float32 registers in the order in
+// which the matrix cores leave a result (lane: column lane % 32; register 4 g + k: row 8 g + lane / 32 * 4 + k of
+// each 32). X goes to LDS once a step, as pairs of float16, for the Gram product; the step's matrix comes back
+// through LDS to every wave, which multiplies it with its own columns straight from its registers. That works because
+// a product may take its 16 columns in any order, as long as both operands take the same: all LDS blocks here hold
+// their columns in the order 0-3, 8-11 (lanes 0-31), 4-7, 12-15 (lanes 32-63), which is the registers' own.
+
+constexpr int kSmallThreads = 512;
+constexpr int kSmallWaves = kSmallThreads / kWave;
+constexpr int kSmallLds = 159 * 1024;
+
+// Column blocks of a wave, at most, where the matrix has 32 A rows: what the LDS allows.
+template <int A>
+constexpr int small_blocks() {
+    return A == 1 ? 5 : A == 2 ? 3 : A == 3 ? 2 : 1;
+}
+
+// Bytes of LDS: both halves of X [32 A][cols] and of a square matrix [32 A][32 A].
+inline int64_t small_lds(int64_t rows, int64_t cols) { return 4 * (rows * cols + rows * rows); }
+inline bool is_small(int64_t rows, int64_t cols) {
+    if (rows > 128 || small_lds(rows, cols) > kSmallLds) return false;
+    const int64_t a = rows / kPanel;
+    return cols / kPanel <= kSmallWaves * (a == 1 ? 5 : a == 2 ? 3 : a == 3 ? 2 : 1);
+}
+
+// Stores this lane's four values (rows g * 8 + lane / 32 * 4 + 0..3 of row block i, one column of column block j) as
+// columns of the other matrix: [columns of the result][rows of the result].
+__device__ __forceinline__ void small_store_turned(_Float16 *plane, int panels, int i, int j, int g, int lane,
+                                                   h16x4 v) {
+    *reinterpret_cast<h16x4 *>(plane + ((i * 2 + g / 2) * panels + j) * kBlock + lane * 8 + g % 2 * 4) = v;
+}
+// The same values after a quad transpose, as [rows of the result][columns of the result].
+__device__ __forceinline__ void small_store_straight(_Float16 *plane, int panels, int i, int j, int g, int lane,
+                                                     h16x4 v) {
+    const int row = g * 8 + lane / 32 * 4 + lane % 4;
+    *reinterpret_cast<h16x4 *>(plane + ((j * 2 + lane % 32 / 16) * panels + i) * kBlock +
+                               (lane / 4 % 2 * kPanel + row) * 8 + lane / 8 % 2 * 4) = quad_transpose(v);
+}
+
+// out += P Q^T over `blocks` blocks of 16 columns, row blocks i and j of planes with `panels` row blocks.
+template <int PRODUCTS>
+__device__ __forceinline__ f32x16 small_product(const _Float16 *hi, const _Float16 *lo, int panels, int i, int j,
+                                                int blocks, int lane) {
+    f32x16 acc[3] = {};
+#pragma unroll 2
+    for (int k = 0; k < blocks; ++k) {
+        const int pi = (k * panels + i) * kBlock + lane * 8, pj = (k * panels + j) * kBlock + lane * 8;
+        const h16x8 ph = *reinterpret_cast<const h16x8 *>(hi + pi), qh = *reinterpret_cast<const h16x8 *>(hi + pj);
+        if constexpr (PRODUCTS == 3) {
+            const h16x8 pl = *reinterpret_cast<const h16x8 *>(lo + pi), ql = *reinterpret_cast<const h16x8 *>(lo + pj);
+            acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, acc[0], 0, 0, 0);
+            acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, acc[1], 0, 0, 0);
+        }
+        acc[2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc[2], 0, 0, 0);
+    }
+    if constexpr (PRODUCTS == 3)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[2][e] += acc[0][e] + acc[1][e];
+    return acc[2];
+}
+
+template <int A>
+struct SmallMatrix {
+    f32x16 x[small_blocks<A>()][A];
+};
+
+// One step on the workgroup's matrix; col_blocks: its blocks of 32 columns.
+template <int A, int PRODUCTS>
+__device__ __forceinline__ void small_step(SmallMatrix<A> &s, int col_blocks, float a, float b, float c, _Float16 *lds,
+                                           int wave, int lane) {
+    constexpr int kTri = A * (A + 1) / 2, kTurns = (kTri + kSmallWaves - 1) / kSmallWaves;
+    _Float16 *xh = lds, *xl = xh + col_blocks * 2 * A * kBlock;
+    _Float16 *gh = xl + col_blocks * 2 * A * kBlock, *gl = gh + 2 * A * A * kBlock;
+#pragma unroll
+    for (int q = 0; q < small_blocks<A>(); ++q) {
+        const int j = wave + q * kSmallWaves;
+        if (j >= col_blocks) break;
+#pragma unroll
+        for (int i = 0; i < A; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float v[4];
+                h16x4 h, l;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = s.x[q][i][g * 4 + k];
+                split<4>(v, h, l);
+                small_store_straight(xh, A, i, j, g, lane, h);
+                if constexpr (PRODUCTS == 3) small_store_straight(xl, A, i, j, g, lane, l);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
+    __syncthreads();
+    // the lower triangle's blocks, in turn over the waves
+    f32x16 gram[kTurns];
+    const auto place = [&](int t, int &i, int &j) {
+        const int n = t * kSmallWaves + wave;
+        i = n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0;
+        j = n - i * (i + 1) / 2;
+        return n < kTri;
+    };
+    const auto store = [&](const f32x16 &v16, int i, int j) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float v[4];
+            h16x4 h, l;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = v16[g * 4 + k];
+            split<4>(v, h, l);
+            small_store_straight(gh, A, i, j, g, lane, h);
+            if (i != j) small_store_turned(gh, A, i, j, g, lane, h);
+            if constexpr (PRODUCTS == 3) {
+                small_store_straight(gl, A, i, j, g, lane, l);
+                if (i != j) small_store_turned(gl, A, i, j, g, lane, l);
+            }
+        }
+    };
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+        int i, j;
+        if (!place(t, i, j)) break;
+        gram[t] = small_product<PRODUCTS>(xh, xl, A, i, j, col_blocks * 2, lane);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) gram[t][e] *= kScaleA / (kScaleX * kScaleX);
+        store(gram[t], i, j);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+        int i, j;
+        if (!place(t, i, j)) break;
+        const f32x16 square = small_product<PRODUCTS>(gh, gl, A, i, j, A * 2, lane);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) gram[t][e] = __builtin_fmaf(b, gram[t][e], square[e] * (c / kScaleA));
+    }
+    __syncthreads();  // the step's matrix takes the Gram matrix's place
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+        int i, j;
+        if (!place(t, i, j)) break;
+        store(gram[t], i, j);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < small_blocks<A>(); ++q) {
+        if (wave + q * kSmallWaves >= col_blocks) break;
+        f32x16 acc[A] = {};
+#pragma unroll
+        for (int k = 0; k < 2 * A; ++k) {
+            float v[8];
+            h16x8 qh, ql;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = s.x[q][k / 2][k % 2 * 8 + e];
+            split<8>(v, qh, ql);
+            h16x8 ph[A], pl[A];
+#pragma unroll
+            for (int i = 0; i < A; ++i) {
+                ph[i] = *reinterpret_cast<const h16x8 *>(gh + (k * A + i) * kBlock + lane * 8);
+                if constexpr (PRODUCTS == 3)
+                    pl[i] = *reinterpret_cast<const h16x8 *>(gl + (k * A + i) * kBlock + lane * 8);
+            }
+            if constexpr (PRODUCTS == 3) {
+#pragma unroll
+                for (int i = 0; i < A; ++i) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[i], qh, acc[i], 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < A; ++i) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], ql, acc[i], 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < A; ++i) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], qh, acc[i], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);  // hoisted reads of all blocks would not fit the registers
+        }
+#pragma unroll
+        for (int i = 0; i < A; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                s.x[q][i][e] = __builtin_fmaf(a, s.x[q][i][e], acc[i][e] * (1.0f / kScaleA));
+    }
+}
+
+// Element access through a buffer descriptor: an offset past the end reads 0 and is not written, so the edges of a
+// matrix need no branches.
+template <typename T>
+struct Buffer {
+    __amdgpu_buffer_rsrc_t rsrc;
+    __device__ __forceinline__ Buffer(const T *base, int count)
+        : rsrc(__builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(base), 0, count * static_cast<int>(sizeof(T)),
+                                                 0x00020000)) {}
+    __device__ __forceinline__ float load(int offset) const {
+        if constexpr (sizeof(T) == 4)
+            return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, offset * 4, 0, 0));
+        else
+            return static_cast<float>(
+                __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(rsrc, offset * 2, 0, 0)));
+    }
+    __device__ __forceinline__ void store(int offset, float v) const {
+        if constexpr (sizeof(T) == 4)
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rsrc, offset * 4, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<T>(v)), rsrc, offset * 2,
+                                                  0, 0);
+    }
+};
+
+// rows <= cols: the matrix as the steps see it, transposed from the update where tall.
+template <typename T, int A>
+__global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const T *__restrict__ update, int rows, int cols,
+                                                                    int tall, int steps, int full_steps, float a,
+                                                                    float b, float c, float eps, T *__restrict__ out) {
+    extern __shared__ __attribute__((aligned(16))) _Float16 s_small[];
+    __shared__ double s_sum[kSmallWaves];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+    const int col_blocks = (cols + kPanel - 1) / kPanel;
+    const size_t base = blockIdx.x * (static_cast<size_t>(rows) * cols);
+    const int row_step = tall ? 1 : cols, col_step = tall ? rows : 1;
+    // the offset of register e of row block i and column block j for this lane
+    const auto offset = [=](int l, int i, int j, int e) {
+        const int row = i * kPanel + e / 4 * 8 + l / 32 * 4 + e % 4, col = j * kPanel + l % 32;
+        return row < rows && col < cols ? row * row_step + col * col_step : 1 << 28;
+    };
+    SmallMatrix<A> s;
+    const Buffer<T> from(update + base, rows * cols);
+    double sum = 0.0;
+#pragma unroll
+    for (int q = 0; q < small_blocks<A>(); ++q)
+#pragma unroll
+        for (int i = 0; i < A; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s.x[q][i][e] = from.load(offset(lane, i, wave + q * kSmallWaves, e));
+#pragma unroll
+    for (int q = 0; q < small_blocks<A>(); ++q)
+#pragma unroll
+        for (int i = 0; i < A; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const double v = static_cast<double>(s.x[q][i][e]);
+                sum = __builtin_fma(v, v, sum);
+            }
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
+    if (lane == 0) s_sum[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+    for (int w = 0; w < kSmallWaves; ++w) sum += s_sum[w];
+    const double scale = static_cast<double>(kScaleX) / (sqrt(sum) + static_cast<double>(eps));
+#pragma unroll
+    for (int q = 0; q < small_blocks<A>(); ++q)
+#pragma unroll
+        for (int i = 0; i < A; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                s.x[q][i][e] = static_cast<float>(static_cast<double>(s.x[q][i][e]) * scale);
+    for (int k = 0; k < steps; ++k) {
+        if (steps - k <= full_steps)
+            small_step<A, 3>(s, col_blocks, a, b, c, s_small, wave, lane);
+        else
+            small_step<A, 1>(s, col_blocks, a, b, c, s_small, wave, lane);
+    }
+    const Buffer<T> to(out + base, rows * cols);
+    int late = lane;  // offsets formed anew: kept from the loads they would take a register each all along
+    asm volatile("" : "+v"(late));
+#pragma unroll
+    for (int q = 0; q < small_blocks<A>(); ++q)
+#pragma unroll
+        for (int i = 0; i < A; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                to.store(offset(late, i, wave + q * kSmallWaves, e), s.x[q][i][e] * (1.0f / kScaleX));
+}
+
 inline int64_t padded(int64_t v) { return (v + kPanel - 1) / kPanel * kPanel; }
 
 struct Layout {
@@ -451,10 +722,34 @@ constexpr int full_steps() {
 }
 
 template <typename T>
+gs_status run_small(const void *update, int64_t batch, int64_t rows, int64_t cols, bool tall, int steps, float a,
+                    float b, float c, float eps, void *out, hipStream_t stream) {
+    const int lds = static_cast<int>(small_lds(padded(rows), padded(cols)));
+#define GS_SMALL(A)                                                                                                  \
+    if (padded(rows) == A * kPanel) {                                                                                \
+        if (lds + 1024 > 65536)                                                                                      \
+            GS_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(ortho_small_kernel<T, A>),                 \
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds));                  \
+        hipLaunchKernelGGL((ortho_small_kernel<T, A>), dim3(static_cast<unsigned>(batch)), dim3(kSmallThreads), lds, \
+                           stream, static_cast<const T *>(update), static_cast<int>(rows), static_cast<int>(cols),   \
+                           tall ? 1 : 0, steps, full_steps<T>(), a, b, c, eps, static_cast<T *>(out));               \
+    }
+    GS_SMALL(1)
+    GS_SMALL(2)
+    GS_SMALL(3)
+    GS_SMALL(4)
+#undef GS_SMALL
+    GS_LAUNCH_TRY("ortho_small_kernel");
+    return ok();
+}
+
+template <typename T>
 gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps, float a, float b, float c, float eps,
               void *out, void *workspace, hipStream_t stream) {
-    const Layout l = lay_out(workspace, batch, m, n);
     const bool tall = m > n;
+    if (is_small(padded(tall ? n : m), padded(tall ? m : n)))
+        return run_small<T>(update, batch, tall ? n : m, tall ? m : n, tall, steps, a, b, c, eps, out, stream);
+    const Layout l = lay_out(workspace, batch, m, n);
     const int M = static_cast<int>(padded(tall ? n : m)), N = static_cast<int>(padded(tall ? m : n));
     const int pm = static_cast<int>(padded(m)), pn = static_cast<int>(padded(n));
     const unsigned z = static_cast<unsigned>(batch);
@@ -499,7 +794,7 @@ using namespace gs;
 extern "C" size_t gs_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n) {
     if (m < 1 || n < 1 || m > 65536 || n > 65536 || batch < 1 || batch > 65535 || batch * m * n >= (int64_t(1) << 40))
         return 0;
-    return lay_out(nullptr, batch, m, n).bytes;
+    return is_small(padded(m < n ? m : n), padded(m < n ? n : m)) ? 0 : lay_out(nullptr, batch, m, n).bytes;
 }
 
 extern "C" gs_status gs_orthogonalize(const void *update, int64_t batch, int64_t m, int64_t n, int steps, float a,
@@ -513,7 +808,7 @@ extern "C" gs_status gs_orthogonalize(const void *update, int64_t batch, int64_t
     if (batch == 0) return ok();
     if (!update || !out) return fail(GS_ERR_INVALID_ARG, "gs_orthogonalize: a required pointer is NULL");
     const size_t need = gs_orthogonalize_workspace_bytes(batch, m, n);
-    if (!workspace || workspace_bytes < need)
+    if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(GS_ERR_WORKSPACE, "gs_orthogonalize: need %zu workspace bytes, got %zu", need,
                     workspace ? workspace_bytes : 0);
     hipStream_t stream = static_cast<hipStream_t>(stream_handle);
