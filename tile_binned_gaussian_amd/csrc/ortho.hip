@@ -358,38 +358,39 @@ __global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, int m,
 // ------------------------------------------------------------------------------------------------------------
 // small matrices: one workgroup a matrix, all steps in one launch
 //
-// Wave w owns the 32 columns of X of blocks w, w + 8, ...: all of their rows, in float32 registers in the order in
-// which the matrix cores leave a result (lane: column lane % 32; register 4 g + k: row 8 g + lane / 32 * 4 + k of
-// each 32). X goes to LDS once a step, as pairs of float16, for the Gram product; the step's matrix comes back
-// through LDS to every wave, which multiplies it with its own columns straight from its registers. That works because
-// a product may take its 16 columns in any order, as long as both operands take the same: all LDS blocks here hold
-// their columns in the order 0-3, 8-11 (lanes 0-31), 4-7, 12-15 (lanes 32-63), which is the registers' own.
+// The 32 x 32 tiles of X are dealt to 16 waves, which keep theirs in float32 registers as the matrix cores leave a
+// result (lane: column lane % 32; register 4 g + k: row 8 g + lane / 32 * 4 + k). Once a step every wave puts its
+// tiles' halves into LDS, columns as rows: so a lane's four values lie together, the last product reads its operand in
+// one piece, and the Gram product, which needs the other order, reads it through LDS's transposing load. A product may
+// take its 16 columns in any order as long as both operands take the same: LDS blocks here hold them in the
+// registers' order, 0-3, 8-11 (lanes 0-31), 4-7, 12-15 (lanes 32-63).
 
-constexpr int kSmallThreads = 512;
+constexpr int kSmallThreads = 1024;
 constexpr int kSmallWaves = kSmallThreads / kWave;
+constexpr int kSmallTurns = 2;  // tiles of X a wave holds, at most
 constexpr int kSmallLds = 159 * 1024;
 
-// Column blocks of a wave, at most, where the matrix has 32 A rows: what the LDS allows.
-template <int A>
-constexpr int small_blocks() {
-    return A == 1 ? 5 : A == 2 ? 3 : A == 3 ? 2 : 1;
-}
+// Parts of a Gram tile's sum, so that most waves have one.
+constexpr int small_parts(int a) { return a == 1 || a == 2 ? 4 : a == 3 ? 2 : 1; }
+constexpr int small_triangle(int a) { return a * (a + 1) / 2; }
 
-// Bytes of LDS: both halves of X [32 A][cols] and of a square matrix [32 A][32 A].
-inline int64_t small_lds(int64_t rows, int64_t cols) { return 4 * (rows * cols + rows * rows); }
+// Bytes of LDS: both halves of X [32 a][cols] and of a square matrix [32 a][32 a], and the Gram tiles' parts.
+inline int64_t small_lds(int64_t rows, int64_t cols) {
+    const int a = static_cast<int>(rows / kPanel);
+    return 4 * (rows * cols + rows * rows) + (small_parts(a) - 1) * small_triangle(a) * 4096;
+}
 inline bool is_small(int64_t rows, int64_t cols) {
-    if (rows > 128 || small_lds(rows, cols) > kSmallLds) return false;
-    const int64_t a = rows / kPanel;
-    return cols / kPanel <= kSmallWaves * (a == 1 ? 5 : a == 2 ? 3 : a == 3 ? 2 : 1);
+    return rows <= 128 && rows / kPanel * (cols / kPanel) <= kSmallTurns * kSmallWaves &&
+           small_lds(rows, cols) <= kSmallLds;
 }
 
 // Stores this lane's four values (rows g * 8 + lane / 32 * 4 + 0..3 of row block i, one column of column block j) as
-// columns of the other matrix: [columns of the result][rows of the result].
+// columns: [columns of the tile][rows of the tile].
 __device__ __forceinline__ void small_store_turned(_Float16 *plane, int panels, int i, int j, int g, int lane,
                                                    h16x4 v) {
     *reinterpret_cast<h16x4 *>(plane + ((i * 2 + g / 2) * panels + j) * kBlock + lane * 8 + g % 2 * 4) = v;
 }
-// The same values after a quad transpose, as [rows of the result][columns of the result].
+// The same values as [rows of the tile][columns of the tile].
 __device__ __forceinline__ void small_store_straight(_Float16 *plane, int panels, int i, int j, int g, int lane,
                                                      h16x4 v) {
     const int row = g * 8 + lane / 32 * 4 + lane % 4;
@@ -397,68 +398,84 @@ __device__ __forceinline__ void small_store_straight(_Float16 *plane, int panels
                                (lane / 4 % 2 * kPanel + row) * 8 + lane / 8 % 2 * 4) = quad_transpose(v);
 }
 
-// out += P Q^T over `blocks` blocks of 16 columns, row blocks i and j of planes with `panels` row blocks.
-template <int PRODUCTS>
-__device__ __forceinline__ f32x16 small_product(const _Float16 *hi, const _Float16 *lo, int panels, int i, int j,
-                                                int blocks, int lane) {
-    f32x16 acc[3] = {};
-#pragma unroll 2
-    for (int k = 0; k < blocks; ++k) {
-        const int pi = (k * panels + i) * kBlock + lane * 8, pj = (k * panels + j) * kBlock + lane * 8;
-        const h16x8 ph = *reinterpret_cast<const h16x8 *>(hi + pi), qh = *reinterpret_cast<const h16x8 *>(hi + pj);
-        if constexpr (PRODUCTS == 3) {
-            const h16x8 pl = *reinterpret_cast<const h16x8 *>(lo + pi), ql = *reinterpret_cast<const h16x8 *>(lo + pj);
-            acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, acc[0], 0, 0, 0);
-            acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, acc[1], 0, 0, 0);
-        }
-        acc[2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc[2], 0, 0, 0);
-    }
-    if constexpr (PRODUCTS == 3)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[2][e] += acc[0][e] + acc[1][e];
-    return acc[2];
+// An operand as it lies in LDS: row block `panel` of a plane, its block k of 16 columns.
+__device__ __forceinline__ h16x8 small_operand(const _Float16 *plane, int panels, int panel, int k, int lane) {
+    return *reinterpret_cast<const h16x8 *>(plane + (k * panels + panel) * kBlock + lane * 8);
 }
 
-template <int A>
-struct SmallMatrix {
-    f32x16 x[small_blocks<A>()][A];
-};
+// An operand across the order in LDS: the rows are the 32 columns of row block i of X, the columns 16 of its columns
+// (half k % 2 of column block k / 2). The transposing load gives each of 16 lanes the values that four of them would
+// have read at its place: lane p reads four rows of column p / 4, and gets row p of four columns.
+__device__ __forceinline__ h16x8 small_operand_turned(const _Float16 *plane, int col_blocks, int i, int k, int lane) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 *LdsPtr;
+    const int p = lane % 16, chunk = p % 4;
+    const int col = k % 2 * 16 + lane / 32 * 8 + p / 4;
+    const _Float16 *at = plane + ((i * 2 + lane / 16 % 2) * col_blocks + k / 2) * kBlock +
+                         (chunk % 2 * kPanel + col) * 8 + chunk / 2 * 4;
+    const s16x4 first = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at));
+    const s16x4 second = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at + 4 * 8));
+    const h16x4 f = __builtin_bit_cast(h16x4, first), s = __builtin_bit_cast(h16x4, second);
+    return __builtin_shufflevector(f, s, 0, 1, 2, 3, 4, 5, 6, 7);
+}
 
-// One step on the workgroup's matrix; col_blocks: its blocks of 32 columns.
+template <int PRODUCTS>
+__device__ __forceinline__ f32x16 small_multiply(f32x16 acc, h16x8 ph, h16x8 pl, h16x8 qh, h16x8 ql) {
+    if constexpr (PRODUCTS == 3) {
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, acc, 0, 0, 0);
+    }
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc, 0, 0, 0);
+}
+
+// One step on the workgroup's matrix: x[t] is tile wave + 16 t, row block tile % A, column block tile / A.
 template <int A, int PRODUCTS>
-__device__ __forceinline__ void small_step(SmallMatrix<A> &s, int col_blocks, float a, float b, float c, _Float16 *lds,
-                                           int wave, int lane) {
-    constexpr int kTri = A * (A + 1) / 2, kTurns = (kTri + kSmallWaves - 1) / kSmallWaves;
+__device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blocks, float a, float b, float c,
+                                           _Float16 *lds, int wave, int lane) {
+    constexpr int kTri = small_triangle(A), kParts = small_parts(A);
     _Float16 *xh = lds, *xl = xh + col_blocks * 2 * A * kBlock;
     _Float16 *gh = xl + col_blocks * 2 * A * kBlock, *gl = gh + 2 * A * A * kBlock;
+    float *parts = reinterpret_cast<float *>(gl + 2 * A * A * kBlock);
 #pragma unroll
-    for (int q = 0; q < small_blocks<A>(); ++q) {
-        const int j = wave + q * kSmallWaves;
-        if (j >= col_blocks) break;
-#pragma unroll
-        for (int i = 0; i < A; ++i)
+    for (int t = 0; t < kSmallTurns; ++t) {
+        const int tile = wave + t * kSmallWaves;
+        if (tile < A * col_blocks)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 float v[4];
                 h16x4 h, l;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = s.x[q][i][g * 4 + k];
+                for (int k = 0; k < 4; ++k) v[k] = x[t][g * 4 + k];
                 split<4>(v, h, l);
-                small_store_straight(xh, A, i, j, g, lane, h);
-                if constexpr (PRODUCTS == 3) small_store_straight(xl, A, i, j, g, lane, l);
-                __builtin_amdgcn_sched_barrier(0);
+                small_store_turned(xh, col_blocks, tile % A, tile / A, g, lane, h);
+                if constexpr (PRODUCTS == 3) small_store_turned(xl, col_blocks, tile % A, tile / A, g, lane, l);
             }
     }
     __syncthreads();
-    // the lower triangle's blocks, in turn over the waves
-    f32x16 gram[kTurns];
-    const auto place = [&](int t, int &i, int &j) {
-        const int n = t * kSmallWaves + wave;
-        i = n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0;
-        j = n - i * (i + 1) / 2;
-        return n < kTri;
-    };
-    const auto store = [&](const f32x16 &v16, int i, int j) {
+    // wave n: tile n % kTri of the lower triangle, part n / kTri of its sum
+    const int tri = wave % kTri, part = wave / kTri;
+    const int ti = tri >= 6 ? 3 : tri >= 3 ? 2 : tri >= 1 ? 1 : 0, tj = tri - ti * (ti + 1) / 2;
+    f32x16 gram = {};
+    if (part < kParts) {
+        const int blocks = col_blocks * 2, to = blocks * (part + 1) / kParts;
+#pragma unroll 2
+        for (int k = blocks * part / kParts; k < to; ++k) {
+            const h16x8 ph = small_operand_turned(xh, col_blocks, ti, k, lane);
+            const h16x8 qh = small_operand_turned(xh, col_blocks, tj, k, lane);
+            h16x8 pl = ph, ql = qh;
+            if constexpr (PRODUCTS == 3) {
+                pl = small_operand_turned(xl, col_blocks, ti, k, lane);
+                ql = small_operand_turned(xl, col_blocks, tj, k, lane);
+            }
+            gram = small_multiply<PRODUCTS>(gram, ph, pl, qh, ql);
+        }
+        if (part > 0)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4 *>(parts + (((part - 1) * kTri + tri) * 4 + g) * 256 + lane * 4) =
+                    f32x4{gram[g * 4], gram[g * 4 + 1], gram[g * 4 + 2], gram[g * 4 + 3]};
+    }
+    const auto store = [&](const f32x16 &v16) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             float v[4];
@@ -466,74 +483,64 @@ __device__ __forceinline__ void small_step(SmallMatrix<A> &s, int col_blocks, fl
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = v16[g * 4 + k];
             split<4>(v, h, l);
-            small_store_straight(gh, A, i, j, g, lane, h);
-            if (i != j) small_store_turned(gh, A, i, j, g, lane, h);
+            small_store_turned(gh, A, ti, tj, g, lane, h);
+            if (ti != tj) small_store_straight(gh, A, ti, tj, g, lane, h);
             if constexpr (PRODUCTS == 3) {
-                small_store_straight(gl, A, i, j, g, lane, l);
-                if (i != j) small_store_turned(gl, A, i, j, g, lane, l);
+                small_store_turned(gl, A, ti, tj, g, lane, l);
+                if (ti != tj) small_store_straight(gl, A, ti, tj, g, lane, l);
             }
         }
     };
+    if constexpr (kParts > 1) __syncthreads();
+    if (part == 0) {
 #pragma unroll
-    for (int t = 0; t < kTurns; ++t) {
-        int i, j;
-        if (!place(t, i, j)) break;
-        gram[t] = small_product<PRODUCTS>(xh, xl, A, i, j, col_blocks * 2, lane);
+        for (int p = 1; p < kParts; ++p)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) gram[t][e] *= kScaleA / (kScaleX * kScaleX);
-        store(gram[t], i, j);
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(parts + (((p - 1) * kTri + tri) * 4 + g) * 256 +
+                                                                 lane * 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) gram[g * 4 + k] += v[k];
+            }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) gram[e] *= kScaleA / (kScaleX * kScaleX);
+        store(gram);
     }
     __syncthreads();
-#pragma unroll
-    for (int t = 0; t < kTurns; ++t) {
-        int i, j;
-        if (!place(t, i, j)) break;
-        const f32x16 square = small_product<PRODUCTS>(gh, gl, A, i, j, A * 2, lane);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) gram[t][e] = __builtin_fmaf(b, gram[t][e], square[e] * (c / kScaleA));
-    }
-    __syncthreads();  // the step's matrix takes the Gram matrix's place
-#pragma unroll
-    for (int t = 0; t < kTurns; ++t) {
-        int i, j;
-        if (!place(t, i, j)) break;
-        store(gram[t], i, j);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < small_blocks<A>(); ++q) {
-        if (wave + q * kSmallWaves >= col_blocks) break;
-        f32x16 acc[A] = {};
-#pragma unroll
+    if (part == 0) {
+        f32x16 square = {};
+#pragma unroll 2
         for (int k = 0; k < 2 * A; ++k) {
-            float v[8];
-            h16x8 qh, ql;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = s.x[q][k / 2][k % 2 * 8 + e];
-            split<8>(v, qh, ql);
-            h16x8 ph[A], pl[A];
-#pragma unroll
-            for (int i = 0; i < A; ++i) {
-                ph[i] = *reinterpret_cast<const h16x8 *>(gh + (k * A + i) * kBlock + lane * 8);
-                if constexpr (PRODUCTS == 3)
-                    pl[i] = *reinterpret_cast<const h16x8 *>(gl + (k * A + i) * kBlock + lane * 8);
-            }
-            if constexpr (PRODUCTS == 3) {
-#pragma unroll
-                for (int i = 0; i < A; ++i) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[i], qh, acc[i], 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < A; ++i) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], ql, acc[i], 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < A; ++i) acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], qh, acc[i], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);  // hoisted reads of all blocks would not fit the registers
+            const h16x8 ph = small_operand(gh, A, ti, k, lane), qh = small_operand(gh, A, tj, k, lane);
+            h16x8 pl = ph, ql = qh;
+            if constexpr (PRODUCTS == 3) pl = small_operand(gl, A, ti, k, lane), ql = small_operand(gl, A, tj, k, lane);
+            square = small_multiply<PRODUCTS>(square, ph, pl, qh, ql);
         }
 #pragma unroll
-        for (int i = 0; i < A; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                s.x[q][i][e] = __builtin_fmaf(a, s.x[q][i][e], acc[i][e] * (1.0f / kScaleA));
+        for (int e = 0; e < 16; ++e) gram[e] = __builtin_fmaf(b, gram[e], square[e] * (c / kScaleA));
     }
+    __syncthreads();  // the step's matrix takes the Gram matrix's place
+    if (part == 0) store(gram);
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kSmallTurns; ++t) {
+        const int tile = wave + t * kSmallWaves;
+        if (tile < A * col_blocks) {
+            f32x16 acc = {};
+#pragma unroll 2
+            for (int k = 0; k < 2 * A; ++k) {
+                const h16x8 ph = small_operand(gh, A, tile % A, k, lane);
+                const h16x8 qh = small_operand(xh, col_blocks, tile / A, k, lane);
+                h16x8 pl = ph, ql = qh;
+                if constexpr (PRODUCTS == 3)
+                    pl = small_operand(gl, A, tile % A, k, lane), ql = small_operand(xl, col_blocks, tile / A, k, lane);
+                acc = small_multiply<PRODUCTS>(acc, ph, pl, qh, ql);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[t][e] = __builtin_fmaf(a, x[t][e], acc[e] * (1.0f / kScaleA));
+        }
+    }
+    __syncthreads();  // the next step's halves take these columns' place
 }
 
 // Element access through a buffer descriptor: an offset past the end reads 0 and is not written, so the edges of a
@@ -571,29 +578,27 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const T *__r
     const int col_blocks = (cols + kPanel - 1) / kPanel;
     const size_t base = blockIdx.x * (static_cast<size_t>(rows) * cols);
     const int row_step = tall ? 1 : cols, col_step = tall ? rows : 1;
-    // the offset of register e of row block i and column block j for this lane
-    const auto offset = [=](int l, int i, int j, int e) {
-        const int row = i * kPanel + e / 4 * 8 + l / 32 * 4 + e % 4, col = j * kPanel + l % 32;
-        return row < rows && col < cols ? row * row_step + col * col_step : 1 << 28;
+    // the offset of register e of tile t for lane l
+    const auto offset = [=](int l, int t, int e) {
+        const int tile = wave + t * kSmallWaves;
+        const int row = tile % A * kPanel + e / 4 * 8 + l / 32 * 4 + e % 4, col = tile / A * kPanel + l % 32;
+        const int at = row * row_step + col * col_step;
+        return row < rows && col < cols ? at : 1 << 28;
     };
-    SmallMatrix<A> s;
+    f32x16 x[kSmallTurns];
     const Buffer<T> from(update + base, rows * cols);
+#pragma unroll
+    for (int t = 0; t < kSmallTurns; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[t][e] = from.load(offset(lane, t, e));
     double sum = 0.0;
 #pragma unroll
-    for (int q = 0; q < small_blocks<A>(); ++q)
+    for (int t = 0; t < kSmallTurns; ++t)
 #pragma unroll
-        for (int i = 0; i < A; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s.x[q][i][e] = from.load(offset(lane, i, wave + q * kSmallWaves, e));
-#pragma unroll
-    for (int q = 0; q < small_blocks<A>(); ++q)
-#pragma unroll
-        for (int i = 0; i < A; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const double v = static_cast<double>(s.x[q][i][e]);
-                sum = __builtin_fma(v, v, sum);
-            }
+        for (int e = 0; e < 16; ++e) {
+            const double v = static_cast<double>(x[t][e]);
+            sum = __builtin_fma(v, v, sum);
+        }
 #pragma unroll
     for (int d = kWave / 2; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
     if (lane == 0) s_sum[wave] = sum;
@@ -602,28 +607,22 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const T *__r
     for (int w = 0; w < kSmallWaves; ++w) sum += s_sum[w];
     const double scale = static_cast<double>(kScaleX) / (sqrt(sum) + static_cast<double>(eps));
 #pragma unroll
-    for (int q = 0; q < small_blocks<A>(); ++q)
+    for (int t = 0; t < kSmallTurns; ++t)
 #pragma unroll
-        for (int i = 0; i < A; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                s.x[q][i][e] = static_cast<float>(static_cast<double>(s.x[q][i][e]) * scale);
+        for (int e = 0; e < 16; ++e) x[t][e] = static_cast<float>(static_cast<double>(x[t][e]) * scale);
     for (int k = 0; k < steps; ++k) {
         if (steps - k <= full_steps)
-            small_step<A, 3>(s, col_blocks, a, b, c, s_small, wave, lane);
+            small_step<A, 3>(x, col_blocks, a, b, c, s_small, wave, lane);
         else
-            small_step<A, 1>(s, col_blocks, a, b, c, s_small, wave, lane);
+            small_step<A, 1>(x, col_blocks, a, b, c, s_small, wave, lane);
     }
     const Buffer<T> to(out + base, rows * cols);
-    int late = lane;  // offsets formed anew: kept from the loads they would take a register each all along
+    int late = lane;  // offsets formed anew: kept from the loads they would take 32 registers all along
     asm volatile("" : "+v"(late));
 #pragma unroll
-    for (int q = 0; q < small_blocks<A>(); ++q)
+    for (int t = 0; t < kSmallTurns; ++t)
 #pragma unroll
-        for (int i = 0; i < A; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                to.store(offset(late, i, wave + q * kSmallWaves, e), s.x[q][i][e] * (1.0f / kScaleX));
+        for (int e = 0; e < 16; ++e) to.store(offset(late, t, e), x[t][e] * (1.0f / kScaleX));
 }
 
 inline int64_t padded(int64_t v) { return (v + kPanel - 1) / kPanel * kPanel; }
