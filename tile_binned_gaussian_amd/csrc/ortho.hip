@@ -25,7 +25,6 @@ constexpr int kNormBlocks = 512;  // workgroups that share a matrix's norm, at m
 constexpr int kPanel = 32;   // rows of a panel; planes are padded to it with zeros both ways
 constexpr int kDepth = 16;   // columns of a block
 constexpr int kBlock = kPanel * kDepth;  // elements of a block: 1 KB
-constexpr int kStages = 4;
 
 // A plane holds a matrix [rows][depth] as blocks of 32 rows and 16 columns, [depth / 16][rows / 32][512], each in the
 // order in which a wave's lanes hold a matrix-core operand: lane l has row l % 32 and the eight columns from
@@ -181,9 +180,11 @@ __device__ __forceinline__ h16x4 quad_transpose(h16x4 v) {
 // A workgroup of four waves makes a T x T tile, each wave a quarter of it. PRODUCTS = 3: both halves of the operands
 // (high high + high low + low high); 1: the high halves alone. A stage of the LDS ring holds 32 columns of the high
 // halves, or 16 of both; while one is multiplied the next is there already (its first operands are read ahead of the
-// barrier) and two more are on their way.
+// barrier) and the others are on their way: two of up to 32 KB, or six of the smallest tile's 8 KB, which few
+// workgroups have to themselves and whose time is the memory's latency.
 template <int T, int PRODUCTS>
 __global__ __launch_bounds__(kThreads, T <= 128 ? 2 : 1) void ortho_product_kernel(ProductArgs a) {
+    constexpr int kStages = T == 64 ? 8 : 4;
     constexpr int F = T / 64;                   // 32 x 32 results of a wave, each way
     constexpr int kPanels = T / kPanel;
     constexpr int PL = PRODUCTS == 1 ? 1 : 2;   // planes staged
@@ -268,7 +269,7 @@ __global__ __launch_bounds__(kThreads, T <= 128 ? 2 : 1) void ortho_product_kern
     for (; issued < kStages - 1; ++issued)
 #pragma unroll
         for (int i = 0; i < L; ++i) issue(i);
-    wait_and_meet<2 * L>();
+    wait_and_meet<(kStages - 2) * L>();
 #pragma unroll
     for (int r = 0; r < R; ++r) fetch(stage_at(0), 0, 0, r);
     using Zero = std::integral_constant<int, 0>;
@@ -277,7 +278,7 @@ __global__ __launch_bounds__(kThreads, T <= 128 ? 2 : 1) void ortho_product_kern
     for (int i = 0; i < blocks / 2; ++i) {
         // two blocks of 16 columns; depth is a multiple of 32. At each meeting the next stage is there and all waves
         // are done with the one before this, whose place the loads then take.
-        wait_and_meet<L>();
+        wait_and_meet<(kStages - 3) * L>();
         if constexpr (S == 2) {
             multiply(0, stage_at(i), 1, Zero(), Half());
             multiply(1, stage_at(i + 1), 0, Half(), All());
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(kThreads, T <= 128 ? 2 : 1) void ortho_product_kern
         } else {
             multiply(0, stage_at(2 * i + 1), 0, Zero(), All());
             ++issued;
-            wait_and_meet<L>();
+            wait_and_meet<(kStages - 3) * L>();
             multiply(1, stage_at(2 * i + 2), 0, Zero(), All());
             ++issued;
         }
