@@ -177,27 +177,10 @@ __device__ __forceinline__ h16x4 quad_transpose(h16x4 v) {
     return __builtin_bit_cast(h16x4, r);
 }
 
-// A workgroup of four waves makes a T x T tile, each wave a quarter of it. PRODUCTS = 3: both halves of the operands
-// (high high + high low + low high); 1: the high halves alone. A stage of the LDS ring holds 32 columns of the high
-// halves, or 16 of both; while one is multiplied the next is there already (its first operands are read ahead of the
-// barrier) and the others are on their way: two of up to 32 KB, or six of the smallest tile's 8 KB, which few
-// workgroups have to themselves and whose time is the memory's latency.
-template <int T, int PRODUCTS>
-__global__ __launch_bounds__(kThreads, T <= 128 ? 2 : 1) void ortho_product_kernel(ProductArgs a) {
-    constexpr int kStages = T == 64 ? 8 : 4;
-    constexpr int F = T / 64;                   // 32 x 32 results of a wave, each way
-    constexpr int kPanels = T / kPanel;
-    constexpr int PL = PRODUCTS == 1 ? 1 : 2;   // planes staged
-    constexpr int S = PRODUCTS == 1 ? 2 : 1;    // blocks of 16 columns in a stage
-    constexpr int kBlocks = 2 * PL * kPanels * S;
-    constexpr int L = kBlocks / 4;              // blocks a wave loads for a stage
-    constexpr uint32_t kStageBytes = kBlocks * kBlock * sizeof(_Float16);
-    __shared__ __attribute__((aligned(1024))) _Float16 s_ring[kStages * kBlocks * kBlock];
-
-    // tiles in order on each of the 8 dies, whose L2 then holds the panels that neighbours share
+// The workgroup's tile: in order on each of the 8 dies, whose L2 then holds the panels that neighbours share.
+__device__ __forceinline__ void tile_of(const ProductArgs &a, int &ti, int &tj) {
     const int tiles = gridDim.x, die = blockIdx.x % 8;
     const int t = die * (tiles / 8) + (die < tiles % 8 ? die : tiles % 8) + blockIdx.x / 8;
-    int ti, tj;
     if (a.symmetric) {
         ti = static_cast<int>((sqrtf(8.0f * static_cast<float>(t) + 1.0f) - 1.0f) * 0.5f);
         while (ti * (ti + 1) / 2 > t) --ti;
@@ -209,6 +192,68 @@ __global__ __launch_bounds__(kThreads, T <= 128 ? 2 : 1) void ortho_product_kern
         ti = band * 4 + in % height;
         tj = in / height;
     }
+}
+
+// What the epilogue adds to four sums of this lane: both halves.
+struct Four {
+    h16x4 hi, lo;
+};
+
+// Where a lane's four sums lie in `turned` and `add`: rows g * 8 + lane / 32 * 4 + 0..3 of row panel mp, column lane % 32
+// of column panel np.
+__device__ __forceinline__ size_t four_at(const ProductArgs &a, size_t batch, int mp, int np, int g, int lane) {
+    return batch * (static_cast<size_t>(a.rows) * a.cols) + block_at(np, mp * 2 + g / 2, a.cols) +
+           (g % 2 * kPanel + lane % 32) * 8 + lane / 32 * 4;
+}
+
+__device__ __forceinline__ Four load_four(const ProductArgs &a, size_t at) {
+    Four f = {};
+    if (a.add.hi) {
+        f.hi = *reinterpret_cast<const h16x4 *>(a.add.hi + at);
+        f.lo = *reinterpret_cast<const h16x4 *>(a.add.lo + at);
+    }
+    return f;
+}
+
+// Four sums on their way out. both: to `turned` too.
+__device__ __forceinline__ void finish_four(const ProductArgs &a, size_t batch, int mp, int np, int g, float *v,
+                                            const Four &add, int lane, bool both) {
+    const size_t at = four_at(a, batch, mp, np, g, lane);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        v[k] = __builtin_fmaf(a.scale_add, static_cast<float>(add.hi[k]) + static_cast<float>(add.lo[k]),
+                              v[k] * a.scale_acc);
+    h16x4 h, l;
+    split<4>(v, h, l);
+    if (both) {
+        *reinterpret_cast<h16x4 *>(a.turned.hi + at) = h;
+        if (a.turned.lo) *reinterpret_cast<h16x4 *>(a.turned.lo + at) = l;
+    }
+    // after the transpose this lane: row g * 8 + lane / 32 * 4 + lane % 4, columns from lane % 32 / 4 * 4
+    const size_t to = batch * (static_cast<size_t>(a.rows) * a.cols) + block_at(mp, np * 2 + lane % 32 / 16, a.rows) +
+                      (lane % 16 / 8 * kPanel + g * 8 + lane / 32 * 4 + lane % 4) * 8 + lane % 8 / 4 * 4;
+    *reinterpret_cast<h16x4 *>(a.straight.hi + to) = quad_transpose(h);
+    if (a.straight.lo) *reinterpret_cast<h16x4 *>(a.straight.lo + to) = quad_transpose(l);
+}
+
+// A workgroup of four waves makes a T x T tile, each wave a quarter of it. PRODUCTS = 3: both halves of the operands
+// (high high + high low + low high); 1: the high halves alone. A stage of the LDS ring holds 32 columns of the high
+// halves, or 16 of both; while one is multiplied the next is there already (its first operands are read ahead of the
+// barrier) and the others are on their way: two of up to 32 KB, or six of the smallest tile's 8 KB, which few
+// workgroups have to themselves and whose time is the memory's latency.
+template <int T, int PRODUCTS, int kStages>
+__global__ __launch_bounds__(kThreads, T <= 128 && kStages == 4 ? 2 : 1) void ortho_product_kernel(ProductArgs a) {
+    constexpr int F = T / 64;                   // 32 x 32 results of a wave, each way
+    constexpr int kPanels = T / kPanel;
+    constexpr int PL = PRODUCTS == 1 ? 1 : 2;   // planes staged
+    constexpr int S = PRODUCTS == 1 ? 2 : 1;    // blocks of 16 columns in a stage
+    constexpr int kBlocks = 2 * PL * kPanels * S;
+    constexpr int L = kBlocks / 4;              // blocks a wave loads for a stage
+    constexpr uint32_t kStageBytes = kBlocks * kBlock * sizeof(_Float16);
+    __shared__ __attribute__((aligned(1024))) _Float16 s_ring[kStages * kBlocks * kBlock];
+
+    int ti, tj;
+    tile_of(a, ti, tj);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
     const size_t batch = blockIdx.y;
     const int row_panels = a.rows / kPanel, col_panels = a.cols / kPanel, blocks = a.depth / kDepth;
@@ -294,43 +339,132 @@ __global__ __launch_bounds__(kThreads, T <= 128 ? 2 : 1) void ortho_product_kern
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     const bool both = !a.symmetric || ti != tj;  // a tile on the diagonal is its own mirror
-    const size_t out_plane = batch * (static_cast<size_t>(a.rows) * a.cols);
 #pragma unroll
     for (int i = 0; i < F; ++i) {
         const int mp = ti * kPanels + wr * F + i;
         if (mp >= row_panels) continue;
+        // a row of results' additions before its first store: one wait for memory, not one for every four values
+        Four add[F][4];
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const int np = tj * kPanels + wc * F + j;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                add[j][g] = load_four(a, four_at(a, batch, mp, np < col_panels ? np : col_panels - 1, g, lane));
+        }
 #pragma unroll
         for (int j = 0; j < F; ++j) {
             const int np = tj * kPanels + wc * F + j;
             if (np >= col_panels) continue;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                // this lane: column lane % 32, rows g * 8 + lane / 32 * 4 + 0..3
-                const size_t at = out_plane + block_at(np, mp * 2 + g / 2, a.cols) +
-                                  (g % 2 * kPanel + lane % 32) * 8 + lane / 32 * 4;
                 float v[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = acc[i][j][g * 4 + k] * a.scale_acc;
-                if (a.add.hi) {
-                    const h16x4 h = *reinterpret_cast<const h16x4 *>(a.add.hi + at);
-                    const h16x4 l = *reinterpret_cast<const h16x4 *>(a.add.lo + at);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k] = __builtin_fmaf(a.scale_add, static_cast<float>(h[k]) + static_cast<float>(l[k]), v[k]);
-                }
-                h16x4 h, l;
-                split<4>(v, h, l);
-                if (both) {
-                    *reinterpret_cast<h16x4 *>(a.turned.hi + at) = h;
-                    if (a.turned.lo) *reinterpret_cast<h16x4 *>(a.turned.lo + at) = l;
-                }
-                // after the transpose this lane: row g * 8 + lane / 32 * 4 + lane % 4, columns from lane % 32 / 4 * 4
-                const size_t to = out_plane + block_at(mp, np * 2 + lane % 32 / 16, a.rows) +
-                                  (lane % 16 / 8 * kPanel + g * 8 + lane / 32 * 4 + lane % 4) * 8 + lane % 8 / 4 * 4;
-                *reinterpret_cast<h16x4 *>(a.straight.hi + to) = quad_transpose(h);
-                if (a.straight.lo) *reinterpret_cast<h16x4 *>(a.straight.lo + to) = quad_transpose(l);
+                for (int k = 0; k < 4; ++k) v[k] = acc[i][j][g * 4 + k];
+                finish_four(a, batch, mp, np, g, v, add[j][g], lane, both);
             }
         }
+    }
+}
+
+// A 64 x 64 tile by WAVES waves that share its sum: each takes its own range of the columns, for the whole tile, with
+// operands straight from memory into registers, whose order a block has. No wave waits for another until the sums
+// are joined through LDS, in order, so the time of a few tiles is not the latency of a barrier at every stage.
+template <int PRODUCTS, int WAVES>
+__global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(ProductArgs a) {
+    constexpr int kTile = 64, kPanels = kTile / kPanel;
+    constexpr int PL = PRODUCTS == 1 ? 1 : 2;
+    __shared__ f32x4 s_sum[WAVES][kPanels * 4][kWave];
+    int ti, tj;
+    tile_of(a, ti, tj);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+    const size_t batch = blockIdx.y;
+    const int row_panels = a.rows / kPanel, col_panels = a.cols / kPanel, blocks = a.depth / kDepth;
+    const int from = blocks * wave / WAVES, to = blocks * (wave + 1) / WAVES;
+    const _Float16 *src[2][PL][kPanels];
+#pragma unroll
+    for (int op = 0; op < 2; ++op)
+#pragma unroll
+        for (int plane = 0; plane < PL; ++plane)
+#pragma unroll
+            for (int f = 0; f < kPanels; ++f) {
+                const Planes &p = op ? a.q : a.p;
+                const int rows = op ? a.cols : a.rows, last = rows / kPanel - 1;
+                const int panel = (op ? tj : ti) * kPanels + f;  // past the edge the last one, not stored
+                src[op][plane][f] = (plane ? p.lo : p.hi) + batch * (static_cast<size_t>(rows) * a.depth) +
+                                    block_at(panel < last ? panel : last, from, rows) + lane * 8;
+            }
+    f32x16 acc[kPanels][kPanels] = {};
+    // a ring of registers: the loads of kAhead blocks are on their way while one is multiplied
+    constexpr int kAhead = 3, kRing = kAhead + 1;
+    h16x8 ring[kRing][2][PL][kPanels];
+    int loaded = from;
+    const auto load = [&](int slot) {
+#pragma unroll
+        for (int op = 0; op < 2; ++op)
+#pragma unroll
+            for (int plane = 0; plane < PL; ++plane)
+#pragma unroll
+                for (int f = 0; f < kPanels; ++f) {
+                    ring[slot][op][plane][f] = *reinterpret_cast<const h16x8 *>(src[op][plane][f]);
+                    // past the end the last block is loaded again, unused
+                    if (loaded + 1 < to) src[op][plane][f] += static_cast<size_t>(op ? col_panels : row_panels) * kBlock;
+                }
+        ++loaded;
+    };
+    const auto multiply = [&](int slot) {
+#pragma unroll
+        for (int term = PRODUCTS == 1 ? 2 : 0; term < 3; ++term)
+#pragma unroll
+            for (int i = 0; i < kPanels; ++i)
+#pragma unroll
+                for (int j = 0; j < kPanels; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[slot][0][term == 0 ? PL - 1 : 0][i],
+                                                                       ring[slot][1][term == 1 ? PL - 1 : 0][j],
+                                                                       acc[i][j], 0, 0, 0);
+    };
+    if (from < to) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) load(d);
+        int k = from;
+        for (; k + kRing <= to; k += kRing) {
+#pragma unroll
+            for (int d = 0; d < kRing; ++d) {
+                load((d + kAhead) % kRing);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(d);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d)
+            if (k + d < to) multiply(d);
+    }
+    const bool both = !a.symmetric || ti != tj;
+    Four add[kPanels];
+#pragma unroll
+    for (int i = 0; i < kPanels; ++i) {
+        const int mp = ti * kPanels + i, np = tj * kPanels + wave / 4;
+        add[i] = load_four(a, four_at(a, batch, mp < row_panels ? mp : row_panels - 1,
+                                      np < col_panels ? np : col_panels - 1, wave % 4, lane));
+    }
+#pragma unroll
+    for (int i = 0; i < kPanels; ++i) {
+        if (i > 0) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kPanels; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                s_sum[wave][j * 4 + g][lane] = f32x4{acc[i][j][g * 4], acc[i][j][g * 4 + 1], acc[i][j][g * 4 + 2],
+                                                     acc[i][j][g * 4 + 3]};
+        __syncthreads();
+        static_assert(WAVES == kPanels * 4, "a wave finishes one group of four rows of each panel");
+        f32x4 sum = s_sum[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) sum += s_sum[w][wave][lane];
+        float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+        const int mp = ti * kPanels + i, np = tj * kPanels + wave / 4;
+        if (mp < row_panels && np < col_panels) finish_four(a, batch, mp, np, wave % 4, v, add[i], lane, both);
     }
 }
 
@@ -696,11 +830,22 @@ gs_status product(ProductArgs g, int64_t batch, int products, hipStream_t stream
                     static_cast<unsigned>(batch));
 #define GS_PRODUCT(T, P)                                                                                  \
     if (edge == T && products == P)                                                                       \
-    hipLaunchKernelGGL((ortho_product_kernel<T, P>), grid, dim3(kThreads), 0, stream, g)
-    GS_PRODUCT(64, 1);
-    GS_PRODUCT(64, 3);
-    GS_PRODUCT(128, 1);
-    GS_PRODUCT(128, 3);
+    hipLaunchKernelGGL((ortho_product_kernel<T, P, 4>), grid, dim3(kThreads), 0, stream, g)
+    if (edge == 64 && products == 1)
+        hipLaunchKernelGGL((ortho_product_direct_kernel<1, 8>), grid, dim3(8 * kWave), 0, stream, g);
+    if (edge == 64 && products == 3)
+        hipLaunchKernelGGL((ortho_product_direct_kernel<3, 8>), grid, dim3(8 * kWave), 0, stream, g);
+    const bool alone = static_cast<int64_t>(grid.x) * batch <= kUnits;
+    if (edge == 128 && alone) {
+        if (products == 1)
+            hipLaunchKernelGGL((ortho_product_kernel<128, 1, 8>), grid, dim3(kThreads), 0, stream, g);
+        else
+            hipLaunchKernelGGL((ortho_product_kernel<128, 3, 8>), grid, dim3(kThreads), 0, stream, g);
+    }
+    if (!alone) {
+        GS_PRODUCT(128, 1);
+        GS_PRODUCT(128, 3);
+    }
     GS_PRODUCT(192, 1);
     GS_PRODUCT(192, 3);
     GS_PRODUCT(256, 1);
