@@ -34,7 +34,8 @@ def check(u, got, **kw):
 
 @pytest.mark.parametrize("name", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("m,n", [(1, 1), (1, 50), (7, 3), (32, 32), (63, 65), (64, 64), (96, 160), (129, 128),
-                                 (160, 96), (200, 513), (300, 1000), (777, 333), (640, 640), (1025, 130), (33, 4000)])
+                                 (160, 96), (200, 513), (300, 1000), (777, 333), (640, 640), (1025, 130), (33, 4000),
+                                 (780, 900)])
 def test_one_matrix(m, n, name):
     u = momentum((m, n), tu.DTYPES[name], m + n)
     check(u, binding.gs_orthogonalize(u.cuda()))

@@ -153,16 +153,22 @@ def expert_combine_grad(source, rows, weights, grad_y):
 # orthogonalised update
 
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
-#: The last steps, whose products take both halves of the operands (22 bits); before them a result of a type with
-#: fewer bits takes the high halves alone (11 bits).
-FULL_STEPS = {torch.float32: 100, torch.float16: 3, torch.bfloat16: 2}
+
+
+def operand_bits(dtype, rows, left):
+    """Bits that a step's three products keep of their operands (the Gram product, its square, the product with X):
+    both halves, 22, or the high halves, 11. rows: of the smaller side; left: steps left, this one among them."""
+    if dtype == torch.float32 or rows <= 736:  # padded to 32, below 768
+        return 22, 22, 22
+    if left > (3 if dtype == torch.float16 else 2):
+        return 11, 11, 11
+    return (22, 22, 22) if dtype == torch.float16 else (11, 22, 22)
 
 
 def orthogonalize(update, steps=5, coefficients=COEFFICIENTS, eps=1e-7, noise=None):
     """The result for one matrix in 64 bits; with noise (a generator) the same with every rounding that the kernels
     make replaced by a random one of its size."""
     a, b, c = coefficients
-    full = FULL_STEPS[update.dtype]
     x = update.double()
     x = x / (x.norm() + eps)
     tall = x.shape[0] > x.shape[1]
@@ -184,10 +190,10 @@ def orthogonalize(update, steps=5, coefficients=COEFFICIENTS, eps=1e-7, noise=No
 
     x = near(x, 2.0 ** -22)
     for s in range(steps):
-        bits = 22 if steps - s <= full else 11
-        A = near(product(x, x.T.contiguous(), bits), 2.0 ** -22)
-        B = near(b * A + c * product(A, A, bits), 2.0 ** -22)
-        x = near(a * x + product(B, x, bits), 2.0 ** -22)
+        gram, square, apply = operand_bits(update.dtype, min(x.shape), steps - s)
+        A = near(product(x, x.T.contiguous(), gram), 2.0 ** -22)
+        B = near(b * A + c * product(A, A, square), 2.0 ** -22)
+        x = near(a * x + product(B, x, apply), 2.0 ** -22)
     return x.T.contiguous() if tall else x
 
 

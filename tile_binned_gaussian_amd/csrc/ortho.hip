@@ -554,17 +554,14 @@ __device__ __forceinline__ h16x8 small_operand_turned(const _Float16 *plane, int
     return __builtin_shufflevector(f, s, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int PRODUCTS>
 __device__ __forceinline__ f32x16 small_multiply(f32x16 acc, h16x8 ph, h16x8 pl, h16x8 qh, h16x8 ql) {
-    if constexpr (PRODUCTS == 3) {
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, acc, 0, 0, 0);
-    }
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, acc, 0, 0, 0);
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc, 0, 0, 0);
 }
 
 // One step on the workgroup's matrix: x[t] is tile wave + 16 t, row block tile % A, column block tile / A.
-template <int A, int PRODUCTS>
+template <int A>
 __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blocks, float a, float b, float c,
                                            _Float16 *lds, int wave, int lane) {
     constexpr int kTri = small_triangle(A), kParts = small_parts(A);
@@ -583,7 +580,7 @@ __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blo
                 for (int k = 0; k < 4; ++k) v[k] = x[t][g * 4 + k];
                 split<4>(v, h, l);
                 small_store_turned(xh, col_blocks, tile % A, tile / A, g, lane, h);
-                if constexpr (PRODUCTS == 3) small_store_turned(xl, col_blocks, tile % A, tile / A, g, lane, l);
+                small_store_turned(xl, col_blocks, tile % A, tile / A, g, lane, l);
             }
     }
     __syncthreads();
@@ -597,12 +594,9 @@ __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blo
         for (int k = blocks * part / kParts; k < to; ++k) {
             const h16x8 ph = small_operand_turned(xh, col_blocks, ti, k, lane);
             const h16x8 qh = small_operand_turned(xh, col_blocks, tj, k, lane);
-            h16x8 pl = ph, ql = qh;
-            if constexpr (PRODUCTS == 3) {
-                pl = small_operand_turned(xl, col_blocks, ti, k, lane);
-                ql = small_operand_turned(xl, col_blocks, tj, k, lane);
-            }
-            gram = small_multiply<PRODUCTS>(gram, ph, pl, qh, ql);
+            const h16x8 pl = small_operand_turned(xl, col_blocks, ti, k, lane);
+            const h16x8 ql = small_operand_turned(xl, col_blocks, tj, k, lane);
+            gram = small_multiply(gram, ph, pl, qh, ql);
         }
         if (part > 0)
 #pragma unroll
@@ -619,10 +613,10 @@ __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blo
             for (int k = 0; k < 4; ++k) v[k] = v16[g * 4 + k];
             split<4>(v, h, l);
             small_store_turned(gh, A, ti, tj, g, lane, h);
-            if (ti != tj) small_store_straight(gh, A, ti, tj, g, lane, h);
-            if constexpr (PRODUCTS == 3) {
-                small_store_turned(gl, A, ti, tj, g, lane, l);
-                if (ti != tj) small_store_straight(gl, A, ti, tj, g, lane, l);
+            small_store_turned(gl, A, ti, tj, g, lane, l);
+            if (ti != tj) {
+                small_store_straight(gh, A, ti, tj, g, lane, h);
+                small_store_straight(gl, A, ti, tj, g, lane, l);
             }
         }
     };
@@ -647,9 +641,8 @@ __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blo
 #pragma unroll 2
         for (int k = 0; k < 2 * A; ++k) {
             const h16x8 ph = small_operand(gh, A, ti, k, lane), qh = small_operand(gh, A, tj, k, lane);
-            h16x8 pl = ph, ql = qh;
-            if constexpr (PRODUCTS == 3) pl = small_operand(gl, A, ti, k, lane), ql = small_operand(gl, A, tj, k, lane);
-            square = small_multiply<PRODUCTS>(square, ph, pl, qh, ql);
+            const h16x8 pl = small_operand(gl, A, ti, k, lane), ql = small_operand(gl, A, tj, k, lane);
+            square = small_multiply(square, ph, pl, qh, ql);
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) gram[e] = __builtin_fmaf(b, gram[e], square[e] * (c / kScaleA));
@@ -666,10 +659,9 @@ __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blo
             for (int k = 0; k < 2 * A; ++k) {
                 const h16x8 ph = small_operand(gh, A, tile % A, k, lane);
                 const h16x8 qh = small_operand(xh, col_blocks, tile / A, k, lane);
-                h16x8 pl = ph, ql = qh;
-                if constexpr (PRODUCTS == 3)
-                    pl = small_operand(gl, A, tile % A, k, lane), ql = small_operand(xl, col_blocks, tile / A, k, lane);
-                acc = small_multiply<PRODUCTS>(acc, ph, pl, qh, ql);
+                const h16x8 pl = small_operand(gl, A, tile % A, k, lane);
+                const h16x8 ql = small_operand(xl, col_blocks, tile / A, k, lane);
+                acc = small_multiply(acc, ph, pl, qh, ql);
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[t][e] = __builtin_fmaf(a, x[t][e], acc[e] * (1.0f / kScaleA));
@@ -705,8 +697,8 @@ struct Buffer {
 // rows <= cols: the matrix as the steps see it, transposed from the update where tall.
 template <typename T, int A>
 __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const T *__restrict__ update, int rows, int cols,
-                                                                    int tall, int steps, int full_steps, float a,
-                                                                    float b, float c, float eps, T *__restrict__ out) {
+                                                                    int tall, int steps, float a, float b, float c,
+                                                                    float eps, T *__restrict__ out) {
     extern __shared__ __attribute__((aligned(16))) _Float16 s_small[];
     __shared__ double s_sum[kSmallWaves];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
@@ -745,12 +737,7 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const T *__r
     for (int t = 0; t < kSmallTurns; ++t)
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[t][e] = static_cast<float>(static_cast<double>(x[t][e]) * scale);
-    for (int k = 0; k < steps; ++k) {
-        if (steps - k <= full_steps)
-            small_step<A, 3>(x, col_blocks, a, b, c, s_small, wave, lane);
-        else
-            small_step<A, 1>(x, col_blocks, a, b, c, s_small, wave, lane);
-    }
+    for (int k = 0; k < steps; ++k) small_step<A>(x, col_blocks, a, b, c, s_small, wave, lane);
     const Buffer<T> to(out + base, rows * cols);
     int late = lane;  // offsets formed anew: kept from the loads they would take 32 registers all along
     asm volatile("" : "+v"(late));
@@ -855,15 +842,25 @@ gs_status product(ProductArgs g, int64_t batch, int products, hipStream_t stream
     return GS_OK;
 }
 
-// The last steps, whose products take both halves of the operands. The earlier ones of a result with fewer than 24
-// bits take the high halves: 2^-12 of an operand is less than the update's own rounding (equal to it for float16),
-// and a step damps the error that reaches it, so what the last steps add counts most. Measured against 64 bits on
-// momentum-like matrices of 32 to 2000 rows (2-norm, next to the result's own rounding): bfloat16 with two full steps
-// of five 1.00 to 1.14 times that rounding, float16 with three 1.00 to 1.12 (with two up to 4.8). X itself, A in b A,
-// and the sums keep both halves throughout.
+// What a step's products take of their operands, 3: both halves, 1: the high halves.
+struct StepProducts {
+    int gram, poly, apply;
+};
+
+// Both halves, but for large matrices of a type with fewer than 24 bits. There the earlier steps take the high halves:
+// 2^-12 of an operand is less than the update's own rounding (equal to it for float16), its errors average out over
+// many rows, and most of what an early step adds is damped by the later ones. X, A in b A and all sums keep both
+// halves. The 2-norm of the error against 64 bits, next to that of the result's own rounding, on momentum-like,
+// Gaussian, decaying and orthonormal matrices of 800 and 1200 rows: bfloat16 1.02 to 1.08, float16 1.00; with one more
+// high step float16 had up to 1.5, and below 768 rows some of these matrices up to 1.5 (512 rows) and 3.4 (33 rows),
+// where these steps cost least. On 4096 x 4096 bfloat16 they take 0.37 of the time of full ones.
+constexpr int kHighRows = 768;
+
 template <typename T>
-constexpr int full_steps() {
-    return std::is_same<T, float>::value ? 1 << 30 : std::is_same<T, _Float16>::value ? 3 : 2;
+StepProducts step_products(int rows, int left) {  // left: steps that are left, this one among them
+    if (std::is_same<T, float>::value || rows < kHighRows) return {3, 3, 3};
+    if (left > (std::is_same<T, _Float16>::value ? 3 : 2)) return {1, 1, 1};
+    return std::is_same<T, _Float16>::value ? StepProducts{3, 3, 3} : StepProducts{1, 3, 3};
 }
 
 template <typename T>
@@ -877,7 +874,7 @@ gs_status run_small(const void *update, int64_t batch, int64_t rows, int64_t col
                                            hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds));                  \
         hipLaunchKernelGGL((ortho_small_kernel<T, A>), dim3(static_cast<unsigned>(batch)), dim3(kSmallThreads), lds, \
                            stream, static_cast<const T *>(update), static_cast<int>(rows), static_cast<int>(cols),   \
-                           tall ? 1 : 0, steps, full_steps<T>(), a, b, c, eps, static_cast<T *>(out));               \
+                           tall ? 1 : 0, steps, a, b, c, eps, static_cast<T *>(out));                                 \
     }
     GS_SMALL(1)
     GS_SMALL(2)
@@ -910,16 +907,19 @@ gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps
                        tall ? l.xt[at] : l.x, tall ? l.x : l.xt[at]);
     GS_LAUNCH_TRY("ortho_split_kernel");
     for (int s = 0; s < steps; ++s) {
+        const StepProducts now = step_products<T>(M, steps - s);
         // the low parts that nothing reads are not written
-        const int products = steps - s <= full_steps<T>() ? 3 : 1;
-        const Planes poly = products == 3 ? l.poly : Planes{l.poly.hi, nullptr};
-        const Planes next = steps - s - 1 <= full_steps<T>() ? l.x : Planes{l.x.hi, nullptr};
+        const Planes poly = now.apply == 3 ? l.poly : Planes{l.poly.hi, nullptr};
+        const bool last = s == steps - 1;
+        const Planes next =
+            (last ? !tall : step_products<T>(M, steps - s - 1).gram == 3) ? l.x : Planes{l.x.hi, nullptr};
         const ProductArgs ops[3] = {
             {l.x, l.x, {}, l.gram, l.gram, M, M, N, 0, 0, 1, kScaleA / (kScaleX * kScaleX), 0.0f},
             {l.gram, l.gram, l.gram, poly, poly, M, M, M, 0, 0, 1, c / kScaleA, b},
             {l.poly, l.xt[at], l.xt[at], next, l.xt[1 - at], M, N, M, 0, 0, 0, 1.0f / kScaleA, a}};
-        for (const ProductArgs &g : ops) {
-            const gs_status bad = product(g, batch, products, stream);
+        const int products[3] = {now.gram, now.poly, now.apply};
+        for (int i = 0; i < 3; ++i) {
+            const gs_status bad = product(ops[i], batch, products[i], stream);
             if (bad != GS_OK) return bad;
         }
         at = 1 - at;
