@@ -204,28 +204,53 @@ __global__ __launch_bounds__(kRowThreads) void expert_dispatch_kernel(const T *_
     zero_tail<T, V>(sent, pairs, *kept, dim, parts);
 }
 
+// The rows of a token's kept pairs are read four at a time: each lane first takes one pair's row number and weight, and
+// the wave then goes through the kept ones, whose numbers are uniform, so no load waits for another's address.
 template <typename T, int V>
 __global__ __launch_bounds__(kRowThreads) void expert_combine_kernel(const T *__restrict__ source,
                                                                      const int32_t *__restrict__ rows,
                                                                      const float *__restrict__ weights, int64_t tokens,
                                                                      int64_t choices, int64_t dim, int parts,
                                                                      T *__restrict__ y) {
-    constexpr int N = Pack<T>::kN;
+    constexpr int N = Pack<T>::kN, kGroup = 4;
     const int64_t pairs = tokens * choices;
+    const int lane = threadIdx.x % kWave;
     const int64_t wave = static_cast<int64_t>(blockIdx.x) * kRowWaves + threadIdx.x / kWave;
     for (int64_t i = wave; i < tokens * parts; i += static_cast<int64_t>(gridDim.x) * kRowWaves) {
         const RowItem it = row_item<T, V>(i, parts);
         float acc[V][N] = {};
-        for (int64_t k = 0; k < choices; ++k) {
-            const int64_t r = rows[it.token * choices + k];
-            if (r < 0 || r >= pairs) continue;
-            const float w = weights ? weights[it.token * choices + k] : 1.0f;
-            typename Pack<T>::V v[V];
-            load_row<T, V>(source + r * dim, it.col, dim, v);
+        for (int64_t k0 = 0; k0 < choices; k0 += kWave) {
+            int32_t row = -1;
+            float weight = 1.0f;
+            if (k0 + lane < choices) {
+                row = rows[it.token * choices + k0 + lane];
+                if (weights) weight = weights[it.token * choices + k0 + lane];
+            }
+            uint64_t kept = __ballot(row >= 0 && row < pairs);
+            while (kept) {
+                typename Pack<T>::V v[kGroup][V];
+                float w[kGroup];
+                int n = 0;
 #pragma unroll
-            for (int a = 0; a < V; ++a)
+                for (int q = 0; q < kGroup; ++q) {
+                    if (kept == 0) break;
+                    const int k = __builtin_ctzll(kept);
+                    kept &= kept - 1;
+                    const int64_t r = __builtin_amdgcn_readlane(row, k);
+                    w[q] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), k));
+                    load_row<T, V>(source + r * dim, it.col, dim, v[q]);
+                    n = q + 1;
+                }
 #pragma unroll
-                for (int j = 0; j < N; ++j) acc[a][j] = __builtin_fmaf(w, static_cast<float>(v[a][j]), acc[a][j]);
+                for (int q = 0; q < kGroup; ++q) {
+                    if (q >= n) break;
+#pragma unroll
+                    for (int a = 0; a < V; ++a)
+#pragma unroll
+                        for (int j = 0; j < N; ++j)
+                            acc[a][j] = __builtin_fmaf(w[q], static_cast<float>(v[q][a][j]), acc[a][j]);
+                }
+            }
         }
         typename Pack<T>::V o[V];
 #pragma unroll
