@@ -27,6 +27,28 @@ __device__ __forceinline__ typename Pack<T>::V load_pack(const T *__restrict__ r
     return v;
 }
 
+// The same for rows of a pack at least, in two parts. A pack that the row's end cuts, or that lies past it, is read to end
+// with the row, so that every lane's load is the same and none waits; end_pack, where the values are first needed,
+// shifts it to its place. Rows of whole packs (a uniform branch) skip that.
+template <typename T>
+__device__ __forceinline__ typename Pack<T>::V read_pack(const T *__restrict__ row, int col, int dim) {
+    const int last = dim - Pack<T>::kN;
+    return *reinterpret_cast<const typename Pack<T>::VU *>(row + (col < last ? col : last));
+}
+template <typename T>
+__device__ __forceinline__ typename Pack<T>::V end_pack(typename Pack<T>::V v, int col, int dim) {
+    constexpr int N = Pack<T>::kN;
+    if (dim % N != 0) {
+        int past = col - (dim - N);
+        past = past < 0 ? 0 : past > N ? N : past;
+        unsigned __int128 bits = __builtin_bit_cast(unsigned __int128, v);
+        bits = past < N ? bits >> (past * 8 * static_cast<int>(sizeof(T))) : static_cast<unsigned __int128>(0);
+        return __builtin_bit_cast(typename Pack<T>::V, bits);
+    }
+    if (col >= dim) v = static_cast<T>(0.0f);
+    return v;
+}
+
 template <typename T>
 __device__ __forceinline__ void store_pack(T *__restrict__ row, int64_t col, int64_t dim, typename Pack<T>::V v) {
     if (col + Pack<T>::kN <= dim) {
@@ -52,6 +74,22 @@ __device__ __forceinline__ void load_floats(const T *__restrict__ row, int64_t c
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) out[j] = col + j < dim ? static_cast<float>(row[col + j]) : 0.0f;
+    }
+}
+
+// The same for rows of a pack at least.
+template <int N, typename T>
+__device__ __forceinline__ void load_floats_long(const T *__restrict__ row, int col, int dim, float *out) {
+    constexpr int P = Pack<T>::kN;
+    static_assert(N % P == 0, "whole packs");
+    typename Pack<T>::V v[N / P];
+#pragma unroll
+    for (int i = 0; i < N / P; ++i) v[i] = read_pack(row, col + i * P, dim);
+#pragma unroll
+    for (int i = 0; i < N / P; ++i) {
+        v[i] = end_pack<T>(v[i], col + i * P, dim);
+#pragma unroll
+        for (int j = 0; j < P; ++j) out[i * P + j] = static_cast<float>(v[i][j]);
     }
 }
 

@@ -12,9 +12,25 @@ namespace gs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFwdBlocks = 2048;    // 8 workgroups a CU; each visits several rows with its weights in registers
-constexpr int kBwdBlocks = 512;     // 2 a CU: each adds one row of column sums to the workspace
+constexpr int kUnits = 256;           // compute units
+constexpr int kWideFwdBlocks = 2048;
+constexpr int kWideBwdParts = 64;
+constexpr int kBwdBlocks = 768;       // at most: the rows of column sums that the workspace holds
 constexpr int kReduceThreads = 1024;
+
+// Floats of a row of column sums in the workspace: whole packs of 16 bytes and cache lines.
+__host__ __device__ constexpr int64_t partial_width(int64_t dim) { return (dim + 31) / 32 * 32; }
+
+// Threads of a workgroup whose rows have G lanes each.
+constexpr int row_threads(int lanes) { return lanes > kThreads ? lanes : kThreads; }
+
+// Which of the workgroup's rows this thread works on; uniform where a row has whole waves, which keeps row addresses
+// out of the lanes' registers.
+template <int G>
+__device__ __forceinline__ int row_group() {
+    const int g = static_cast<int>(threadIdx.x) / G;
+    return G >= kWave ? __builtin_amdgcn_readfirstlane(g) : g;
+}
 
 // Sum over the G lanes that share a row; slot: LDS words of this sum alone when G spans waves. A row's two sums take
 // different slots, so one barrier between writing and reading a slot is enough.
@@ -33,33 +49,60 @@ __device__ __forceinline__ float row_sum(float v, float *slot) {
     }
 }
 
+// Two sums at once. Rows that follow each other take two slots in turn: then the one barrier is enough.
+template <int G>
+__device__ __forceinline__ void row_sums(float &a, float &b, float2 *slot) {
+    constexpr int kLanes = G < kWave ? G : kWave;
+    a = group_sum<kLanes>(a);
+    b = group_sum<kLanes>(b);
+    if constexpr (G > kWave) {
+        if (threadIdx.x % kWave == 0) slot[threadIdx.x / kWave] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.0f;
+#pragma unroll
+        for (int i = 0; i < G / kWave; ++i) {
+            a += slot[i].x;
+            b += slot[i].y;
+        }
+    }
+}
+
+// Waves of the forward that a SIMD holds at once: 64 registers a wave with up to 8 columns a lane, 80 with 16.
+constexpr int fwd_waves(int columns) { return columns > 8 ? 6 : 8; }
+
 template <typename T, typename W, int G, int V>
-__global__ __launch_bounds__(kThreads) void norm_fwd_kernel(const T *__restrict__ x, const W *__restrict__ weight,
-                                                            const W *__restrict__ bias, int64_t rows, int64_t dim,
+__global__ __launch_bounds__(row_threads(G), fwd_waves(V * Pack<T>::kN)) void norm_fwd_kernel(const T *__restrict__ x, const W *__restrict__ weight,
+                                                            const W *__restrict__ bias, int64_t rows, int dim,
                                                             float eps, T *__restrict__ y, float *__restrict__ mean,
                                                             float *__restrict__ rstd) {
-    constexpr int N = Pack<T>::kN, kRows = kThreads / G;
-    __shared__ float s_sum[2][kThreads / kWave];
+    constexpr int N = Pack<T>::kN, kRows = row_threads(G) / G;
+    __shared__ float s_sum[2][row_threads(G) / kWave];
     const int lane = threadIdx.x % G;
     const float n = static_cast<float>(dim);
     float w[V * N], b[V * N];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int64_t col = (static_cast<int64_t>(v) * G + lane) * N;
-        load_floats<N>(weight, col, dim, w + v * N);
+        const int col = (v * G + lane) * N;
+        load_floats_long<N>(weight, col, dim, w + v * N);
 #pragma unroll
         for (int j = 0; j < N; ++j) b[v * N + j] = 0.0f;
-        if (bias) load_floats<N>(bias, col, dim, b + v * N);
+        if (bias) load_floats_long<N>(bias, col, dim, b + v * N);
     }
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G; r < rows;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + row_group<G>(); r < rows;
          r += static_cast<int64_t>(gridDim.x) * kRows) {
         float c[V * N];
         float s = 0.0f;
+        typename Pack<T>::V p[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) p[v] = read_pack(x + r * dim, (v * G + lane) * N, dim);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            load_floats<N>(x + r * dim, (static_cast<int64_t>(v) * G + lane) * N, dim, c + v * N);
+            p[v] = end_pack<T>(p[v], (v * G + lane) * N, dim);
 #pragma unroll
-            for (int j = 0; j < N; ++j) s += c[v * N + j];
+            for (int j = 0; j < N; ++j) {
+                c[v * N + j] = static_cast<float>(p[v][j]);
+                s += c[v * N + j];
+            }
         }
         const float m = row_sum<G>(s, s_sum[0]) / n;
         float q = 0.0f;
@@ -68,7 +111,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(const T *__restrict_
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 float &e = c[v * N + j];
-                e = (static_cast<int64_t>(v) * G + lane) * N + j < dim ? e - m : 0.0f;
+                e = (v * G + lane) * N + j < dim ? e - m : 0.0f;
                 q = __builtin_fmaf(e, e, q);
             }
         const float rs = 1.0f / sqrtf(row_sum<G>(q, s_sum[1]) / n + eps);
@@ -78,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(const T *__restrict_
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 o[j] = static_cast<T>(__builtin_fmaf(c[v * N + j] * rs, w[v * N + j], b[v * N + j]));
-            store_pack(y + r * dim, (static_cast<int64_t>(v) * G + lane) * N, dim, o);
+            store_pack(y + r * dim, (v * G + lane) * N, dim, o);
         }
         if (mean && lane == 0) {
             mean[r] = m;
@@ -135,57 +178,85 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_wide_kernel(const T *__rest
 }
 
 template <typename T, typename W, int G, int V>
-__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(const T *__restrict__ x, const W *__restrict__ weight,
+__global__ __launch_bounds__(row_threads(G)) void norm_bwd_kernel(const T *__restrict__ x, const W *__restrict__ weight,
                                                             const float *__restrict__ mean,
                                                             const float *__restrict__ rstd,
-                                                            const T *__restrict__ grad_y, int64_t rows, int64_t dim,
+                                                            const T *__restrict__ grad_y, int64_t rows, int dim,
                                                             T *__restrict__ grad_x, float *__restrict__ partial) {
-    constexpr int N = Pack<T>::kN, kRows = kThreads / G;
-    __shared__ float s_sum[2][2][kThreads / kWave];
+    constexpr int N = Pack<T>::kN, kRows = row_threads(G) / G;
+    __shared__ float2 s_sum[2][row_threads(G) / kWave];
     __shared__ float s_cols[kRows > 1 ? kThreads * (N + 1) : 1];
-    const int lane = threadIdx.x % G, group = threadIdx.x / G;
-    const float n = static_cast<float>(dim);
+    const int lane = threadIdx.x % G, group = row_group<G>();
+    const float inverse = 1.0f / static_cast<float>(dim);
     float w[V * N], dw[V * N], db[V * N];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        load_floats<N>(weight, (static_cast<int64_t>(v) * G + lane) * N, dim, w + v * N);
+        load_floats_long<N>(weight, (v * G + lane) * N, dim, w + v * N);
 #pragma unroll
         for (int j = 0; j < N; ++j) dw[v * N + j] = db[v * N + j] = 0.0f;
     }
     int turn = 0;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + group; r < rows;
-         r += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
-        const float m = mean[r], rs = rstd[r];
-        float xh[V * N], g[V * N];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+    int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + group;
+    // the next row is on its way while one is worked on: too few rows are in flight on a CU otherwise
+    typename Pack<T>::V px[V], pg[V];
+    float pm = 0.0f, pr = 0.0f;
+    const auto fetch = [&](int64_t at) {
+        pm = mean[at];
+        pr = rstd[at];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int col = (v * G + lane) * N;
+            px[v] = read_pack(x + at * dim, col, dim);
+            pg[v] = read_pack(grad_y + at * dim, col, dim);
+        }
+    };
+    if (r < rows) fetch(r);
+    for (; r < rows; r += step, turn ^= 1) {
+        const float m = pm, rs = pr;
+        typename Pack<T>::V cx[V], cg[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            cx[v] = end_pack<T>(px[v], (v * G + lane) * N, dim);
+            cg[v] = end_pack<T>(pg[v], (v * G + lane) * N, dim);
+        }
+        if (r + step < rows) fetch(r + step);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int64_t col = (static_cast<int64_t>(v) * G + lane) * N;
-            load_floats<N>(x + r * dim, col, dim, xh + v * N);
-            load_floats<N>(grad_y + r * dim, col, dim, g + v * N);
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int j = v * N; j < v * N + N; ++j) {
-                xh[j] = (xh[j] - m) * rs;
-                dw[j] = __builtin_fmaf(g[j], xh[j], dw[j]);
-                db[j] += g[j];
-                g[j] *= w[j];  // zero past the row's end, as weight and grad_y are
-                s1 += g[j];
-                s2 = __builtin_fmaf(g[j], xh[j], s2);
+            for (int j = 0; j < N; ++j) {
+                const float xh = (static_cast<float>(cx[v][j]) - m) * rs, gy = static_cast<float>(cg[v][j]);
+                dw[v * N + j] = __builtin_fmaf(gy, xh, dw[v * N + j]);
+                db[v * N + j] += gy;
+                const float g = gy * w[v * N + j];  // zero past the row's end, as weight and grad_y are
+                s1 += g;
+                s2 = __builtin_fmaf(g, xh, s2);
             }
-        }
-        s1 = row_sum<G>(s1, s_sum[turn][0]) / n;
-        s2 = row_sum<G>(s2, s_sum[turn][1]) / n;
+        __builtin_amdgcn_sched_barrier(0);  // nothing but the packed row and the sums is kept over the barrier
+        row_sums<G>(s1, s2, s_sum[turn]);
+        s1 *= inverse;
+        s2 *= inverse;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            // formed anew from the packed row: kept from above, xh and g would take a register each
+            u32x4 bx = __builtin_bit_cast(u32x4, cx[v]), bg = __builtin_bit_cast(u32x4, cg[v]);
+            asm volatile("" : "+v"(bx), "+v"(bg));
+            cx[v] = __builtin_bit_cast(typename Pack<T>::V, bx);
+            cg[v] = __builtin_bit_cast(typename Pack<T>::V, bg);
             typename Pack<T>::V o;
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                o[j] = static_cast<T>(rs * (g[v * N + j] - s1 - xh[v * N + j] * s2));
-            store_pack(grad_x + r * dim, (static_cast<int64_t>(v) * G + lane) * N, dim, o);
+            for (int j = 0; j < N; ++j) {
+                const float xh = (static_cast<float>(cx[v][j]) - m) * rs;
+                const float g = static_cast<float>(cg[v][j]) * w[v * N + j];
+                o[j] = static_cast<T>(rs * (g - s1 - xh * s2));
+            }
+            store_pack(grad_x + r * dim, (v * G + lane) * N, dim, o);
         }
     }
     // the workgroup's column sums: its groups' added in order
-    float *out = partial + static_cast<int64_t>(blockIdx.x) * 2 * dim;
+    const int64_t width = partial_width(dim);
+    float *out = partial + static_cast<int64_t>(blockIdx.x) * 2 * width;
 #pragma unroll
     for (int which = 0; which < 2; ++which)
 #pragma unroll
@@ -202,10 +273,12 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(const T *__restrict_
                         for (int k = 1; k < kRows; ++k) acc[j] += s_cols[(k * G + lane) * (N + 1) + j];
             }
             if (group == 0) {
-                const int64_t col = (static_cast<int64_t>(v) * G + lane) * N;
+                const int col = (v * G + lane) * N;
+                if (col < width)
 #pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (col + j < dim) out[which * dim + col + j] = acc[j];
+                    for (int j = 0; j < N; j += 4)
+                        *reinterpret_cast<float4 *>(out + which * width + col + j) =
+                            make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
             }
         }
 }
@@ -266,9 +339,9 @@ __global__ __launch_bounds__(kThreads) void norm_columns_kernel(const T *__restr
         dw = __builtin_fmaf(g, (static_cast<float>(x[r * dim + col]) - mean[r]) * rstd[r], dw);
         db += g;
     }
-    float *out = partial + static_cast<int64_t>(blockIdx.y) * 2 * dim;
+    float *out = partial + static_cast<int64_t>(blockIdx.y) * 2 * partial_width(dim);
     out[col] = dw;
-    out[dim + col] = db;
+    out[partial_width(dim) + col] = db;
 }
 
 // grad_weight (y = 0) and grad_bias (y = 1): 64 columns a workgroup, its 16 waves take the partial sums in turn.
@@ -282,9 +355,10 @@ __global__ __launch_bounds__(kReduceThreads) void norm_reduce_kernel(const float
     const int64_t col = static_cast<int64_t>(blockIdx.x) * kWave + lane;
     float s = 0.0f;
     if (col < dim) {
-        const float *p = partial + blockIdx.y * dim + col;
+        const int64_t width = partial_width(dim);
+        const float *p = partial + blockIdx.y * width + col;
 #pragma unroll 8
-        for (int i = wave; i < parts; i += kWaves) s += p[static_cast<int64_t>(i) * 2 * dim];
+        for (int i = wave; i < parts; i += kWaves) s += p[static_cast<int64_t>(i) * 2 * width];
     }
     s_part[wave][lane] = s;
     __syncthreads();
@@ -294,47 +368,75 @@ __global__ __launch_bounds__(kReduceThreads) void norm_reduce_kernel(const float
     }
 }
 
-// How a row is held: the lanes that share it and the packs of a lane; wide: more than 256 lanes' 4 packs.
+// How a row is held: the lanes that share it and the packs of a lane; none: wider than registers hold, or shorter than
+// a pack.
 struct RowShape {
     int lanes, packs;
 };
 
 inline RowShape row_shape(int64_t dim, int pack) {
     const int64_t packs = (dim + pack - 1) / pack;
+    if (dim < pack) return {0, 0};
     if (packs <= 16) return {16, 1};
     if (packs <= 64) return {64, 1};
     if (packs <= 128) return {64, 2};
     if (packs <= 256) return {256, 1};
     if (packs <= 512) return {256, 2};
-    if (packs <= 1024) return {256, 4};
+    if (packs <= 1024) return {512, 2};
+    if (packs <= 2048 && pack == 4) return {1024, 2};
     return {0, 0};
 }
 
-int64_t bwd_blocks(int64_t rows) { return rows < kBwdBlocks ? rows : kBwdBlocks; }
+// Workgroups that share `need` turns evenly, at most `most` of them.
+int64_t even_blocks(int64_t need, int64_t most) {
+    const int64_t turns = (need + most - 1) / most;
+    return turns == 0 ? 0 : (need + turns - 1) / turns;
+}
+
+// Workgroups of the forward: as many as run at once, which visit the rows in turn with their weights in registers.
+int64_t fwd_blocks(int64_t rows, int lanes, int columns) {
+    const int64_t waves = row_threads(lanes) / kWave, per = row_threads(lanes) / lanes;
+    return even_blocks((rows + per - 1) / per, kUnits * 4 * fwd_waves(columns) / waves);
+}
+
+// Workgroups of the backward: one a CU at least, for the memory's rate; more, up to what runs at once, only while each
+// still has 8 turns, because each writes a row of float32 column sums that the second kernel reads.
+int64_t bwd_blocks(int64_t rows, int lanes) {
+    const int64_t waves = row_threads(lanes) / kWave, per = row_threads(lanes) / lanes;
+    const int64_t need = (rows + per - 1) / per;
+    int64_t most = kUnits * (waves < 12 ? 12 / waves : 1);
+    if (most > kBwdBlocks) most = kBwdBlocks;
+    if (most > need / 8) most = need / 8;
+    if (most < kUnits) most = kUnits;
+    return even_blocks(need, most);
+}
 
 template <typename T, typename W>
 gs_status run_fwd(const void *x, const void *weight, const void *bias, int64_t rows, int64_t dim, float eps, void *y,
                   float *mean, float *rstd, hipStream_t stream) {
     const RowShape shape = row_shape(dim, Pack<T>::kN);
-#define GS_NORM_FWD(G, V)                                                                                             \
-    if (shape.lanes == G && shape.packs == V) {                                                                       \
-        const int64_t blocks = (rows + kThreads / G - 1) / (kThreads / G);                                            \
-        hipLaunchKernelGGL((norm_fwd_kernel<T, W, G, V>),                                                             \
-                           dim3(static_cast<unsigned>(blocks < kFwdBlocks ? blocks : kFwdBlocks)), dim3(kThreads), 0, \
-                           stream, static_cast<const T *>(x), static_cast<const W *>(weight),                         \
-                           static_cast<const W *>(bias), rows, dim, eps, static_cast<T *>(y), mean, rstd);            \
-        GS_LAUNCH_TRY("norm_fwd_kernel");                                                                             \
-        return ok();                                                                                                  \
+#define GS_NORM_FWD(G, V)                                                                                            \
+    if (shape.lanes == G && shape.packs == V) {                                                                      \
+        hipLaunchKernelGGL((norm_fwd_kernel<T, W, G, V>), dim3(static_cast<unsigned>(                                \
+                               fwd_blocks(rows, G, V * Pack<T>::kN))),                                               \
+                           dim3(row_threads(G)), 0, stream, static_cast<const T *>(x),                               \
+                           static_cast<const W *>(weight), static_cast<const W *>(bias), rows,                       \
+                           static_cast<int>(dim), eps, static_cast<T *>(y), mean, rstd);                             \
+        GS_LAUNCH_TRY("norm_fwd_kernel");                                                                            \
+        return ok();                                                                                                 \
     }
     GS_NORM_FWD(16, 1)
     GS_NORM_FWD(64, 1)
     GS_NORM_FWD(64, 2)
     GS_NORM_FWD(256, 1)
     GS_NORM_FWD(256, 2)
-    GS_NORM_FWD(256, 4)
+    GS_NORM_FWD(512, 2)
+    if constexpr (Pack<T>::kN == 4) {
+        GS_NORM_FWD(1024, 2)
+    }
 #undef GS_NORM_FWD
     hipLaunchKernelGGL((norm_fwd_wide_kernel<T, W>),
-                       dim3(static_cast<unsigned>(rows < kFwdBlocks ? rows : kFwdBlocks)), dim3(kThreads), 0, stream,
+                       dim3(static_cast<unsigned>(rows < kWideFwdBlocks ? rows : kWideFwdBlocks)), dim3(kThreads), 0, stream,
                        static_cast<const T *>(x), static_cast<const W *>(weight), static_cast<const W *>(bias), rows,
                        dim, eps, static_cast<T *>(y), mean, rstd);
     GS_LAUNCH_TRY("norm_fwd_wide_kernel");
@@ -349,29 +451,31 @@ gs_status run_bwd(const void *x, const void *weight, const float *mean, const fl
     const T *tx = static_cast<const T *>(x), *tg = static_cast<const T *>(grad_y);
     const W *tw = static_cast<const W *>(weight);
     T *to = static_cast<T *>(grad_x);
-    int64_t parts = bwd_blocks(rows);
-#define GS_NORM_BWD(G, V)                                                                                          \
-    if (shape.lanes == G && shape.packs == V) {                                                                    \
-        parts = (rows + kThreads / G - 1) / (kThreads / G);                                                        \
-        if (parts > kBwdBlocks) parts = kBwdBlocks;                                                                \
-        if (rows > 0)                                                                                              \
-            hipLaunchKernelGGL((norm_bwd_kernel<T, W, G, V>), dim3(static_cast<unsigned>(parts)), dim3(kThreads),  \
-                               0, stream, tx, tw, mean, rstd, tg, rows, dim, to, partial);                         \
+    int64_t parts = rows < kWideBwdParts ? rows : kWideBwdParts;
+#define GS_NORM_BWD(G, V)                                                                                           \
+    if (shape.lanes == G && shape.packs == V) {                                                                     \
+        parts = bwd_blocks(rows, G);                                                                                \
+        if (rows > 0)                                                                                               \
+            hipLaunchKernelGGL((norm_bwd_kernel<T, W, G, V>), dim3(static_cast<unsigned>(parts)),                   \
+                               dim3(row_threads(G)), 0, stream, tx, tw, mean, rstd, tg, rows, static_cast<int>(dim), \
+                               to, partial);                                                                        \
     }
     GS_NORM_BWD(16, 1)
     GS_NORM_BWD(64, 1)
     GS_NORM_BWD(64, 2)
     GS_NORM_BWD(256, 1)
     GS_NORM_BWD(256, 2)
-    GS_NORM_BWD(256, 4)
+    GS_NORM_BWD(512, 2)
+    if constexpr (Pack<T>::kN == 4) {
+        GS_NORM_BWD(1024, 2)
+    }
 #undef GS_NORM_BWD
     GS_LAUNCH_TRY("norm_bwd_kernel");
     if (shape.lanes == 0 && rows > 0) {
         hipLaunchKernelGGL((norm_bwd_wide_kernel<T, W>),
-                           dim3(static_cast<unsigned>(rows < kFwdBlocks ? rows : kFwdBlocks)), dim3(kThreads), 0,
+                           dim3(static_cast<unsigned>(rows < kWideFwdBlocks ? rows : kWideFwdBlocks)), dim3(kThreads), 0,
                            stream, tx, tw, mean, rstd, tg, rows, dim, to);
         GS_LAUNCH_TRY("norm_bwd_wide_kernel");
-        if (parts > 64) parts = 64;
         hipLaunchKernelGGL((norm_columns_kernel<T>),
                            dim3(static_cast<unsigned>((dim + kThreads - 1) / kThreads), static_cast<unsigned>(parts)),
                            dim3(kThreads), 0, stream, tx, mean, rstd, tg, rows, dim, partial);
@@ -426,7 +530,7 @@ extern "C" gs_status gs_layer_norm_fwd(const void *x, const void *weight, const 
 
 extern "C" size_t gs_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
     if (rows < 0 || rows >= kLimit || dim < 1 || dim >= kLimit) return 0;
-    return static_cast<size_t>(bwd_blocks(rows)) * 2 * static_cast<size_t>(dim) * sizeof(float);
+    return static_cast<size_t>(rows < kBwdBlocks ? rows : kBwdBlocks) * 2 * static_cast<size_t>(partial_width(dim)) * sizeof(float);
 }
 
 extern "C" gs_status gs_layer_norm_bwd(const void *x, const void *weight, const float *mean, const float *rstd,
