@@ -190,3 +190,10 @@ def test_orthogonalize_form_moves_singular_values_only():
         for _ in range(5):
             s = a * s + b * s ** 3 + c * s ** 5
         torch.testing.assert_close(got, left @ torch.diag(s) @ right, rtol=1e-9, atol=1e-9)
+
+
+def test_a_workspace_of_the_caller_is_looked_at():
+    """A given workspace has to be bytes on the operands' device."""
+    for bad in (torch.zeros(4, dtype=torch.float32), torch.zeros(4, dtype=torch.uint8), [1, 2]):
+        with pytest.raises((TypeError, ValueError), match="workspace"):
+            binding._given_room(bad, torch.device("cuda", 0))

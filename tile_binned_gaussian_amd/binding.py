@@ -620,7 +620,8 @@ def _room(nbytes, device):
     return ws, ws.data_ptr(), nbytes
 
 
-def _given_room(workspace):
+def _given_room(workspace, device):
+    _req(workspace, "workspace", torch.uint8, device)
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
@@ -698,7 +699,7 @@ def gs_layer_norm_bwd(x, weight, mean, rstd, grad_y, grad_bias=True, out=None, s
         ow = _arg(out.weight, "grad_weight", weight.dtype, dev, (dim,))
         ob = None if out.bias is None else _arg(out.bias, "grad_bias", weight.dtype, dev, (dim,))
     ws, pws, room = _room(lib.gs_layer_norm_bwd_workspace_bytes(rows, dim), dev) if workspace is None \
-        else _given_room(workspace)
+        else _given_room(workspace, dev)
     _check(lib.gs_layer_norm_bwd(px, pw, pm, pr, pg, rows, dim, code, wcode, ox, ow, ob, pws, room,
                                  _stream_int(stream)))
     return out
@@ -743,7 +744,7 @@ def gs_expert_plan(ids, experts, out=None, stream=None, workspace=None) -> Exper
         po = _arg(out.offsets, "offsets", torch.int32, dev, (E + 1,))
         pr, pp = _arg(out.rows, "rows", torch.int32, dev, (T, K)), _arg(out.pairs, "pairs", torch.int32, dev, (T * K,))
     ws, pws, room = _room(lib.gs_expert_plan_workspace_bytes(T, K, E), dev) if workspace is None \
-        else _given_room(workspace)
+        else _given_room(workspace, dev)
     _check(lib.gs_expert_plan(ids.data_ptr(), T, K, E, po, pr, pp, pws, room, _stream_int(stream)))
     return out
 
@@ -835,7 +836,7 @@ def gs_orthogonalize(update, steps=5, coefficients=(3.4445, -4.7750, 2.0315), ep
     else:
         _arg(out, "out", update.dtype, dev, update.shape)
     ws, pws, room = _room(lib.gs_orthogonalize_workspace_bytes(B, m, n), dev) if workspace is None \
-        else _given_room(workspace)
+        else _given_room(workspace, dev)
     _check(lib.gs_orthogonalize(pu, B, m, n, int(steps), a, b, c, eps, code, out.data_ptr(), pws, room,
                                 _stream_int(stream)))
     return out
