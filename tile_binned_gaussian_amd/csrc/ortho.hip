@@ -55,13 +55,14 @@ __device__ __forceinline__ void split(const float *v, H &hi, H &lo) {
 
 // The sum over the workgroup's threads, in every thread.
 __device__ __forceinline__ double workgroup_sum(double v, double *s_part) {
-    s_part[threadIdx.x] = v;
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, kWave);
+    if (threadIdx.x % kWave == 0) s_part[threadIdx.x / kWave] = v;
     __syncthreads();
-    for (int d = kThreads / 2; d > 0; d >>= 1) {
-        if (static_cast<int>(threadIdx.x) < d) s_part[threadIdx.x] += s_part[threadIdx.x + d];
-        __syncthreads();
-    }
-    return s_part[0];
+    v = 0.0;
+#pragma unroll
+    for (int w = 0; w < kThreads / kWave; ++w) v += s_part[w];
+    return v;
 }
 
 // Partial sums of squares of matrix blockIdx.y in float64.
@@ -69,7 +70,7 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_norm_kernel(const T *__restrict__ update, int64_t count,
                                                               double *__restrict__ partial) {
     constexpr int N = Pack<T>::kN;
-    __shared__ double s_part[kThreads];
+    __shared__ double s_part[kThreads / kWave];
     const T *u = update + blockIdx.y * count;
     double s = 0.0;
     for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * N; i < count;
@@ -94,22 +95,27 @@ __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restri
                                                                Planes turned) {
     constexpr int kTile = 64;
     __shared__ float s_tile[kTile][kTile + 1];
-    __shared__ double s_part[kThreads];
+    __shared__ double s_part[kThreads / kWave];
+    const size_t plane = blockIdx.z * static_cast<size_t>(pm) * pn;
+    const int r0 = blockIdx.y * kTile, c0 = blockIdx.x * kTile;
+    const int tr = threadIdx.x / kTile, tc = threadIdx.x % kTile;
+    constexpr int kTurns = kTile * kTile / kThreads;
+    T in[kTurns];  // on their way while the norm is summed
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int r = r0 + tr + i * (kThreads / kTile), c = c0 + tc;
+        in[i] = update[(static_cast<size_t>(blockIdx.z) * m + (r < m ? r : m - 1)) * n + (c < n ? c : n - 1)];
+    }
     double sum = 0.0;
     for (int i = threadIdx.x; i < parts; i += kThreads) sum += partial[blockIdx.z * parts + i];
     const double scale =
         static_cast<double>(kScaleX) / (sqrt(workgroup_sum(sum, s_part)) + static_cast<double>(eps));
-    const size_t plane = blockIdx.z * static_cast<size_t>(pm) * pn;
-    const int r0 = blockIdx.y * kTile, c0 = blockIdx.x * kTile;
-    const int tc = threadIdx.x % kTile;
-    for (int tr = threadIdx.x / kTile; tr < kTile; tr += kThreads / kTile) {
-        const int r = r0 + tr, c = c0 + tc;
-        float v = 0.0f;
-        if (r < m && c < n)
-            v = static_cast<float>(
-                static_cast<double>(static_cast<float>(update[(static_cast<size_t>(blockIdx.z) * m + r) * n + c])) *
-                scale);
-        s_tile[tr][tc] = v;
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int row = tr + i * (kThreads / kTile);
+        s_tile[row][tc] = r0 + row < m && c0 + tc < n
+                              ? static_cast<float>(static_cast<double>(static_cast<float>(in[i])) * scale)
+                              : 0.0f;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < kTile * kTile / 8; i += kThreads) {
@@ -145,6 +151,10 @@ struct ProductArgs {
     int tile_rows, tile_cols;
     int symmetric;    // P = Q and the result is symmetric: tiles of the lower triangle, written to both sides
     float scale_acc, scale_add;
+    // the last step's: the result itself, [out_rows][out_cols] of out_type for each matrix, in place of planes
+    void *out;
+    int out_type, out_rows, out_cols;
+    int out_turned;   // its rows are the product's columns
 };
 
 // One block from memory to LDS, 16 bytes a lane, without registers in between. lds: byte address, the same in the
@@ -177,16 +187,50 @@ __device__ __forceinline__ h16x4 quad_transpose(h16x4 v) {
     return __builtin_bit_cast(h16x4, r);
 }
 
+// The same of float32 values.
+__device__ __forceinline__ void quad_transpose(float (&v)[4]) {
+    const int q = threadIdx.x % 4;
+    const auto swap = [](float given, auto ctrl) {
+        return __builtin_bit_cast(
+            float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, given), decltype(ctrl)::value, 0xF, 0xF, true));
+    };
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {  // with the neighbour: the even lane gets rows 0 and 2, the odd one rows 1 and 3
+        const float got = swap(q % 2 ? v[k] : v[k + 1], std::integral_constant<int, 0xB1>());
+        v[k + (q % 2 ? 0 : 1)] = got;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {  // with the lane two on
+        const float got = swap(q < 2 ? v[k + 2] : v[k], std::integral_constant<int, 0x4E>());
+        if (q < 2) v[k + 2] = got;
+        else v[k] = got;
+    }
+}
+
 // The workgroup's tile: in order on each of the 8 dies, whose L2 then holds the panels that neighbours share.
 __device__ __forceinline__ void tile_of(const ProductArgs &a, int &ti, int &tj) {
     const int tiles = gridDim.x, die = blockIdx.x % 8;
     const int t = die * (tiles / 8) + (die < tiles % 8 ? die : tiles % 8) + blockIdx.x / 8;
-    if (a.symmetric) {
-        ti = static_cast<int>((sqrtf(8.0f * static_cast<float>(t) + 1.0f) - 1.0f) * 0.5f);
-        while (ti * (ti + 1) / 2 > t) --ti;
-        while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
-        tj = t - ti * (ti + 1) / 2;
-    } else {  // bands of four tile rows
+    // bands of four tile rows, column by column
+    if (a.symmetric) {  // of the lower triangle: band k has 8 k k + 2 k tiles before it
+        int band = static_cast<int>(sqrtf(static_cast<float>(t) * 0.125f));
+        while (8 * band * band + 2 * band > t) --band;
+        while (8 * (band + 1) * (band + 1) + 2 * (band + 1) <= t) ++band;
+        const int height = a.tile_rows - band * 4 < 4 ? a.tile_rows - band * 4 : 4;
+        int in = t - (8 * band * band + 2 * band);
+        const int whole = height * (band * 4 + 1);  // in columns that all rows of the band reach
+        if (in < whole) {
+            ti = in % height;
+            tj = in / height;
+        } else {
+            in -= whole;
+            int first = 1;  // the first row of the band that reaches the column
+            while (in >= height - first) in -= height - first++;
+            ti = first + in;
+            tj = band * 4 + first;
+        }
+        ti += band * 4;
+    } else {
         const int band = t / (4 * a.tile_cols), in = t % (4 * a.tile_cols);
         const int height = a.tile_rows - band * 4 < 4 ? a.tile_rows - band * 4 : 4;
         ti = band * 4 + in % height;
@@ -215,6 +259,23 @@ __device__ __forceinline__ Four load_four(const ProductArgs &a, size_t at) {
     return f;
 }
 
+// Four neighbours of a row of the result, those past its end left out.
+template <typename T>
+__device__ __forceinline__ void store_out(const ProductArgs &a, size_t batch, int row, int col, const float *v) {
+    if (row >= a.out_rows || col >= a.out_cols) return;
+    T *to = static_cast<T *>(a.out) + (batch * a.out_rows + row) * a.out_cols + col;
+    typedef T V __attribute__((ext_vector_type(4)));
+    typedef V VU __attribute__((aligned(sizeof(T))));
+    if (col + 4 <= a.out_cols) {
+        *reinterpret_cast<VU *>(to) = V{static_cast<T>(v[0]), static_cast<T>(v[1]), static_cast<T>(v[2]),
+                                        static_cast<T>(v[3])};
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        if (col + k < a.out_cols) to[k] = static_cast<T>(v[k]);
+}
+
 // Four sums on their way out. both: to `turned` too.
 __device__ __forceinline__ void finish_four(const ProductArgs &a, size_t batch, int mp, int np, int g, float *v,
                                             const Four &add, int lane, bool both) {
@@ -223,6 +284,25 @@ __device__ __forceinline__ void finish_four(const ProductArgs &a, size_t batch, 
     for (int k = 0; k < 4; ++k)
         v[k] = __builtin_fmaf(a.scale_add, static_cast<float>(add.hi[k]) + static_cast<float>(add.lo[k]),
                               v[k] * a.scale_acc);
+    if (a.out) {
+        float r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] = v[k] * (1.0f / kScaleX);
+        int row = mp * kPanel + g * 8 + lane / 32 * 4, col = np * kPanel + lane % 32;
+        if (a.out_turned) {
+            const int down = row;
+            row = col;
+            col = down;
+        } else {
+            quad_transpose(r);
+            row += lane % 4;
+            col = np * kPanel + lane % 32 / 4 * 4;
+        }
+        if (a.out_type == GS_F32) store_out<float>(a, batch, row, col, r);
+        else if (a.out_type == GS_BF16) store_out<__bf16>(a, batch, row, col, r);
+        else store_out<_Float16>(a, batch, row, col, r);
+        return;
+    }
     h16x4 h, l;
     split<4>(v, h, l);
     if (both) {
@@ -236,19 +316,22 @@ __device__ __forceinline__ void finish_four(const ProductArgs &a, size_t batch, 
     if (a.straight.lo) *reinterpret_cast<h16x4 *>(a.straight.lo + to) = quad_transpose(l);
 }
 
-// A workgroup of four waves makes a T x T tile, each wave a quarter of it. PRODUCTS = 3: both halves of the operands
+// A workgroup of WR x WC waves makes a T x T tile, each wave its part of it. PRODUCTS = 3: both halves of the operands
 // (high high + high low + low high); 1: the high halves alone. A stage of the LDS ring holds 32 columns of the high
 // halves, or 16 of both; while one is multiplied the next is there already (its first operands are read ahead of the
 // barrier) and the others are on their way: two of up to 32 KB, or six of the smallest tile's 8 KB, which few
 // workgroups have to themselves and whose time is the memory's latency.
-template <int T, int PRODUCTS, int kStages>
-__global__ __launch_bounds__(kThreads, T <= 128 && kStages == 4 ? 2 : 1) void ortho_product_kernel(ProductArgs a) {
-    constexpr int F = T / 64;                   // 32 x 32 results of a wave, each way
+template <int T, int PRODUCTS, int kStages, int WR, int WC>
+__global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (T <= 128 && kStages == 4 ? 2 : 1)) void ortho_product_kernel(
+    ProductArgs a) {
     constexpr int kPanels = T / kPanel;
+    constexpr int FR = kPanels / WR, FC = kPanels / WC;  // 32 x 32 results of a wave, each way
+    static_assert(FR * WR == kPanels && FC * WC == kPanels, "whole results");
     constexpr int PL = PRODUCTS == 1 ? 1 : 2;   // planes staged
     constexpr int S = PRODUCTS == 1 ? 2 : 1;    // blocks of 16 columns in a stage
     constexpr int kBlocks = 2 * PL * kPanels * S;
-    constexpr int L = kBlocks / 4;              // blocks a wave loads for a stage
+    constexpr int L = kBlocks / (WR * WC);      // blocks a wave loads for a stage
+    static_assert(L * WR * WC == kBlocks, "the waves share the loads evenly");
     constexpr uint32_t kStageBytes = kBlocks * kBlock * sizeof(_Float16);
     __shared__ __attribute__((aligned(1024))) _Float16 s_ring[kStages * kBlocks * kBlock];
 
@@ -283,20 +366,20 @@ __global__ __launch_bounds__(kThreads, T <= 128 && kStages == 4 ? 2 : 1) void or
         // past the end the last stage is loaded again, unused
         if (issued + 1 < stages) src[i] += wave * L + i < kBlocks / 2 ? row_step : col_step;
     };
-    const int wr = wave / 2, wc = wave % 2;
-    constexpr int R = 2 * PL * F;  // operands of a wave for one block of 16 columns
+    const int wr = wave / WC, wc = wave % WC;
+    constexpr int R = PL * (FR + FC);  // operands of a wave for one block of 16 columns: rows high, low, columns high, low
     h16x8 frag[2][R];
     const auto fetch = [&](const _Float16 *stage_at, int s, int turn, int r) {
-        const int op = r / (PL * F), plane = r / F % PL, f = r % F;
+        const int op = r < PL * FR ? 0 : 1, q = r - op * PL * FR, F = op ? FC : FR, plane = q / F, f = q % F;
         frag[turn][r] = *reinterpret_cast<const h16x8 *>(
             stage_at + (((op * PL + plane) * kPanels + (op ? wc : wr) * F + f) * S + s) * kBlock);
     };
     const auto stage_at = [&](int stage) { return s_ring + (stage % kStages) * (kBlocks * kBlock) + lane * 8; };
-    f32x16 acc[F][F] = {};
+    f32x16 acc[FR][FC] = {};
     // The products of one block of 16 columns with, in between and in this order, the reads of the next block's
     // operands and FIRST..LAST of the stage's loads.
     const auto multiply = [&](int turn, const _Float16 *next, int next_s, auto first, auto last) {
-        constexpr int M = PRODUCTS * F * F, kFirst = decltype(first)::value, kLoads = decltype(last)::value - kFirst;
+        constexpr int M = PRODUCTS * FR * FC, kFirst = decltype(first)::value, kLoads = decltype(last)::value - kFirst;
         constexpr int kReads = M > R ? M - M / 4 : M;  // the reads end early enough to be done at the next barrier
 #pragma unroll
         for (int x = 0; x < M; ++x) {
@@ -304,10 +387,10 @@ __global__ __launch_bounds__(kThreads, T <= 128 && kStages == 4 ? 2 : 1) void or
             for (int r = x * R / kReads; r < (x + 1) * R / kReads && r < R; ++r) fetch(next, next_s, 1 - turn, r);
 #pragma unroll
             for (int i = x * kLoads / M; i < (x + 1) * kLoads / M; ++i) issue(kFirst + i);
-            const int term = PRODUCTS == 1 ? 2 : x / (F * F), i = x / F % F, j = x % F;
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag[turn][(term == 0 ? PL - 1 : 0) * F + i],
-                                                               frag[turn][(PL + (term == 1 ? PL - 1 : 0)) * F + j],
-                                                               acc[i][j], 0, 0, 0);
+            const int term = PRODUCTS == 1 ? 2 : x / (FR * FC), i = x / FC % FR, j = x % FC;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                frag[turn][(term == 0 ? PL - 1 : 0) * FR + i],
+                frag[turn][PL * FR + (term == 1 ? PL - 1 : 0) * FC + j], acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -340,21 +423,21 @@ __global__ __launch_bounds__(kThreads, T <= 128 && kStages == 4 ? 2 : 1) void or
 
     const bool both = !a.symmetric || ti != tj;  // a tile on the diagonal is its own mirror
 #pragma unroll
-    for (int i = 0; i < F; ++i) {
-        const int mp = ti * kPanels + wr * F + i;
+    for (int i = 0; i < FR; ++i) {
+        const int mp = ti * kPanels + wr * FR + i;
         if (mp >= row_panels) continue;
         // a row of results' additions before its first store: one wait for memory, not one for every four values
-        Four add[F][4];
+        Four add[FC][4];
 #pragma unroll
-        for (int j = 0; j < F; ++j) {
-            const int np = tj * kPanels + wc * F + j;
+        for (int j = 0; j < FC; ++j) {
+            const int np = tj * kPanels + wc * FC + j;
 #pragma unroll
             for (int g = 0; g < 4; ++g)
                 add[j][g] = load_four(a, four_at(a, batch, mp, np < col_panels ? np : col_panels - 1, g, lane));
         }
 #pragma unroll
-        for (int j = 0; j < F; ++j) {
-            const int np = tj * kPanels + wc * F + j;
+        for (int j = 0; j < FC; ++j) {
+            const int np = tj * kPanels + wc * FC + j;
             if (np >= col_panels) continue;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -468,7 +551,7 @@ __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(Prod
     }
 }
 
-// out [batch][m][n] from the planes that hold its rows.
+// out [batch][m][n] from the planes that hold its rows, where there are no steps.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, int m, int n, int pm, int pn,
                                                                 T *__restrict__ out) {
@@ -815,28 +898,24 @@ gs_status product(ProductArgs g, int64_t batch, int products, hipStream_t stream
     const dim3 grid(static_cast<unsigned>(g.symmetric ? g.tile_rows * (g.tile_rows + 1) / 2
                                                       : g.tile_rows * g.tile_cols),
                     static_cast<unsigned>(batch));
-#define GS_PRODUCT(T, P)                                                                                  \
-    if (edge == T && products == P)                                                                       \
-    hipLaunchKernelGGL((ortho_product_kernel<T, P, 4>), grid, dim3(kThreads), 0, stream, g)
+    const bool alone = static_cast<int64_t>(grid.x) * batch <= kUnits;
+#define GS_PRODUCT(T, STAGES, WR, WC, when)                                                                          \
+    if (edge == T && (when)) {                                                                                       \
+        if (products == 1)                                                                                           \
+            hipLaunchKernelGGL((ortho_product_kernel<T, 1, STAGES, WR, WC>), grid, dim3(WR * WC * kWave), 0, stream, \
+                               g);                                                                                   \
+        else                                                                                                         \
+            hipLaunchKernelGGL((ortho_product_kernel<T, 3, STAGES, WR, WC>), grid, dim3(WR * WC * kWave), 0, stream, \
+                               g);                                                                                   \
+    }
     if (edge == 64 && products == 1)
         hipLaunchKernelGGL((ortho_product_direct_kernel<1, 8>), grid, dim3(8 * kWave), 0, stream, g);
     if (edge == 64 && products == 3)
         hipLaunchKernelGGL((ortho_product_direct_kernel<3, 8>), grid, dim3(8 * kWave), 0, stream, g);
-    const bool alone = static_cast<int64_t>(grid.x) * batch <= kUnits;
-    if (edge == 128 && alone) {
-        if (products == 1)
-            hipLaunchKernelGGL((ortho_product_kernel<128, 1, 8>), grid, dim3(kThreads), 0, stream, g);
-        else
-            hipLaunchKernelGGL((ortho_product_kernel<128, 3, 8>), grid, dim3(kThreads), 0, stream, g);
-    }
-    if (!alone) {
-        GS_PRODUCT(128, 1);
-        GS_PRODUCT(128, 3);
-    }
-    GS_PRODUCT(192, 1);
-    GS_PRODUCT(192, 3);
-    GS_PRODUCT(256, 1);
-    GS_PRODUCT(256, 3);
+    GS_PRODUCT(128, 6, 4, 2, alone)
+    GS_PRODUCT(128, 4, 4, 2, !alone)
+    GS_PRODUCT(192, 4, 6, 2, true)
+    GS_PRODUCT(256, 4, 2, 4, true)
 #undef GS_PRODUCT
     GS_LAUNCH_TRY("ortho_product_kernel");
     return GS_OK;
@@ -910,13 +989,18 @@ gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps
         const StepProducts now = step_products<T>(M, steps - s);
         // the low parts that nothing reads are not written
         const Planes poly = now.apply == 3 ? l.poly : Planes{l.poly.hi, nullptr};
-        const bool last = s == steps - 1;
-        const Planes next =
-            (last ? !tall : step_products<T>(M, steps - s - 1).gram == 3) ? l.x : Planes{l.x.hi, nullptr};
-        const ProductArgs ops[3] = {
-            {l.x, l.x, {}, l.gram, l.gram, M, M, N, 0, 0, 1, kScaleA / (kScaleX * kScaleX), 0.0f},
-            {l.gram, l.gram, l.gram, poly, poly, M, M, M, 0, 0, 1, c / kScaleA, b},
-            {l.poly, l.xt[at], l.xt[at], next, l.xt[1 - at], M, N, M, 0, 0, 0, 1.0f / kScaleA, a}};
+        const Planes next = step_products<T>(M, steps - s - 1).gram == 3 ? l.x : Planes{l.x.hi, nullptr};
+        ProductArgs ops[3] = {
+            {l.x, l.x, {}, l.gram, l.gram, M, M, N, 0, 0, 1, kScaleA / (kScaleX * kScaleX), 0.0f, nullptr, 0, 0, 0, 0},
+            {l.gram, l.gram, l.gram, poly, poly, M, M, M, 0, 0, 1, c / kScaleA, b, nullptr, 0, 0, 0, 0},
+            {l.poly, l.xt[at], l.xt[at], next, l.xt[1 - at], M, N, M, 0, 0, 0, 1.0f / kScaleA, a, nullptr, 0, 0, 0, 0}};
+        if (s == steps - 1) {
+            ops[2].out = out;
+            ops[2].out_type = std::is_same<T, float>::value ? GS_F32 : std::is_same<T, __bf16>::value ? GS_BF16 : GS_F16;
+            ops[2].out_rows = static_cast<int>(m);
+            ops[2].out_cols = static_cast<int>(n);
+            ops[2].out_turned = tall ? 1 : 0;
+        }
         const int products[3] = {now.gram, now.poly, now.apply};
         for (int i = 0; i < 3; ++i) {
             const gs_status bad = product(ops[i], batch, products[i], stream);
@@ -924,6 +1008,7 @@ gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps
         }
         at = 1 - at;
     }
+    if (steps > 0) return ok();
     hipLaunchKernelGGL((ortho_finish_kernel<T>), dim3((pn + 63) / 64, pm / 32, z), dim3(kThreads), 0, stream,
                        tall ? l.xt[at] : l.x, static_cast<int>(m), static_cast<int>(n), pm, pn,
                        static_cast<T *>(out));
