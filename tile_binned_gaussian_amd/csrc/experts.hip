@@ -16,13 +16,14 @@ constexpr int kMaxExperts = 4096;
 constexpr int kPlanThreads = 1024;   // up to kWideExperts experts
 constexpr int kWideThreads = 256;    // above: one LDS counter per expert and wave has to fit
 constexpr int kWideExperts = 1024;
-constexpr int64_t kPlanChunk = 4096;  // pairs of one workgroup, at least
+constexpr int64_t kPlanAlone = 4096;  // pairs that one workgroup takes alone, in one launch
 constexpr int64_t kPlanChunks = 256;  // workgroups, at most
 
+// Pairs of a workgroup: one step of its threads, or what 256 workgroups need.
 int64_t plan_chunk(int64_t pairs) {
-    int64_t c = (pairs + kPlanChunks - 1) / kPlanChunks;
-    c = (c + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
-    return c < kPlanChunk ? kPlanChunk : c;
+    if (pairs <= kPlanAlone) return kPlanAlone;
+    const int64_t c = (pairs + kPlanChunks - 1) / kPlanChunks;
+    return (c + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
 }
 
 int64_t plan_chunks(int64_t pairs) { return pairs == 0 ? 1 : (pairs + plan_chunk(pairs) - 1) / plan_chunk(pairs); }
@@ -68,7 +69,8 @@ __global__ __launch_bounds__(kPlanThreads) void expert_place_kernel(const int32_
     const int64_t part = ((end - begin + blockDim.x - 1) / blockDim.x) * kWave;
     const int64_t from = begin + wave * part;
     const int64_t to = from + part < end ? from + part : end;
-    for (int i = threadIdx.x; i < waves * experts; i += blockDim.x) s_plan[i] = 0;
+    int32_t *s_total = s_plan + waves * experts, *s_before = s_total + experts;
+    for (int i = threadIdx.x; i < (waves + 2) * experts; i += blockDim.x) s_plan[i] = 0;
     if (threadIdx.x == 0) s_carry = 0;
     __syncthreads();
     for (int64_t p = from + lane; p < to; p += kWave) {
@@ -76,21 +78,33 @@ __global__ __launch_bounds__(kPlanThreads) void expert_place_kernel(const int32_
         if (e >= 0 && e < experts) atomicAdd(&next[e], 1);
     }
     __syncthreads();
-    // first row of every expert (all chunks), then of this chunk and of each of its waves
+    // every expert's pairs, of all chunks and of those before this one: where there are fewer experts than threads,
+    // several threads an expert share the chunks (a read of the counts is a trip to L2, and they are read in turn)
+    if (single) {
+        for (int e = threadIdx.x; e < experts; e += blockDim.x)
+            for (int w = 0; w < waves; ++w) s_total[e] += s_plan[w * experts + e];
+    } else {
+        const int per = min(1 << bits, static_cast<int>(blockDim.x)), shares = blockDim.x / per;
+        for (int e = threadIdx.x % per; e < experts; e += per) {
+            int32_t total = 0, before = 0;
+#pragma unroll 8
+            for (int c = threadIdx.x / per; c < static_cast<int>(gridDim.x); c += shares) {
+                const int32_t n = counts[static_cast<int64_t>(c) * experts + e];
+                before += c < static_cast<int>(blockIdx.x) ? n : 0;
+                total += n;
+            }
+            atomicAdd(&s_total[e], total);
+            atomicAdd(&s_before[e], before);
+        }
+    }
+    __syncthreads();
+    // first row of every expert, then of this chunk and of each of its waves
     for (int e0 = 0; e0 < experts; e0 += blockDim.x) {
         const int e = e0 + threadIdx.x;
         int32_t total = 0, before = 0;
         if (e < experts) {
-            if (single) {
-                for (int w = 0; w < waves; ++w) total += s_plan[w * experts + e];
-            } else {
-#pragma unroll 8
-                for (int c = 0; c < static_cast<int>(gridDim.x); ++c) {
-                    const int32_t n = counts[static_cast<int64_t>(c) * experts + e];
-                    before += c < static_cast<int>(blockIdx.x) ? n : 0;
-                    total += n;
-                }
-            }
+            total = s_total[e];
+            before = s_before[e];
         }
         const int32_t sum = wave_inclusive_sum(total);
         if (lane == kWave - 1) s_wave[wave] = sum;
@@ -380,7 +394,7 @@ extern "C" gs_status gs_expert_plan(const int32_t *ids, int64_t tokens, int64_t 
                            ids, n, chunk, experts, counts);
         GS_LAUNCH_TRY("expert_count_kernel");
     }
-    const size_t lds = static_cast<size_t>(threads / kWave) * static_cast<size_t>(experts) * sizeof(int32_t);
+    const size_t lds = static_cast<size_t>(threads / kWave + 2) * static_cast<size_t>(experts) * sizeof(int32_t);
     if (lds + 1024 > 65536)
         GS_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(expert_place_kernel),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds)));
