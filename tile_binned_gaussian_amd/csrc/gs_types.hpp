@@ -29,11 +29,13 @@ __device__ __forceinline__ typename Pack<T>::V load_pack(const T *__restrict__ r
 
 // The same for rows of a pack at least, in two parts. A pack that the row's end cuts, or that lies past it, is read to end
 // with the row, so that every lane's load is the same and none waits; end_pack, where the values are first needed,
-// shifts it to its place. Rows of whole packs (a uniform branch) skip that.
-template <typename T>
+// shifts it to its place. Rows of whole packs (a uniform branch) skip that. ONCE: read this one time, and kept from
+// taking room in the caches.
+template <bool ONCE = false, typename T>
 __device__ __forceinline__ typename Pack<T>::V read_pack(const T *__restrict__ row, int col, int dim) {
     const int last = dim - Pack<T>::kN;
-    return *reinterpret_cast<const typename Pack<T>::VU *>(row + (col < last ? col : last));
+    const auto *from = reinterpret_cast<const typename Pack<T>::VU *>(row + (col < last ? col : last));
+    return ONCE ? __builtin_nontemporal_load(from) : *from;
 }
 template <typename T>
 __device__ __forceinline__ typename Pack<T>::V end_pack(typename Pack<T>::V v, int col, int dim) {

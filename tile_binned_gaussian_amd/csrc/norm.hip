@@ -198,7 +198,8 @@ __global__ __launch_bounds__(row_threads(G)) void norm_bwd_kernel(const T *__res
     int turn = 0;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
     int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + group;
-    // the next row is on its way while one is worked on: too few rows are in flight on a CU otherwise
+    // The next row is on its way while one is worked on: too few rows are in flight on a CU otherwise. Rows pass the
+    // caches by (16384 x 4096 float32 127 us, through them 147; the forward, with one array less, is faster through them).
     typename Pack<T>::V px[V], pg[V];
     float pm = 0.0f, pr = 0.0f;
     const auto fetch = [&](int64_t at) {
@@ -207,8 +208,8 @@ __global__ __launch_bounds__(row_threads(G)) void norm_bwd_kernel(const T *__res
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int col = (v * G + lane) * N;
-            px[v] = read_pack(x + at * dim, col, dim);
-            pg[v] = read_pack(grad_y + at * dim, col, dim);
+            px[v] = read_pack<true>(x + at * dim, col, dim);
+            pg[v] = read_pack<true>(grad_y + at * dim, col, dim);
         }
     };
     if (r < rows) fetch(r);
