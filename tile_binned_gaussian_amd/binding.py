@@ -657,11 +657,12 @@ def gs_layer_norm_fwd(x, weight, bias=None, eps=1e-5, stats=True, out=None, stre
     pb = None if bias is None else _arg(bias, "bias", weight.dtype, dev, (dim,))
     shape = x.shape[:-1]
     if out is None:
-        out = LayerNorm(torch.empty_like(x),
-                        torch.empty(shape, dtype=torch.float32, device=dev) if stats else None,
-                        torch.empty(shape, dtype=torch.float32, device=dev) if stats else None)
-        py = out.y.data_ptr()
-        pm, pr = (out.mean.data_ptr(), out.rstd.data_ptr()) if stats else (None, None)
+        y, mean, rstd, pm, pr = torch.empty_like(x), None, None, None, None
+        if stats:
+            mean = torch.empty(shape, dtype=torch.float32, device=dev)
+            rstd = torch.empty_like(mean)
+            pm, pr = mean.data_ptr(), rstd.data_ptr()
+        out, py = LayerNorm(y, mean, rstd), y.data_ptr()
     else:
         py, pm, pr = _arg(out.y, "y", x.dtype, dev, x.shape), None, None
         if (out.mean is None) != (out.rstd is None):
@@ -729,7 +730,9 @@ def gs_expert_plan(ids, experts, out=None, stream=None, workspace=None) -> Exper
     """The (token, choice) pairs of ids [tokens, choices] int32 in stable order of their expert; an id outside
     [0, experts) drops its pair."""
     lib = load_library()
-    _req(ids, "ids", torch.int32)
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    pi = _arg(ids, "ids", torch.int32, ids.device, ids.shape)
     if ids.dim() != 2 or ids.shape[1] < 1:
         raise ValueError("ids must be [tokens, choices]")
     dev = ids.device
@@ -737,15 +740,14 @@ def gs_expert_plan(ids, experts, out=None, stream=None, workspace=None) -> Exper
     if E < 1:
         raise ValueError("experts must be >= 1")
     if out is None:
-        out = ExpertPlan(torch.empty(E + 1, dtype=torch.int32, device=dev), torch.empty_like(ids),
-                         torch.empty(T * K, dtype=torch.int32, device=dev))
+        out = ExpertPlan(ids.new_empty(E + 1), torch.empty_like(ids), ids.new_empty(T * K))
         po, pr, pp = out.offsets.data_ptr(), out.rows.data_ptr(), out.pairs.data_ptr()
     else:
         po = _arg(out.offsets, "offsets", torch.int32, dev, (E + 1,))
         pr, pp = _arg(out.rows, "rows", torch.int32, dev, (T, K)), _arg(out.pairs, "pairs", torch.int32, dev, (T * K,))
     ws, pws, room = _room(lib.gs_expert_plan_workspace_bytes(T, K, E), dev) if workspace is None \
         else _given_room(workspace, dev)
-    _check(lib.gs_expert_plan(ids.data_ptr(), T, K, E, po, pr, pp, pws, room, _stream_int(stream)))
+    _check(lib.gs_expert_plan(pi, T, K, E, po, pr, pp, pws, room, _stream_int(stream)))
     return out
 
 
@@ -760,7 +762,7 @@ def gs_expert_dispatch(x, plan, out=None, stream=None):
         raise ValueError(f"x must be [{T}, dim] (got {tuple(x.shape)})")
     px, D = _arg(x, "x", x.dtype, dev, x.shape), x.shape[1]
     if out is None:
-        out = torch.empty((T * K, D), dtype=x.dtype, device=dev)
+        out = x.new_empty((T * K, D))
     else:
         _arg(out, "sent", x.dtype, dev, (T * K, D))
     _check(lib.gs_expert_dispatch(px, po, pr, T, K, E, D, code, out.data_ptr(), _stream_int(stream)))
@@ -784,7 +786,7 @@ def gs_expert_combine(source, plan, weights=None, out=None, stream=None):
     ps = _arg(source, "source", source.dtype, dev, source.shape)
     pw = None if weights is None else _arg(weights, "weights", torch.float32, dev, (T, K))
     if out is None:
-        out = torch.empty((T, D), dtype=source.dtype, device=dev)
+        out = source.new_empty((T, D))
     else:
         _arg(out, "y", source.dtype, dev, (T, D))
     _check(lib.gs_expert_combine(ps, pr, pw, T, K, D, code, out.data_ptr(), _stream_int(stream)))
