@@ -4,6 +4,10 @@
 // Every row operation walks the tokens, not the sorted rows: a token's own row (x in the dispatch, the output
 // gradient in the combine's backward) is read once for all of its choices, and the sorted rows, which are the bulk of
 // the bytes, are each read or written once. No atomics on memory: results do not depend on the order of workgroups.
+//
+// All of it is bound by memory. 32768 tokens, 8 choices of 64 experts, rows of 2048 bf16 (2.4 GB): plan 13 us, dispatch
+// 208 to 230 us (5.3 to 5.8 TB/s), combine 207 us (5.8 TB/s, what plain reads reach); 16384 x 2 rows of 4096 bf16: combine's
+// backward 128 us (5.1 TB/s). A large copy runs at 4.8 TB/s. Few tokens are three launches of 3 to 4 us each.
 #include "gs_types.hpp"
 
 namespace gs {
@@ -16,7 +20,9 @@ constexpr int kMaxExperts = 4096;
 constexpr int kPlanThreads = 1024;   // up to kWideExperts experts
 constexpr int kWideThreads = 256;    // above: one LDS counter per expert and wave has to fit
 constexpr int kWideExperts = 1024;
-constexpr int64_t kPlanAlone = 4096;  // pairs that one workgroup takes alone, in one launch
+// Pairs that one workgroup takes alone, in one launch: 4096 pairs of 8 to 256 experts 7.1 to 8.8 us in one launch and 7.3
+// to 7.9 in two, whose second costs the host 3.5 us more; 8192 pairs 10.4 to 13.4 us alone, 8.4 to 9.1 in two.
+constexpr int64_t kPlanAlone = 4096;
 constexpr int64_t kPlanChunks = 256;  // workgroups, at most
 
 // Pairs of a workgroup: one step of its threads, or what 256 workgroups need.
@@ -283,7 +289,9 @@ __global__ __launch_bounds__(kRowThreads) void expert_combine_kernel(const T *__
     }
 }
 
-// One wave a token, all of its columns in turn: the dot products need whole rows.
+// One wave a token, all of its columns in turn: the dot products need whole rows. The choices follow each other: the
+// token's gradient comes from L1 for all but the first, and with several choices' rows under way at once fewer waves fit
+// (16384 x 2 rows of 4096 bf16, with its combine: 208 us, four at once 257, two at once 211).
 template <typename T, int V>
 __global__ __launch_bounds__(kRowThreads) void expert_combine_bwd_kernel(
     const T *__restrict__ source, const int32_t *__restrict__ kept, const int32_t *__restrict__ rows,
@@ -340,7 +348,8 @@ gs_status check_rows(const char *name, int64_t tokens, int64_t choices, int expe
     return GS_OK;
 }
 
-// Packs a lane holds at once, and the parts of a row that make.
+// Packs a lane holds at once, and the parts of a row that make: as many as the row has, up to four, so that a token's
+// whole row is under way at once (32768 x 8 rows of 2048 bf16 with four packs 507 us, with two 528, with one 533).
 inline int row_packs(int64_t dim, int pack) {
     const int64_t packs = (dim + pack - 1) / pack;
     return packs <= kWave ? 1 : packs <= 2 * kWave ? 2 : 4;

@@ -3,6 +3,10 @@
 // float32 has no matrix-core rate to speak of next to float16's (157 against 2500 TFLOP/s), so every operand is held
 // as a pair of float16, high and low part (22 bits together), and a product of two operands is three matrix products,
 // high high + high low + low high, summed in float32. The term left out is 2^-22 of the product.
+// The time of large matrices is the products' (4096 x 4096 bf16: all but 0.05 of 2.1 ms), at the rate of this card's large
+// float16 library product, 1.2 PFLOP/s: 1.27 with both halves, 1.0 with the high halves alone, and the card's clock falls
+// to 1.7 GHz under either. Small and middling ones are launches and the latency of their chains.
+//
 // X holds values scaled by 2^12 and the Gram side by 2^10: entries of X are at most its largest singular value, and
 // the scale keeps the low parts of the smallest ones out of float16's subnormals.
 #include <type_traits>
@@ -65,7 +69,7 @@ __device__ __forceinline__ double workgroup_sum(double v, double *s_part) {
     return v;
 }
 
-// Partial sums of squares of matrix blockIdx.y in float64.
+// Partial sums of squares of matrix blockIdx.y in float64. 4096 x 4096 bf16: 13 us (2.6 TB/s; the float64 sums take as long).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_norm_kernel(const T *__restrict__ update, int64_t count,
                                                               double *__restrict__ partial) {
@@ -87,7 +91,7 @@ __global__ __launch_bounds__(kThreads) void ortho_norm_kernel(const T *__restric
 }
 
 // X = update / (norm + eps) in both orders: `direct` holds the update's rows, `turned` its columns; 64 x 64 elements
-// a workgroup, zeros in the padding.
+// a workgroup, zeros in the padding. Bound by memory: 4096 x 4096 bf16 33 us for 168 MB (5.0 TB/s).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restrict__ update,
                                                                const double *__restrict__ partial, int parts, int m,
@@ -319,11 +323,13 @@ __device__ __forceinline__ void finish_four(const ProductArgs &a, size_t batch, 
 // A workgroup of WR x WC waves makes a T x T tile, each wave its part of it. PRODUCTS = 3: both halves of the operands
 // (high high + high low + low high); 1: the high halves alone. A stage of the LDS ring holds 32 columns of the high
 // halves, or 16 of both; while one is multiplied the next is there already (its first operands are read ahead of the
-// barrier) and the others are on their way: two of up to 32 KB, or six of the smallest tile's 8 KB, which few
-// workgroups have to themselves and whose time is the memory's latency.
-template <int T, int PRODUCTS, int kStages, int WR, int WC>
-__global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (T <= 128 && kStages == 4 ? 2 : 1)) void ortho_product_kernel(
-    ProductArgs a) {
+// barrier) and two more are on their way.
+// Two or three waves a SIMD, so that one has products to issue where another waits at the barrier: 8 x 1024 x 1024 bf16
+// 542 us, with one wave a SIMD 581. The reads of LDS that smaller parts cost are a third of its rate. With 16 waves, six or
+// eight stages, or the other way round of the waves it is the same within 2%.
+template <int T, int PRODUCTS, int WR, int WC>
+__global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (T <= 128 ? 2 : 1)) void ortho_product_kernel(ProductArgs a) {
+    constexpr int kStages = 4;
     constexpr int kPanels = T / kPanel;
     constexpr int FR = kPanels / WR, FC = kPanels / WC;  // 32 x 32 results of a wave, each way
     static_assert(FR * WR == kPanels && FC * WC == kPanels, "whole results");
@@ -451,7 +457,8 @@ __global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (T <= 128 && kStages ==
 }
 
 // A 64 x 64 tile by WAVES waves that share its sum: each takes its own range of the columns, for the whole tile, with
-// operands straight from memory into registers, whose order a block has. No wave waits for another until the sums
+// operands straight from memory into registers, whose order a block has (2500 x 1111 f32: 322 us next to 341 with these tiles
+// through LDS in eight stages; 171 tiles of depth 2528 take 21 us, 13 TB/s out of L2). No wave waits for another until the sums
 // are joined through LDS, in order, so the time of a few tiles is not the latency of a barrier at every stage.
 template <int PRODUCTS, int WAVES>
 __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(ProductArgs a) {
@@ -575,6 +582,9 @@ __global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, int m,
 
 // ------------------------------------------------------------------------------------------------------------
 // small matrices: one workgroup a matrix, all steps in one launch
+//
+// 16 x 96 x 160 f32 36 us, as launches of the kernels above 95; 128 x 128 45 and 99, 32 x 1000 28 and 87. A step is 7 us: six
+// phases with a barrier each, of which the products take 2 and the operands out of LDS about as much.
 //
 // The 32 x 32 tiles of X are dealt to 16 waves, which keep theirs in float32 registers as the matrix cores leave a
 // result (lane: column lane % 32; register 4 g + k: row 8 g + lane / 32 * 4 + k). Once a step every wave puts its
@@ -871,7 +881,9 @@ gs_status check_sizes(int64_t batch, int64_t m, int64_t n) {
 constexpr int kUnits = 256;  // compute units
 
 // The tile edge of a product: least rounds of workgroups over the chip, times a tile's work, times what a tile of
-// that edge takes of the matrix cores' time next to the largest (its operands come through LDS more often).
+// that edge takes of the matrix cores' time next to the largest (its operands come through L2 and LDS more often). Measured
+// at depth 4096 with both halves, a round of tiles on all units: 324 us at 256, 196 at 192 (1.08 times the time of an
+// entry), about 75 at 128 (1.3) and 31 at 64 (2).
 int tile_edge(int64_t batch, int rows, int cols, bool symmetric) {
     int best = 0;
     double least = 0.0;
@@ -898,24 +910,20 @@ gs_status product(ProductArgs g, int64_t batch, int products, hipStream_t stream
     const dim3 grid(static_cast<unsigned>(g.symmetric ? g.tile_rows * (g.tile_rows + 1) / 2
                                                       : g.tile_rows * g.tile_cols),
                     static_cast<unsigned>(batch));
-    const bool alone = static_cast<int64_t>(grid.x) * batch <= kUnits;
-#define GS_PRODUCT(T, STAGES, WR, WC, when)                                                                          \
-    if (edge == T && (when)) {                                                                                       \
-        if (products == 1)                                                                                           \
-            hipLaunchKernelGGL((ortho_product_kernel<T, 1, STAGES, WR, WC>), grid, dim3(WR * WC * kWave), 0, stream, \
-                               g);                                                                                   \
-        else                                                                                                         \
-            hipLaunchKernelGGL((ortho_product_kernel<T, 3, STAGES, WR, WC>), grid, dim3(WR * WC * kWave), 0, stream, \
-                               g);                                                                                   \
+#define GS_PRODUCT(T, WR, WC)                                                                                       \
+    if (edge == T) {                                                                                               \
+        if (products == 1)                                                                                         \
+            hipLaunchKernelGGL((ortho_product_kernel<T, 1, WR, WC>), grid, dim3(WR * WC * kWave), 0, stream, g);   \
+        else                                                                                                       \
+            hipLaunchKernelGGL((ortho_product_kernel<T, 3, WR, WC>), grid, dim3(WR * WC * kWave), 0, stream, g);   \
     }
     if (edge == 64 && products == 1)
         hipLaunchKernelGGL((ortho_product_direct_kernel<1, 8>), grid, dim3(8 * kWave), 0, stream, g);
     if (edge == 64 && products == 3)
         hipLaunchKernelGGL((ortho_product_direct_kernel<3, 8>), grid, dim3(8 * kWave), 0, stream, g);
-    GS_PRODUCT(128, 6, 4, 2, alone)
-    GS_PRODUCT(128, 4, 4, 2, !alone)
-    GS_PRODUCT(192, 4, 6, 2, true)
-    GS_PRODUCT(256, 4, 2, 4, true)
+    GS_PRODUCT(128, 4, 2)
+    GS_PRODUCT(192, 6, 2)
+    GS_PRODUCT(256, 2, 4)
 #undef GS_PRODUCT
     GS_LAUNCH_TRY("ortho_product_kernel");
     return GS_OK;
