@@ -75,10 +75,9 @@ __device__ __forceinline__ void row_sums(float &a, float &b, float2 *slot) {
 constexpr int fwd_waves(int columns) { return columns > 8 ? 6 : 8; }
 
 template <typename T, typename W, int G, int V>
-__global__ __launch_bounds__(row_threads(G), fwd_waves(V * Pack<T>::kN)) void norm_fwd_kernel(const T *__restrict__ x, const W *__restrict__ weight,
-                                                            const W *__restrict__ bias, int64_t rows, int dim,
-                                                            float eps, T *__restrict__ y, float *__restrict__ mean,
-                                                            float *__restrict__ rstd) {
+__global__ __launch_bounds__(row_threads(G), fwd_waves(V * Pack<T>::kN)) void norm_fwd_kernel(
+    const T *__restrict__ x, const W *__restrict__ weight, const W *__restrict__ bias, int64_t rows, int dim, float eps,
+    T *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd) {
     constexpr int N = Pack<T>::kN, kRows = row_threads(G) / G;
     __shared__ float s_sum[2][row_threads(G) / kWave];
     const int lane = threadIdx.x % G;

@@ -69,7 +69,7 @@ __device__ __forceinline__ double workgroup_sum(double v, double *s_part) {
     return v;
 }
 
-// Partial sums of squares of matrix blockIdx.y in float64. 4096 x 4096 bf16: 13 us (2.6 TB/s; the float64 sums take as long).
+// Partial sums of squares of matrix blockIdx.y in float64. 4096 x 4096 bf16: 13 us (2.6 TB/s), 0.6% of the call.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_norm_kernel(const T *__restrict__ update, int64_t count,
                                                               double *__restrict__ partial) {
