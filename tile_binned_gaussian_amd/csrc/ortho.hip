@@ -51,10 +51,20 @@ __device__ __forceinline__ size_t eight_at(int row, int col, int rows) {
 template <int N, typename H>
 __device__ __forceinline__ void split(const float *v, H &hi, H &lo) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        hi[j] = static_cast<_Float16>(v[j]);
-        lo[j] = static_cast<_Float16>(v[j] - static_cast<float>(hi[j]));
+    for (int j = 0; j < N; ++j) hi[j] = static_cast<_Float16>(v[j]);
+    // pairs are rounded together and stay packed: seen through, each would be rounded once more by itself
+    typedef uint32_t Words __attribute__((ext_vector_type(N / 2)));
+    Words w = __builtin_bit_cast(Words, hi);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+        uint32_t word = w[j];
+        asm volatile("" : "+v"(word));
+        w[j] = word;
     }
+    hi = __builtin_bit_cast(H, w);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        lo[j] = static_cast<_Float16>(__builtin_fmaf(static_cast<float>(hi[j]), -1.0f, v[j]));
 }
 
 // The sum over the workgroup's threads, in every thread.
@@ -583,8 +593,9 @@ __global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, int m,
 // ------------------------------------------------------------------------------------------------------------
 // small matrices: one workgroup a matrix, all steps in one launch
 //
-// 16 x 96 x 160 f32 36 us, as launches of the kernels above 95; 128 x 128 45 and 99, 32 x 1000 28 and 87. A step is 7 us: six
-// phases with a barrier each, of which the products take 2 and the operands out of LDS about as much.
+// 16 x 96 x 160 f32 30 us, as launches of the kernels above 95; 128 x 128 37 and 99, 32 x 1000 27 and 87. A step is 5.4 us: six
+// phases with a barrier each. A SIMD's vector instructions take 60% of it (halves and addresses) and its matrix products
+// 30%; LDS is busy a third of the time, without bank conflicts (with them, and addresses formed in full: 36 us).
 //
 // The 32 x 32 tiles of X are dealt to 16 waves, which keep theirs in float32 registers as the matrix cores leave a
 // result (lane: column lane % 32; register 4 g + k: row 8 g + lane / 32 * 4 + k). Once a step every wave puts its
@@ -612,37 +623,59 @@ inline bool is_small(int64_t rows, int64_t cols) {
            small_lds(rows, cols) <= kSmallLds;
 }
 
-// Stores this lane's four values (rows g * 8 + lane / 32 * 4 + 0..3 of row block i, one column of column block j) as
-// columns: [columns of the tile][rows of the tile].
-__device__ __forceinline__ void small_store_turned(_Float16 *plane, int panels, int i, int j, int g, int lane,
-                                                   h16x4 v) {
-    *reinterpret_cast<h16x4 *>(plane + ((i * 2 + g / 2) * panels + j) * kBlock + lane * 8 + g % 2 * 4) = v;
+// Element offset in a block of the small kernel's LDS: half h of its columns, row, and the block's own number k of 16
+// columns. Rows are in an order of their own in each half and in odd blocks, so that the transposing load, which reads four
+// rows of both halves of two blocks at once, finds them in different banks.
+__device__ __forceinline__ int small_at(int h, int row, int k) {
+    return (h * kPanel + (row ^ (h * 4) ^ (k % 2 * 8))) * 8;
 }
-// The same values as [rows of the tile][columns of the tile].
-__device__ __forceinline__ void small_store_straight(_Float16 *plane, int panels, int i, int j, int g, int lane,
-                                                     h16x4 v) {
-    const int row = g * 8 + lane / 32 * 4 + lane % 4;
-    *reinterpret_cast<h16x4 *>(plane + ((j * 2 + lane % 32 / 16) * panels + i) * kBlock +
-                               (lane / 4 % 2 * kPanel + row) * 8 + lane / 8 % 2 * 4) = quad_transpose(v);
+
+// Where a lane's accesses lie in a block, in elements, formed once for all steps.
+struct SmallLane {
+    int whole;     // the 16 bytes that a lane stores of a column and reads of an operand, in even blocks
+    int straight;  // the 8 bytes of the four rows from 0 on, after the transpose; its block: k
+    int across;    // the transposing load's 8 bytes, its block: half
+    int k, half;
+};
+__device__ __forceinline__ SmallLane small_lane(int lane) {
+    SmallLane l;
+    l.whole = small_at(lane / 32, lane % 32, 0);
+    l.k = lane % 32 / 16;
+    l.straight = small_at(lane / 4 % 2, lane / 32 * 4 + lane % 4, l.k) + lane / 8 % 2 * 4;
+    const int p = lane % 16, chunk = p % 4;
+    l.half = lane / 16 % 2;
+    l.across = small_at(chunk % 2, lane / 32 * 8 + p / 4, l.half) + chunk / 2 * 4;
+    return l;
+}
+
+// Stores eight of this lane's values (rows t * 16 + lane / 32 * 4 + 0..3 and the four rows 8 on of row block i, one column
+// of column block j) as columns: [columns of the tile][rows of the tile].
+__device__ __forceinline__ void small_store_turned(_Float16 *plane, int panels, int i, int j, int t,
+                                                   const SmallLane &l, h16x8 v) {
+    *reinterpret_cast<h16x8 *>(plane + ((i * 2 + t) * panels + j) * kBlock + (l.whole ^ (t * 64))) = v;
+}
+// Four of the same values, rows g * 8 + lane / 32 * 4 + 0..3, as [rows of the tile][columns of the tile].
+__device__ __forceinline__ void small_store_straight(_Float16 *plane, int panels, int i, int j, int g,
+                                                     const SmallLane &l, h16x4 v) {
+    *reinterpret_cast<h16x4 *>(plane + ((j * 2 + l.k) * panels + i) * kBlock + (l.straight ^ (g * 64))) =
+        quad_transpose(v);
 }
 
 // An operand as it lies in LDS: row block `panel` of a plane, its block k of 16 columns.
-__device__ __forceinline__ h16x8 small_operand(const _Float16 *plane, int panels, int panel, int k, int lane) {
-    return *reinterpret_cast<const h16x8 *>(plane + (k * panels + panel) * kBlock + lane * 8);
+__device__ __forceinline__ h16x8 small_operand(const _Float16 *plane, int panels, int panel, int k,
+                                               const SmallLane &l) {
+    return *reinterpret_cast<const h16x8 *>(plane + (k * panels + panel) * kBlock + (l.whole ^ (k % 2 * 64)));
 }
 
 // An operand across the order in LDS: the rows are the 32 columns of row block i of X, the columns 16 of its columns
 // (half k % 2 of column block k / 2). The transposing load gives each of 16 lanes the values that four of them would
 // have read at its place: lane p reads four rows of column p / 4, and gets row p of four columns.
-__device__ __forceinline__ h16x8 small_operand_turned(const _Float16 *plane, int col_blocks, int i, int k, int lane) {
+__device__ __forceinline__ h16x8 small_operand_turned(const _Float16 *plane, int k, int across, int across4) {
     typedef short s16x4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s16x4 *LdsPtr;
-    const int p = lane % 16, chunk = p % 4;
-    const int col = k % 2 * 16 + lane / 32 * 8 + p / 4;
-    const _Float16 *at = plane + ((i * 2 + lane / 16 % 2) * col_blocks + k / 2) * kBlock +
-                         (chunk % 2 * kPanel + col) * 8 + chunk / 2 * 4;
-    const s16x4 first = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at));
-    const s16x4 second = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at + 4 * 8));
+    const _Float16 *at = plane + k / 2 * kBlock + k % 2 * 128;
+    const s16x4 first = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at + across));
+    const s16x4 second = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at + across4));
     const h16x4 f = __builtin_bit_cast(h16x4, first), s = __builtin_bit_cast(h16x4, second);
     return __builtin_shufflevector(f, s, 0, 1, 2, 3, 4, 5, 6, 7);
 }
@@ -656,7 +689,7 @@ __device__ __forceinline__ f32x16 small_multiply(f32x16 acc, h16x8 ph, h16x8 pl,
 // One step on the workgroup's matrix: x[t] is tile wave + 16 t, row block tile % A, column block tile / A.
 template <int A>
 __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blocks, float a, float b, float c,
-                                           _Float16 *lds, int wave, int lane) {
+                                           _Float16 *lds, int wave, int lane, const SmallLane &l) {
     constexpr int kTri = small_triangle(A), kParts = small_parts(A);
     _Float16 *xh = lds, *xl = xh + col_blocks * 2 * A * kBlock;
     _Float16 *gh = xl + col_blocks * 2 * A * kBlock, *gl = gh + 2 * A * A * kBlock;
@@ -666,14 +699,14 @@ __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blo
         const int tile = wave + t * kSmallWaves;
         if (tile < A * col_blocks)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float v[4];
-                h16x4 h, l;
+            for (int u = 0; u < 2; ++u) {
+                float v[8];
+                h16x8 hi, lo;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = x[t][g * 4 + k];
-                split<4>(v, h, l);
-                small_store_turned(xh, col_blocks, tile % A, tile / A, g, lane, h);
-                small_store_turned(xl, col_blocks, tile % A, tile / A, g, lane, l);
+                for (int k = 0; k < 8; ++k) v[k] = x[t][u * 8 + k];
+                split<8>(v, hi, lo);
+                small_store_turned(xh, col_blocks, tile % A, tile / A, u, l, hi);
+                small_store_turned(xl, col_blocks, tile % A, tile / A, u, l, lo);
             }
     }
     __syncthreads();
@@ -683,12 +716,14 @@ __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blo
     f32x16 gram = {};
     if (part < kParts) {
         const int blocks = col_blocks * 2, to = blocks * (part + 1) / kParts;
+        const int across = l.across + l.half * col_blocks * kBlock, across4 = across ^ 32;
+        const int pi = ti * 2 * col_blocks * kBlock, pj = tj * 2 * col_blocks * kBlock;
 #pragma unroll 2
         for (int k = blocks * part / kParts; k < to; ++k) {
-            const h16x8 ph = small_operand_turned(xh, col_blocks, ti, k, lane);
-            const h16x8 qh = small_operand_turned(xh, col_blocks, tj, k, lane);
-            const h16x8 pl = small_operand_turned(xl, col_blocks, ti, k, lane);
-            const h16x8 ql = small_operand_turned(xl, col_blocks, tj, k, lane);
+            const h16x8 ph = small_operand_turned(xh + pi, k, across, across4);
+            const h16x8 qh = small_operand_turned(xh + pj, k, across, across4);
+            const h16x8 pl = small_operand_turned(xl + pi, k, across, across4);
+            const h16x8 ql = small_operand_turned(xl + pj, k, across, across4);
             gram = small_multiply(gram, ph, pl, qh, ql);
         }
         if (part > 0)
@@ -699,18 +734,22 @@ __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blo
     }
     const auto store = [&](const f32x16 &v16) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            float v[4];
-            h16x4 h, l;
+        for (int u = 0; u < 2; ++u) {
+            float v[8];
+            h16x8 hi, lo;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = v16[g * 4 + k];
-            split<4>(v, h, l);
-            small_store_turned(gh, A, ti, tj, g, lane, h);
-            small_store_turned(gl, A, ti, tj, g, lane, l);
-            if (ti != tj) {
-                small_store_straight(gh, A, ti, tj, g, lane, h);
-                small_store_straight(gl, A, ti, tj, g, lane, l);
-            }
+            for (int k = 0; k < 8; ++k) v[k] = v16[u * 8 + k];
+            split<8>(v, hi, lo);
+            small_store_turned(gh, A, ti, tj, u, l, hi);
+            small_store_turned(gl, A, ti, tj, u, l, lo);
+            if (ti != tj)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    small_store_straight(gh, A, ti, tj, u * 2 + g, l,
+                                         h16x4{hi[g * 4], hi[g * 4 + 1], hi[g * 4 + 2], hi[g * 4 + 3]});
+                    small_store_straight(gl, A, ti, tj, u * 2 + g, l,
+                                         h16x4{lo[g * 4], lo[g * 4 + 1], lo[g * 4 + 2], lo[g * 4 + 3]});
+                }
         }
     };
     if constexpr (kParts > 1) __syncthreads();
@@ -731,10 +770,10 @@ __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blo
     __syncthreads();
     if (part == 0) {
         f32x16 square = {};
-#pragma unroll 2
+#pragma unroll
         for (int k = 0; k < 2 * A; ++k) {
-            const h16x8 ph = small_operand(gh, A, ti, k, lane), qh = small_operand(gh, A, tj, k, lane);
-            const h16x8 pl = small_operand(gl, A, ti, k, lane), ql = small_operand(gl, A, tj, k, lane);
+            const h16x8 ph = small_operand(gh, A, ti, k, l), qh = small_operand(gh, A, tj, k, l);
+            const h16x8 pl = small_operand(gl, A, ti, k, l), ql = small_operand(gl, A, tj, k, l);
             square = small_multiply(square, ph, pl, qh, ql);
         }
 #pragma unroll
@@ -748,12 +787,12 @@ __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blo
         const int tile = wave + t * kSmallWaves;
         if (tile < A * col_blocks) {
             f32x16 acc = {};
-#pragma unroll 2
+#pragma unroll
             for (int k = 0; k < 2 * A; ++k) {
-                const h16x8 ph = small_operand(gh, A, tile % A, k, lane);
-                const h16x8 qh = small_operand(xh, col_blocks, tile / A, k, lane);
-                const h16x8 pl = small_operand(gl, A, tile % A, k, lane);
-                const h16x8 ql = small_operand(xl, col_blocks, tile / A, k, lane);
+                const h16x8 ph = small_operand(gh, A, tile % A, k, l);
+                const h16x8 qh = small_operand(xh, col_blocks, tile / A, k, l);
+                const h16x8 pl = small_operand(gl, A, tile % A, k, l);
+                const h16x8 ql = small_operand(xl, col_blocks, tile / A, k, l);
                 acc = small_multiply(acc, ph, pl, qh, ql);
             }
 #pragma unroll
@@ -798,46 +837,62 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const T *__r
     const int col_blocks = (cols + kPanel - 1) / kPanel;
     const size_t base = blockIdx.x * (static_cast<size_t>(rows) * cols);
     const int row_step = tall ? 1 : cols, col_step = tall ? rows : 1;
-    // the offset of register e of tile t for lane l
+    // the offset of register e of tile t for lane l: in a wide matrix a row past the last one is past the end by itself
     const auto offset = [=](int l, int t, int e) {
         const int tile = wave + t * kSmallWaves;
-        const int row = tile % A * kPanel + e / 4 * 8 + l / 32 * 4 + e % 4, col = tile / A * kPanel + l % 32;
-        const int at = row * row_step + col * col_step;
-        return row < rows && col < cols ? at : 1 << 28;
+        const int row = tile % A * kPanel + l / 32 * 4, col = tile / A * kPanel + l % 32, down = e / 4 * 8 + e % 4;
+        const int first = col < cols ? row * row_step + col * col_step : 1 << 28;
+        const int at = first + down * row_step;
+        return tall && row + down >= rows ? 1 << 28 : at;
     };
+    const auto has = [=](int t) { return wave + t * kSmallWaves < A * col_blocks; };  // tile t of this wave
     f32x16 x[kSmallTurns];
     const Buffer<T> from(update + base, rows * cols);
 #pragma unroll
-    for (int t = 0; t < kSmallTurns; ++t)
+    for (int t = 0; t < kSmallTurns; ++t) {
+        x[t] = f32x16{};
+        if (has(t))
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[t][e] = from.load(offset(lane, t, e));
+            for (int e = 0; e < 16; ++e) x[t][e] = from.load(offset(lane, t, e));
+    }
     double sum = 0.0;
 #pragma unroll
     for (int t = 0; t < kSmallTurns; ++t)
+        if (has(t))
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const double v = static_cast<double>(x[t][e]);
-            sum = __builtin_fma(v, v, sum);
-        }
+            for (int e = 0; e < 16; ++e) {
+                const double v = static_cast<double>(x[t][e]);
+                sum = __builtin_fma(v, v, sum);
+            }
 #pragma unroll
     for (int d = kWave / 2; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
     if (lane == 0) s_sum[wave] = sum;
     __syncthreads();
     sum = 0.0;
     for (int w = 0; w < kSmallWaves; ++w) sum += s_sum[w];
-    const double scale = static_cast<double>(kScaleX) / (sqrt(sum) + static_cast<double>(eps));
+    // the power of two first, which rounds nothing that counts next to the norm: no scale leaves float32's range
+    int exponent;
+    const float mantissa = static_cast<float>(
+        frexp(static_cast<double>(kScaleX) / (sqrt(sum) + static_cast<double>(eps)), &exponent));
 #pragma unroll
     for (int t = 0; t < kSmallTurns; ++t)
+        if (has(t))
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[t][e] = static_cast<float>(static_cast<double>(x[t][e]) * scale);
-    for (int k = 0; k < steps; ++k) small_step<A>(x, col_blocks, a, b, c, s_small, wave, lane);
+            for (int e = 0; e < 16; ++e) x[t][e] = ldexpf(x[t][e], exponent) * mantissa;
+    SmallLane at = small_lane(lane);
+    for (int k = 0; k < steps; ++k) {
+        // addresses formed anew from these in every step: kept, they would not fit the registers
+        asm volatile("" : "+v"(at.whole), "+v"(at.straight), "+v"(at.across));
+        small_step<A>(x, col_blocks, a, b, c, s_small, wave, lane, at);
+    }
     const Buffer<T> to(out + base, rows * cols);
     int late = lane;  // offsets formed anew: kept from the loads they would take 32 registers all along
     asm volatile("" : "+v"(late));
 #pragma unroll
     for (int t = 0; t < kSmallTurns; ++t)
+        if (has(t))
 #pragma unroll
-        for (int e = 0; e < 16; ++e) to.store(offset(late, t, e), x[t][e] * (1.0f / kScaleX));
+            for (int e = 0; e < 16; ++e) to.store(offset(late, t, e), x[t][e] * (1.0f / kScaleX));
 }
 
 inline int64_t padded(int64_t v) { return (v + kPanel - 1) / kPanel * kPanel; }
