@@ -145,3 +145,34 @@ def test_a_large_matrix_on_the_device():
         # float32: 15 products of 2^-22 and less, grown by at most a few; bfloat16: the result's own 2^-9 and the
         # first steps' 2^-12, grown likewise
         assert ((got - x).norm() / x.norm()).item() <= room
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(64, 3001), (300, 4000), (4100, 200), (2, 130, 5000), (33, 20011), (500, 2100)])
+def test_few_tiles_of_many_columns(shape, name):
+    """Workgroups share a tile's sum: right, and the same bits again, from a workspace full of anything and in a graph."""
+    u = momentum(shape, tu.DTYPES[name], sum(shape))
+    d = u.cuda()
+    got = binding.gs_orthogonalize(d)
+    for i in range(shape[0] if len(shape) == 3 else 1):
+        check(u[i], got[i]) if len(shape) == 3 else check(u, got)
+    batch = shape[0] if len(shape) == 3 else 1
+    room = binding.load_library().gs_orthogonalize_workspace_bytes(batch, *shape[-2:])
+    ws = torch.full((room,), 255, dtype=torch.uint8, device="cuda")
+    assert torch.equal(binding.gs_orthogonalize(d, workspace=ws), got)
+    out = torch.empty_like(d)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.gs_orthogonalize(d, out=out, workspace=ws)
+    for _ in range(3):
+        out.zero_()
+        ws.fill_(170)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got)
+
+
+def test_shared_tiles_with_high_halves_alone():
+    u = momentum((770, 2000), torch.bfloat16, 5)
+    check(u, binding.gs_orthogonalize(u.cuda()))

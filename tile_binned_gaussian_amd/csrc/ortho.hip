@@ -169,6 +169,9 @@ struct ProductArgs {
     void *out;
     int out_type, out_rows, out_cols;
     int out_turned;   // its rows are the product's columns
+    // few tiles of many columns: workgroups that share a tile's sum, and their parts of it [tile][split][64 x 64]
+    int splits;
+    float *parts;
 };
 
 // One block from memory to LDS, 16 bytes a lane, without registers in between. lds: byte address, the same in the
@@ -466,11 +469,31 @@ __global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (T <= 128 ? 2 : 1)) voi
     }
 }
 
+// Of a 64 x 64 tile: its panel i's group of four rows wave % 4 in its column panel wave / 4, as eight waves finish it.
+__device__ __forceinline__ Four load_part_four(const ProductArgs &a, size_t batch, int ti, int tj, int i, int wave,
+                                               int lane) {
+    const int mp = ti * 2 + i, np = tj * 2 + wave / 4, rows = a.rows / kPanel, cols = a.cols / kPanel;
+    return load_four(a, four_at(a, batch, mp < rows ? mp : rows - 1, np < cols ? np : cols - 1, wave % 4, lane));
+}
+__device__ __forceinline__ void finish_part_four(const ProductArgs &a, size_t batch, int ti, int tj, int i, int wave,
+                                                 int lane, f32x4 sum, const Four &add, bool both) {
+    float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+    const int mp = ti * 2 + i, np = tj * 2 + wave / 4;
+    if (mp < a.rows / kPanel && np < a.cols / kPanel)
+        finish_four(a, batch, mp, np, wave % 4, v, add, lane, both);
+}
+__device__ __forceinline__ f32x4 *part_at(const ProductArgs &a, size_t tile, int split, int i, int wave, int lane) {
+    return reinterpret_cast<f32x4 *>(a.parts) + ((tile * a.splits + split) * 16 + i * 8 + wave) * kWave + lane;
+}
+
 // A 64 x 64 tile by WAVES waves that share its sum: each takes its own range of the columns, for the whole tile, with
 // operands straight from memory into registers, whose order a block has (2500 x 1111 f32: 322 us next to 341 with these tiles
 // through LDS in eight stages; 171 tiles of depth 2528 take 21 us, 13 TB/s out of L2). No wave waits for another until the sums
 // are joined through LDS, in order, so the time of a few tiles is not the latency of a barrier at every stage.
-template <int PRODUCTS, int WAVES>
+// Where there are few tiles, several workgroups share one's columns, because a unit draws only so much from L2 (300 x 4000:
+// 15 tiles by 15 units 24 us). Each leaves its part in memory for the kernel that joins them. (Joined by the last workgroup
+// to come, a call was slower than without: making the parts visible to it costs every unit its L2.)
+template <int PRODUCTS, int WAVES, bool SHARED>
 __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(ProductArgs a) {
     constexpr int kTile = 64, kPanels = kTile / kPanel;
     constexpr int PL = PRODUCTS == 1 ? 1 : 2;
@@ -480,7 +503,12 @@ __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(Prod
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
     const size_t batch = blockIdx.y;
     const int row_panels = a.rows / kPanel, col_panels = a.cols / kPanel, blocks = a.depth / kDepth;
-    const int from = blocks * wave / WAVES, to = blocks * (wave + 1) / WAVES;
+    int first = 0, mine = blocks;  // the workgroup's blocks
+    if (SHARED) {
+        first = blocks * static_cast<int>(blockIdx.z) / a.splits;
+        mine = blocks * static_cast<int>(blockIdx.z + 1) / a.splits - first;
+    }
+    const int from = first + mine * wave / WAVES, to = first + mine * (wave + 1) / WAVES;
     const _Float16 *src[2][PL][kPanels];
 #pragma unroll
     for (int op = 0; op < 2; ++op)
@@ -543,11 +571,7 @@ __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(Prod
     const bool both = !a.symmetric || ti != tj;
     Four add[kPanels];
 #pragma unroll
-    for (int i = 0; i < kPanels; ++i) {
-        const int mp = ti * kPanels + i, np = tj * kPanels + wave / 4;
-        add[i] = load_four(a, four_at(a, batch, mp < row_panels ? mp : row_panels - 1,
-                                      np < col_panels ? np : col_panels - 1, wave % 4, lane));
-    }
+    for (int i = 0; i < kPanels; ++i) add[i] = load_part_four(a, batch, ti, tj, i, wave, lane);
 #pragma unroll
     for (int i = 0; i < kPanels; ++i) {
         if (i > 0) __syncthreads();
@@ -562,10 +586,24 @@ __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(Prod
         f32x4 sum = s_sum[0][wave][lane];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) sum += s_sum[w][wave][lane];
-        float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-        const int mp = ti * kPanels + i, np = tj * kPanels + wave / 4;
-        if (mp < row_panels && np < col_panels) finish_four(a, batch, mp, np, wave % 4, v, add[i], lane, both);
+        if (SHARED)
+            *part_at(a, batch * gridDim.x + blockIdx.x, blockIdx.z, i, wave, lane) = sum;
+        else
+            finish_part_four(a, batch, ti, tj, i, wave, lane, sum, add[i], both);
     }
+}
+
+// The sums of a tile that workgroups shared, their parts added in order: half a tile a workgroup.
+__global__ __launch_bounds__(8 *kWave) void ortho_join_kernel(ProductArgs a) {
+    int ti, tj;
+    tile_of(a, ti, tj);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave, i = blockIdx.z;
+    const size_t batch = blockIdx.y, tile = batch * gridDim.x + blockIdx.x;
+    const Four add = load_part_four(a, batch, ti, tj, i, wave, lane);
+    f32x4 sum = *part_at(a, tile, 0, i, wave, lane);
+#pragma unroll 4
+    for (int p = 1; p < a.splits; ++p) sum += *part_at(a, tile, p, i, wave, lane);
+    finish_part_four(a, batch, ti, tj, i, wave, lane, sum, add, !a.symmetric || ti != tj);
 }
 
 // out [batch][m][n] from the planes that hold its rows, where there are no steps.
@@ -594,8 +632,8 @@ __global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, int m,
 // small matrices: one workgroup a matrix, all steps in one launch
 //
 // 16 x 96 x 160 f32 30 us, as launches of the kernels above 95; 128 x 128 37 and 99, 32 x 1000 27 and 87. A step is 5.4 us: six
-// phases with a barrier each. A SIMD's vector instructions take 60% of it (halves and addresses) and its matrix products
-// 30%; LDS is busy a third of the time, without bank conflicts (with them, and addresses formed in full: 36 us).
+// phases with a barrier each. A SIMD's vector instructions take half of it (halves and addresses) and its matrix products
+// a third; LDS is busy a third of the time, without bank conflicts (with them, and addresses formed in full: 36 us).
 //
 // The 32 x 32 tiles of X are dealt to 16 waves, which keep theirs in float32 registers as the matrix cores leave a
 // result (lane: column lane % 32; register 4 g + k: row 8 g + lane / 32 * 4 + k). Once a step every wave puts its
@@ -897,11 +935,29 @@ __global__ __launch_bounds__(kSmallThreads) void ortho_small_kernel(const T *__r
 
 inline int64_t padded(int64_t v) { return (v + kPanel - 1) / kPanel * kPanel; }
 
+constexpr int kUnits = 256;  // compute units
+
 struct Layout {
     double *partial;
+    float *parts;
     Planes x, xt[2], gram, poly;
     size_t bytes;
 };
+
+int tile_edge(int64_t batch, int rows, int cols, bool symmetric);
+
+// Workgroups that share the sum of each tile of edge 64: as many as leave no unit without one, with four blocks or more
+// for each wave. 300 x 4000 f32: with shared tiles 184 us, without 240; 512 x 4000 208 and 258; 64 x 3000 bf16 115 and 142. By two the second
+// launch eats what it gives.
+int tile_splits(int64_t tiles, int depth) {
+    const int64_t most = kUnits / tiles, work = depth / kDepth / 32;
+    const int64_t n = most < work ? most : work;
+    return n < 3 ? 1 : n > 16 ? 16 : static_cast<int>(n);
+}
+int64_t tile_count(int64_t batch, int rows, int cols, int edge, bool symmetric) {
+    const int64_t r = (rows + edge - 1) / edge, c = (cols + edge - 1) / edge;
+    return batch * (symmetric ? r * (r + 1) / 2 : r * c);
+}
 
 Layout lay_out(void *workspace, int64_t batch, int64_t m, int64_t n) {
     const int64_t M = m < n ? m : n, N = m < n ? n : m;
@@ -910,6 +966,11 @@ Layout lay_out(void *workspace, int64_t batch, int64_t m, int64_t n) {
     Carver c(workspace);
     Layout l;
     l.partial = c.take<double>(static_cast<size_t>(batch) * kNormBlocks);
+    // the Gram product's parts; the others' sums are as long as it has rows, too short to share where tiles are few
+    const int m32 = static_cast<int>(padded(M));
+    const int64_t tiles = tile_count(batch, m32, m32, 64, true);
+    const int splits = tile_edge(batch, m32, m32, true) == 64 ? tile_splits(tiles, static_cast<int>(padded(N))) : 1;
+    l.parts = c.take<float>(splits > 1 ? static_cast<size_t>(tiles) * splits * 64 * 64 : 0);
     const auto planes = [&c](size_t count) {
         Planes p;
         p.hi = c.take<_Float16>(count);
@@ -933,8 +994,6 @@ gs_status check_sizes(int64_t batch, int64_t m, int64_t n) {
     return GS_OK;
 }
 
-constexpr int kUnits = 256;  // compute units
-
 // The tile edge of a product: least rounds of workgroups over the chip, times a tile's work, times what a tile of
 // that edge takes of the matrix cores' time next to the largest (its operands come through L2 and LDS more often). Measured
 // at depth 4096 with both halves, a round of tiles on all units: 324 us at 256, 196 at 192 (1.08 times the time of an
@@ -947,8 +1006,7 @@ int tile_edge(int64_t batch, int rows, int cols, bool symmetric) {
         double cost;
     } edges[] = {{256, 1.0}, {192, 1.05}, {128, 1.25}, {64, 2.0}};
     for (const auto &e : edges) {
-        const int64_t r = (rows + e.edge - 1) / e.edge, c = (cols + e.edge - 1) / e.edge;
-        const int64_t tiles = batch * (symmetric ? r * (r + 1) / 2 : r * c);
+        const int64_t tiles = tile_count(batch, rows, cols, e.edge, symmetric);
         const double t = static_cast<double>((tiles + kUnits - 1) / kUnits) * e.edge * e.edge * e.cost;
         if (best == 0 || t < least) {
             best = e.edge;
@@ -972,10 +1030,20 @@ gs_status product(ProductArgs g, int64_t batch, int products, hipStream_t stream
         else                                                                                                       \
             hipLaunchKernelGGL((ortho_product_kernel<T, 3, WR, WC>), grid, dim3(WR * WC * kWave), 0, stream, g);   \
     }
-    if (edge == 64 && products == 1)
-        hipLaunchKernelGGL((ortho_product_direct_kernel<1, 8>), grid, dim3(8 * kWave), 0, stream, g);
-    if (edge == 64 && products == 3)
-        hipLaunchKernelGGL((ortho_product_direct_kernel<3, 8>), grid, dim3(8 * kWave), 0, stream, g);
+    if (edge == 64) {
+        g.splits = g.symmetric && g.parts
+                       ? tile_splits(tile_count(batch, g.rows, g.cols, edge, true), g.depth) : 1;
+        const dim3 shared(grid.x, grid.y, static_cast<unsigned>(g.splits));
+#define GS_DIRECT(P, SHARED)                                                                                         \
+    if (products == P && (g.splits > 1) == SHARED)                                                                   \
+    hipLaunchKernelGGL((ortho_product_direct_kernel<P, 8, SHARED>), shared, dim3(8 * kWave), 0, stream, g)
+        GS_DIRECT(1, false);
+        GS_DIRECT(1, true);
+        GS_DIRECT(3, false);
+        GS_DIRECT(3, true);
+#undef GS_DIRECT
+        if (g.splits > 1) hipLaunchKernelGGL(ortho_join_kernel, dim3(grid.x, grid.y, 2), dim3(8 * kWave), 0, stream, g);
+    }
     GS_PRODUCT(128, 4, 2)
     GS_PRODUCT(192, 6, 2)
     GS_PRODUCT(256, 2, 4)
@@ -1054,9 +1122,11 @@ gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps
         const Planes poly = now.apply == 3 ? l.poly : Planes{l.poly.hi, nullptr};
         const Planes next = step_products<T>(M, steps - s - 1).gram == 3 ? l.x : Planes{l.x.hi, nullptr};
         ProductArgs ops[3] = {
-            {l.x, l.x, {}, l.gram, l.gram, M, M, N, 0, 0, 1, kScaleA / (kScaleX * kScaleX), 0.0f, nullptr, 0, 0, 0, 0},
-            {l.gram, l.gram, l.gram, poly, poly, M, M, M, 0, 0, 1, c / kScaleA, b, nullptr, 0, 0, 0, 0},
-            {l.poly, l.xt[at], l.xt[at], next, l.xt[1 - at], M, N, M, 0, 0, 0, 1.0f / kScaleA, a, nullptr, 0, 0, 0, 0}};
+            {l.x, l.x, {}, l.gram, l.gram, M, M, N, 0, 0, 1, kScaleA / (kScaleX * kScaleX), 0.0f, nullptr, 0, 0, 0, 0, 1,
+             l.parts},
+            {l.gram, l.gram, l.gram, poly, poly, M, M, M, 0, 0, 1, c / kScaleA, b, nullptr, 0, 0, 0, 0, 1, nullptr},
+            {l.poly, l.xt[at], l.xt[at], next, l.xt[1 - at], M, N, M, 0, 0, 0, 1.0f / kScaleA, a, nullptr, 0, 0, 0, 0, 1,
+             nullptr}};
         if (s == steps - 1) {
             ops[2].out = out;
             ops[2].out_type = std::is_same<T, float>::value ? GS_F32 : std::is_same<T, __bf16>::value ? GS_BF16 : GS_F16;
