@@ -375,8 +375,8 @@ gs_status gs_layer_norm_fwd(const void *x, const void *weight, const void *bias,
  *   grad_x = rstd * (g - sum(g) / dim - xh * sum(g * xh) / dim)   (per row)
  *   grad_weight = sum over rows of grad_y * xh,   grad_bias = sum over rows of grad_y.
  * grad_x has x's type, grad_weight and grad_bias the weight's. grad_bias may be NULL (not computed). With rows = 0
- * the two sums are zeros. All outputs are overwritten. workspace: gs_layer_norm_bwd_workspace_bytes(rows, dim)
- * bytes (0 for sizes out of range), float32 partial sums. Limits as the forward's. Asynchronous.
+ * the two sums are zeros. All outputs are overwritten; grad_x may not overlap an input.
+ * workspace: gs_layer_norm_bwd_workspace_bytes(rows, dim) bytes (0 for sizes out of range), float32 partial sums. Limits as the forward's. Asynchronous.
  */
 size_t gs_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
 
@@ -434,7 +434,9 @@ gs_status gs_expert_combine_bwd(const void *source, const int32_t *offsets, cons
  * (b A + c A A) X, with (a, b, c) = coefficients (X transposed around the steps where m > n, which gives the same
  * result with the smaller products). out = X, in update's type.
  * update, out [batch, m, n] of dtype; out may be update. The norm's sums are float64. X, A and b A + c A A are held
- * as pairs of float16 (high and low part, 22 bits together, scaled by a power of two). Every singular value must
+ * as pairs of float16 (high and low part, 22 bits together, scaled by a power of two). For 16-bit types and 768 rows or
+ * more (the smaller side, padded to 32) the leading steps' products take the high parts alone: the result's error is
+ * then at most 1.08 times its own rounding on the matrices it was measured on. Every singular value must
  * stay below 16 and every entry of b A + c A A below 64 in magnitude, as they do for coefficients that converge.
  * A matrix that holds an infinity or NaN gives NaN; others in the batch are not affected.
  * Limits: 0 <= batch <= 65535, 1 <= m, n <= 65536, batch * m * n < 2^40, 0 <= steps <= 100. Asynchronous.
