@@ -376,7 +376,8 @@ gs_status gs_layer_norm_fwd(const void *x, const void *weight, const void *bias,
  *   grad_weight = sum over rows of grad_y * xh,   grad_bias = sum over rows of grad_y.
  * grad_x has x's type, grad_weight and grad_bias the weight's. grad_bias may be NULL (not computed). With rows = 0
  * the two sums are zeros. All outputs are overwritten; grad_x may not overlap an input.
- * workspace: gs_layer_norm_bwd_workspace_bytes(rows, dim) bytes (0 for sizes out of range), float32 partial sums. Limits as the forward's. Asynchronous.
+ * workspace: gs_layer_norm_bwd_workspace_bytes(rows, dim) bytes (0 for sizes out of range),
+ * float32 partial sums. Limits as the forward's. Asynchronous.
  */
 size_t gs_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
 

@@ -231,3 +231,8 @@ def test_more_elements_than_32_bits_count():
     assert torch.equal(y[-100:], x[-100:] * 4)
     g = binding.gs_expert_combine_bwd(sent, plan, torch.full((T, K), 0.5, device="cuda"), x)
     assert torch.equal(g.rows[-50:], x[last] * 0.5)
+
+
+@pytest.mark.parametrize("T,K,E", [(4097, 64, 7), (200001, 2, 33), (150000, 3, 2000), (270000, 1, 1)])
+def test_plan_of_more_pairs_than_a_step_of_every_workgroup(T, K, E):
+    check_plan(random_ids(T, K, E, T + K + E), E)
