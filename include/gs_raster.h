@@ -349,9 +349,9 @@ gs_status gs_rasterize_bwd(const float *means2d, const float *conics, const floa
 
 /* ------------------------------------------------------------------------------------------------------------
  * Training operators of a layer of experts. Their arrays hold one of three element types, named by a gs_dtype;
- * sums, statistics and products are formed in float32 or wider and rounded once where they are stored. The order of
- * every sum depends on the sizes alone: the same inputs give the same bits on every run. Rows may start at any
- * multiple of the element's size.
+ * sums and statistics are formed in float32 or wider and rounded once where they are stored; so are products, but for
+ * gs_orthogonalize's, whose operands are held as it says. The order of every sum depends on the sizes alone: the same
+ * inputs give the same bits on every run. Rows may start at any multiple of the element's size.
  */
 typedef enum gs_dtype {
     GS_F32 = 0,
@@ -435,9 +435,8 @@ gs_status gs_expert_combine_bwd(const void *source, const int32_t *offsets, cons
  * (b A + c A A) X, with (a, b, c) = coefficients (X transposed around the steps where m > n, which gives the same
  * result with the smaller products). out = X, in update's type.
  * update, out [batch, m, n] of dtype; out may be update. The norm's sums are float64. X, A and b A + c A A are held
- * as pairs of float16 (high and low part, 22 bits together, scaled by a power of two). For 16-bit types and 768 rows or
- * more (the smaller side, padded to 32) the leading steps' products take the high parts alone: the result's error is
- * then at most 1.08 times its own rounding on the matrices it was measured on. Every singular value must
+ * as pairs of float16 (high and low part, 22 bits together, scaled by a power of two), for every type and in every step;
+ * a product leaves out what the two low parts give, 2^-22 of it, and sums in float32. Every singular value must
  * stay below 16 and every entry of b A + c A A below 64 in magnitude, as they do for coefficients that converge.
  * A matrix that holds an infinity or NaN gives NaN; others in the batch are not affected.
  * Limits: 0 <= batch <= 65535, 1 <= m, n <= 65536, batch * m * n < 2^40, 0 <= steps <= 100. Asynchronous.

@@ -3,9 +3,11 @@
 // float32 has no matrix-core rate to speak of next to float16's (157 against 2500 TFLOP/s), so every operand is held
 // as a pair of float16, high and low part (22 bits together), and a product of two operands is three matrix products,
 // high high + high low + low high, summed in float32. The term left out is 2^-22 of the product.
-// The time of large matrices is the products' (4096 x 4096 bf16: all but 0.05 of 2.1 ms), at the rate of this card's large
-// float16 library product, 1.2 PFLOP/s: 1.27 with both halves, 1.0 with the high halves alone, and the card's clock falls
-// to 1.7 GHz under either. Small and middling ones are launches and the latency of their chains.
+// Every step takes both halves, whatever the result's type: with the default coefficients an error of an operand grows by
+// up to 122 in twelve steps, and steps on the high halves alone left float16 results up to 50 times their own rounding off.
+// The time of large matrices is the products' (4096 x 4096: all but 0.05 of 3.4 ms, 1.2 PFLOP/s, the rate of this card's
+// large float16 library product; its clock falls under the load). Small and middling ones are launches and the latency of
+// their chains.
 //
 // X holds values scaled by 2^12 and the Gram side by 2^10: entries of X are at most its largest singular value, and
 // the scale keeps the low parts of the smallest ones out of float16's subnormals.
@@ -159,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restri
 struct ProductArgs {
     Planes p, q;
     Planes add;       // [cols][rows], as `turned`; hi NULL: nothing is added
-    Planes straight;  // [rows][cols]; lo NULL: only the high parts are written
+    Planes straight;  // [rows][cols]
     Planes turned;    // [cols][rows]
     int rows, cols, depth;  // multiples of 32
     int tile_rows, tile_cols;
@@ -324,31 +326,27 @@ __device__ __forceinline__ void finish_four(const ProductArgs &a, size_t batch, 
     split<4>(v, h, l);
     if (both) {
         *reinterpret_cast<h16x4 *>(a.turned.hi + at) = h;
-        if (a.turned.lo) *reinterpret_cast<h16x4 *>(a.turned.lo + at) = l;
+        *reinterpret_cast<h16x4 *>(a.turned.lo + at) = l;
     }
     // after the transpose this lane: row g * 8 + lane / 32 * 4 + lane % 4, columns from lane % 32 / 4 * 4
     const size_t to = batch * (static_cast<size_t>(a.rows) * a.cols) + block_at(mp, np * 2 + lane % 32 / 16, a.rows) +
                       (lane % 16 / 8 * kPanel + g * 8 + lane / 32 * 4 + lane % 4) * 8 + lane % 8 / 4 * 4;
     *reinterpret_cast<h16x4 *>(a.straight.hi + to) = quad_transpose(h);
-    if (a.straight.lo) *reinterpret_cast<h16x4 *>(a.straight.lo + to) = quad_transpose(l);
+    *reinterpret_cast<h16x4 *>(a.straight.lo + to) = quad_transpose(l);
 }
 
-// A workgroup of WR x WC waves makes a T x T tile, each wave its part of it. PRODUCTS = 3: both halves of the operands
-// (high high + high low + low high); 1: the high halves alone. A stage of the LDS ring holds 32 columns of the high
-// halves, or 16 of both; while one is multiplied the next is there already (its first operands are read ahead of the
-// barrier) and two more are on their way.
-// Two or three waves a SIMD, so that one has products to issue where another waits at the barrier: 8 x 1024 x 1024 bf16
-// 542 us, with one wave a SIMD 581. The reads of LDS that smaller parts cost are a third of its rate. With 16 waves, six or
-// eight stages, or the other way round of the waves it is the same within 2%.
-template <int T, int PRODUCTS, int WR, int WC>
+// A workgroup of WR x WC waves makes a T x T tile, each wave its part of it. A stage of the LDS ring holds 16 columns of
+// both halves; while one is multiplied the next is there already (its operands are read ahead of the barrier) and two
+// more are on their way.
+// Two or three waves a SIMD, so that one has products to issue where another waits at the barrier (8 x 1024 x 1024 732 us).
+// The reads of LDS that smaller parts cost are a third of its rate.
+template <int T, int WR, int WC>
 __global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (T <= 128 ? 2 : 1)) void ortho_product_kernel(ProductArgs a) {
     constexpr int kStages = 4;
     constexpr int kPanels = T / kPanel;
     constexpr int FR = kPanels / WR, FC = kPanels / WC;  // 32 x 32 results of a wave, each way
     static_assert(FR * WR == kPanels && FC * WC == kPanels, "whole results");
-    constexpr int PL = PRODUCTS == 1 ? 1 : 2;   // planes staged
-    constexpr int S = PRODUCTS == 1 ? 2 : 1;    // blocks of 16 columns in a stage
-    constexpr int kBlocks = 2 * PL * kPanels * S;
+    constexpr int kBlocks = 4 * kPanels;        // of a stage: both halves of the rows' panels and of the columns'
     constexpr int L = kBlocks / (WR * WC);      // blocks a wave loads for a stage
     static_assert(L * WR * WC == kBlocks, "the waves share the loads evenly");
     constexpr uint32_t kStageBytes = kBlocks * kBlock * sizeof(_Float16);
@@ -365,78 +363,67 @@ __global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (T <= 128 ? 2 : 1)) voi
 #pragma unroll
     for (int i = 0; i < L; ++i) {
         const int b = wave * L + i;
-        const int s = b % S, panel = b / S % kPanels, plane = b / (S * kPanels) % PL, op = b / (S * kPanels * PL);
+        const int panel = b % kPanels, plane = b / kPanels % 2, op = b / (kPanels * 2);
         int at = (op ? tj : ti) * kPanels + panel;
         const int last = (op ? col_panels : row_panels) - 1;
         at = at < last ? at : last;
         const Planes &from = op ? a.q : a.p;
         src[i] = (plane ? from.lo : from.hi) + batch * (static_cast<size_t>(op ? a.cols : a.rows) * a.depth) +
-                 block_at(at, s, op ? a.cols : a.rows);
+                 block_at(at, 0, op ? a.cols : a.rows);
     }
     const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) _Float16 *)s_ring));
     const uint32_t lane_bytes = lane * 16;
-    const int stages = blocks / S;
-    const size_t row_step = static_cast<size_t>(S) * row_panels * kBlock;
-    const size_t col_step = static_cast<size_t>(S) * col_panels * kBlock;
+    const size_t row_step = static_cast<size_t>(row_panels) * kBlock;
+    const size_t col_step = static_cast<size_t>(col_panels) * kBlock;
     int issued = 0;
     const auto issue = [&](int i) {  // block i of this wave's share of stage `issued`
         load_block(src[i], lane_bytes, ring + (issued % kStages) * kStageBytes + (wave * L + i) * 1024);
         // past the end the last stage is loaded again, unused
-        if (issued + 1 < stages) src[i] += wave * L + i < kBlocks / 2 ? row_step : col_step;
+        if (issued + 1 < blocks) src[i] += wave * L + i < kBlocks / 2 ? row_step : col_step;
     };
     const int wr = wave / WC, wc = wave % WC;
-    constexpr int R = PL * (FR + FC);  // operands of a wave for one block of 16 columns: rows high, low, columns high, low
+    constexpr int R = 2 * (FR + FC);  // operands of a wave for one block of 16 columns: rows high, low, columns high, low
     h16x8 frag[2][R];
-    const auto fetch = [&](const _Float16 *stage_at, int s, int turn, int r) {
-        const int op = r < PL * FR ? 0 : 1, q = r - op * PL * FR, F = op ? FC : FR, plane = q / F, f = q % F;
+    const auto fetch = [&](const _Float16 *stage_at, int turn, int r) {
+        const int op = r < 2 * FR ? 0 : 1, q = r - op * 2 * FR, F = op ? FC : FR, plane = q / F, f = q % F;
         frag[turn][r] = *reinterpret_cast<const h16x8 *>(
-            stage_at + (((op * PL + plane) * kPanels + (op ? wc : wr) * F + f) * S + s) * kBlock);
+            stage_at + ((op * 2 + plane) * kPanels + (op ? wc : wr) * F + f) * kBlock);
     };
     const auto stage_at = [&](int stage) { return s_ring + (stage % kStages) * (kBlocks * kBlock) + lane * 8; };
     f32x16 acc[FR][FC] = {};
     // The products of one block of 16 columns with, in between and in this order, the reads of the next block's
-    // operands and FIRST..LAST of the stage's loads.
-    const auto multiply = [&](int turn, const _Float16 *next, int next_s, auto first, auto last) {
-        constexpr int M = PRODUCTS * FR * FC, kFirst = decltype(first)::value, kLoads = decltype(last)::value - kFirst;
+    // operands and the loads of the stage `issued`.
+    const auto multiply = [&](int turn, const _Float16 *next) {
+        constexpr int M = 3 * FR * FC;
         constexpr int kReads = M > R ? M - M / 4 : M;  // the reads end early enough to be done at the next barrier
 #pragma unroll
         for (int x = 0; x < M; ++x) {
 #pragma unroll
-            for (int r = x * R / kReads; r < (x + 1) * R / kReads && r < R; ++r) fetch(next, next_s, 1 - turn, r);
+            for (int r = x * R / kReads; r < (x + 1) * R / kReads && r < R; ++r) fetch(next, 1 - turn, r);
 #pragma unroll
-            for (int i = x * kLoads / M; i < (x + 1) * kLoads / M; ++i) issue(kFirst + i);
-            const int term = PRODUCTS == 1 ? 2 : x / (FR * FC), i = x / FC % FR, j = x % FC;
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                frag[turn][(term == 0 ? PL - 1 : 0) * FR + i],
-                frag[turn][PL * FR + (term == 1 ? PL - 1 : 0) * FC + j], acc[i][j], 0, 0, 0);
+            for (int i = x * L / M; i < (x + 1) * L / M; ++i) issue(i);
+            const int term = x / (FR * FC), i = x / FC % FR, j = x % FC;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag[turn][(term == 0 ? FR : 0) + i],
+                                                               frag[turn][2 * FR + (term == 1 ? FC : 0) + j],
+                                                               acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
+        ++issued;
     };
     for (; issued < kStages - 1; ++issued)
 #pragma unroll
         for (int i = 0; i < L; ++i) issue(i);
     wait_and_meet<(kStages - 2) * L>();
 #pragma unroll
-    for (int r = 0; r < R; ++r) fetch(stage_at(0), 0, 0, r);
-    using Zero = std::integral_constant<int, 0>;
-    using Half = std::integral_constant<int, L / 2>;
-    using All = std::integral_constant<int, L>;
-    for (int i = 0; i < blocks / 2; ++i) {
+    for (int r = 0; r < R; ++r) fetch(stage_at(0), 0, r);
+    for (int i = 0; i < blocks; i += 2) {
         // two blocks of 16 columns; depth is a multiple of 32. At each meeting the next stage is there and all waves
         // are done with the one before this, whose place the loads then take.
         wait_and_meet<(kStages - 3) * L>();
-        if constexpr (S == 2) {
-            multiply(0, stage_at(i), 1, Zero(), Half());
-            multiply(1, stage_at(i + 1), 0, Half(), All());
-            ++issued;
-        } else {
-            multiply(0, stage_at(2 * i + 1), 0, Zero(), All());
-            ++issued;
-            wait_and_meet<(kStages - 3) * L>();
-            multiply(1, stage_at(2 * i + 2), 0, Zero(), All());
-            ++issued;
-        }
+        multiply(0, stage_at(i + 1));
+        wait_and_meet<(kStages - 3) * L>();
+        multiply(1, stage_at(i + 2));
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
@@ -493,10 +480,9 @@ __device__ __forceinline__ f32x4 *part_at(const ProductArgs &a, size_t tile, int
 // Where there are few tiles, several workgroups share one's columns, because a unit draws only so much from L2 (300 x 4000:
 // 15 tiles by 15 units 24 us). Each leaves its part in memory for the kernel that joins them. (Joined by the last workgroup
 // to come, a call was slower than without: making the parts visible to it costs every unit its L2.)
-template <int PRODUCTS, int WAVES, bool SHARED>
+template <int WAVES, bool SHARED>
 __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(ProductArgs a) {
     constexpr int kTile = 64, kPanels = kTile / kPanel;
-    constexpr int PL = PRODUCTS == 1 ? 1 : 2;
     __shared__ f32x4 s_sum[WAVES][kPanels * 4][kWave];
     int ti, tj;
     tile_of(a, ti, tj);
@@ -509,11 +495,11 @@ __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(Prod
         mine = blocks * static_cast<int>(blockIdx.z + 1) / a.splits - first;
     }
     const int from = first + mine * wave / WAVES, to = first + mine * (wave + 1) / WAVES;
-    const _Float16 *src[2][PL][kPanels];
+    const _Float16 *src[2][2][kPanels];
 #pragma unroll
     for (int op = 0; op < 2; ++op)
 #pragma unroll
-        for (int plane = 0; plane < PL; ++plane)
+        for (int plane = 0; plane < 2; ++plane)
 #pragma unroll
             for (int f = 0; f < kPanels; ++f) {
                 const Planes &p = op ? a.q : a.p;
@@ -525,13 +511,13 @@ __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(Prod
     f32x16 acc[kPanels][kPanels] = {};
     // a ring of registers: the loads of kAhead blocks are on their way while one is multiplied
     constexpr int kAhead = 3, kRing = kAhead + 1;
-    h16x8 ring[kRing][2][PL][kPanels];
+    h16x8 ring[kRing][2][2][kPanels];
     int loaded = from;
     const auto load = [&](int slot) {
 #pragma unroll
         for (int op = 0; op < 2; ++op)
 #pragma unroll
-            for (int plane = 0; plane < PL; ++plane)
+            for (int plane = 0; plane < 2; ++plane)
 #pragma unroll
                 for (int f = 0; f < kPanels; ++f) {
                     ring[slot][op][plane][f] = *reinterpret_cast<const h16x8 *>(src[op][plane][f]);
@@ -542,13 +528,13 @@ __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(Prod
     };
     const auto multiply = [&](int slot) {
 #pragma unroll
-        for (int term = PRODUCTS == 1 ? 2 : 0; term < 3; ++term)
+        for (int term = 0; term < 3; ++term)
 #pragma unroll
             for (int i = 0; i < kPanels; ++i)
 #pragma unroll
                 for (int j = 0; j < kPanels; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[slot][0][term == 0 ? PL - 1 : 0][i],
-                                                                       ring[slot][1][term == 1 ? PL - 1 : 0][j],
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[slot][0][term == 0 ? 1 : 0][i],
+                                                                       ring[slot][1][term == 1 ? 1 : 0][j],
                                                                        acc[i][j], 0, 0, 0);
     };
     if (from < to) {
@@ -1016,7 +1002,7 @@ int tile_edge(int64_t batch, int rows, int cols, bool symmetric) {
     return best;
 }
 
-gs_status product(ProductArgs g, int64_t batch, int products, hipStream_t stream) {
+gs_status product(ProductArgs g, int64_t batch, hipStream_t stream) {
     const int edge = tile_edge(batch, g.rows, g.cols, g.symmetric != 0);
     g.tile_rows = (g.rows + edge - 1) / edge;
     g.tile_cols = (g.cols + edge - 1) / edge;
@@ -1024,53 +1010,25 @@ gs_status product(ProductArgs g, int64_t batch, int products, hipStream_t stream
                                                       : g.tile_rows * g.tile_cols),
                     static_cast<unsigned>(batch));
 #define GS_PRODUCT(T, WR, WC)                                                                                       \
-    if (edge == T) {                                                                                               \
-        if (products == 1)                                                                                         \
-            hipLaunchKernelGGL((ortho_product_kernel<T, 1, WR, WC>), grid, dim3(WR * WC * kWave), 0, stream, g);   \
-        else                                                                                                       \
-            hipLaunchKernelGGL((ortho_product_kernel<T, 3, WR, WC>), grid, dim3(WR * WC * kWave), 0, stream, g);   \
-    }
+    if (edge == T)                                                                                                 \
+    hipLaunchKernelGGL((ortho_product_kernel<T, WR, WC>), grid, dim3(WR * WC * kWave), 0, stream, g)
     if (edge == 64) {
         g.splits = g.symmetric && g.parts
                        ? tile_splits(tile_count(batch, g.rows, g.cols, edge, true), g.depth) : 1;
         const dim3 shared(grid.x, grid.y, static_cast<unsigned>(g.splits));
-#define GS_DIRECT(P, SHARED)                                                                                         \
-    if (products == P && (g.splits > 1) == SHARED)                                                                   \
-    hipLaunchKernelGGL((ortho_product_direct_kernel<P, 8, SHARED>), shared, dim3(8 * kWave), 0, stream, g)
-        GS_DIRECT(1, false);
-        GS_DIRECT(1, true);
-        GS_DIRECT(3, false);
-        GS_DIRECT(3, true);
-#undef GS_DIRECT
-        if (g.splits > 1) hipLaunchKernelGGL(ortho_join_kernel, dim3(grid.x, grid.y, 2), dim3(8 * kWave), 0, stream, g);
+        if (g.splits > 1) {
+            hipLaunchKernelGGL((ortho_product_direct_kernel<8, true>), shared, dim3(8 * kWave), 0, stream, g);
+            hipLaunchKernelGGL(ortho_join_kernel, dim3(grid.x, grid.y, 2), dim3(8 * kWave), 0, stream, g);
+        } else {
+            hipLaunchKernelGGL((ortho_product_direct_kernel<8, false>), shared, dim3(8 * kWave), 0, stream, g);
+        }
     }
-    GS_PRODUCT(128, 4, 2)
-    GS_PRODUCT(192, 6, 2)
-    GS_PRODUCT(256, 2, 4)
+    GS_PRODUCT(128, 4, 2);
+    GS_PRODUCT(192, 6, 2);
+    GS_PRODUCT(256, 2, 4);
 #undef GS_PRODUCT
     GS_LAUNCH_TRY("ortho_product_kernel");
     return GS_OK;
-}
-
-// What a step's products take of their operands, 3: both halves, 1: the high halves.
-struct StepProducts {
-    int gram, poly, apply;
-};
-
-// Both halves, but for large matrices of a type with fewer than 24 bits. There the earlier steps take the high halves:
-// 2^-12 of an operand is less than the update's own rounding (equal to it for float16), its errors average out over
-// many rows, and most of what an early step adds is damped by the later ones. X, A in b A and all sums keep both
-// halves. The 2-norm of the error against 64 bits, next to that of the result's own rounding, on momentum-like,
-// Gaussian, decaying and orthonormal matrices of 800 and 1200 rows: bfloat16 1.02 to 1.08, float16 1.00; with one more
-// high step float16 had up to 1.5, and below 768 rows some of these matrices up to 1.5 (512 rows) and 3.4 (33 rows),
-// where these steps cost least. On 4096 x 4096 bfloat16 they take 0.37 of the time of full ones.
-constexpr int kHighRows = 768;
-
-template <typename T>
-StepProducts step_products(int rows, int left) {  // left: steps that are left, this one among them
-    if (std::is_same<T, float>::value || rows < kHighRows) return {3, 3, 3};
-    if (left > (std::is_same<T, _Float16>::value ? 3 : 2)) return {1, 1, 1};
-    return std::is_same<T, _Float16>::value ? StepProducts{3, 3, 3} : StepProducts{1, 3, 3};
 }
 
 template <typename T>
@@ -1117,15 +1075,11 @@ gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps
                        tall ? l.xt[at] : l.x, tall ? l.x : l.xt[at]);
     GS_LAUNCH_TRY("ortho_split_kernel");
     for (int s = 0; s < steps; ++s) {
-        const StepProducts now = step_products<T>(M, steps - s);
-        // the low parts that nothing reads are not written
-        const Planes poly = now.apply == 3 ? l.poly : Planes{l.poly.hi, nullptr};
-        const Planes next = step_products<T>(M, steps - s - 1).gram == 3 ? l.x : Planes{l.x.hi, nullptr};
         ProductArgs ops[3] = {
             {l.x, l.x, {}, l.gram, l.gram, M, M, N, 0, 0, 1, kScaleA / (kScaleX * kScaleX), 0.0f, nullptr, 0, 0, 0, 0, 1,
              l.parts},
-            {l.gram, l.gram, l.gram, poly, poly, M, M, M, 0, 0, 1, c / kScaleA, b, nullptr, 0, 0, 0, 0, 1, nullptr},
-            {l.poly, l.xt[at], l.xt[at], next, l.xt[1 - at], M, N, M, 0, 0, 0, 1.0f / kScaleA, a, nullptr, 0, 0, 0, 0, 1,
+            {l.gram, l.gram, l.gram, l.poly, l.poly, M, M, M, 0, 0, 1, c / kScaleA, b, nullptr, 0, 0, 0, 0, 1, nullptr},
+            {l.poly, l.xt[at], l.xt[at], l.x, l.xt[1 - at], M, N, M, 0, 0, 0, 1.0f / kScaleA, a, nullptr, 0, 0, 0, 0, 1,
              nullptr}};
         if (s == steps - 1) {
             ops[2].out = out;
@@ -1134,9 +1088,8 @@ gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps
             ops[2].out_cols = static_cast<int>(n);
             ops[2].out_turned = tall ? 1 : 0;
         }
-        const int products[3] = {now.gram, now.poly, now.apply};
-        for (int i = 0; i < 3; ++i) {
-            const gs_status bad = product(ops[i], batch, products[i], stream);
+        for (const ProductArgs &op : ops) {
+            const gs_status bad = product(op, batch, stream);
             if (bad != GS_OK) return bad;
         }
         at = 1 - at;
