@@ -1,0 +1,34 @@
+"""The training operators at the ends of what they take."""
+import pytest
+import torch
+
+import train_util as tu
+from gpu_util import require_gpu
+from tile_binned_gaussian_amd import binding
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [3, 64, 77, 200, 513, 1000, 4100, 9001])
+def test_gradient_of_a_large_constant_row(dim, name):
+    """x is its own mean, so xh = 0 in every column, rstd = 1 / sqrt(eps) and grad_x = rstd (g - mean g): finite, though
+    (0 - mean) * rstd is not. 64 columns are whole packs of fewer lanes than share a row."""
+    dtype = tu.DTYPES[name]
+    g = torch.Generator().manual_seed(dim)
+    x = torch.full((3, dim), 2.0 ** 113, dtype=dtype)
+    x[1] = torch.randn(dim, generator=g).to(dtype)
+    w, gy = (1 + 0.1 * torch.randn(dim, generator=g)).to(dtype), torch.randn(3, dim, generator=g).to(dtype)
+    mean, rstd = tu.layer_norm(x, w, None, 1e-17)[1:]
+    mean, rstd = mean.float(), rstd.float()  # 2^113 * 3.2e8 is beyond float32
+    assert mean[0] == 2.0 ** 113 and (mean[0] * rstd[0]).isinf()
+    got = binding.gs_layer_norm_bwd(x.cuda(), w.cuda(), mean.cuda(), rstd.cuda(), gy.cuda())
+    want = tu.layer_norm_grad(x, w, mean, rstd, gy)
+    bound = tu.layer_norm_grad_bound(x, w, mean, rstd, gy)
+    for part, a, b, c in zip(("x", "weight", "bias"), (got.x, got.weight, got.bias), want, bound):
+        tu.assert_within(a, b, c, f"grad {part}")

@@ -230,7 +230,9 @@ __global__ __launch_bounds__(row_threads(G)) void norm_bwd_kernel(const T *__res
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const float xh = (static_cast<float>(cx[v][j]) - m) * rs, gy = static_cast<float>(cg[v][j]);
+                // past the row's end 0 itself: (0 - m) * rs may leave float32's range, and times 0 it would be NaN
+                const float xh = (v * G + lane) * N + j < dim ? (static_cast<float>(cx[v][j]) - m) * rs : 0.0f;
+                const float gy = static_cast<float>(cg[v][j]);
                 dw[v * N + j] = __builtin_fmaf(gy, xh, dw[v * N + j]);
                 db[v * N + j] += gy;
                 const float g = gy * w[v * N + j];  // zero past the row's end, as weight and grad_y are
@@ -311,7 +313,7 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_wide_kernel(const T *__rest
                 typename Pack<T>::V o;
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    xh[j] = (xh[j] - m) * rs;
+                    xh[j] = col + j < dim ? (xh[j] - m) * rs : 0.0f;  // past the end as above
                     g[j] *= w[j];
                     if (pass == 0) {
                         s1 += g[j];
