@@ -437,7 +437,8 @@ gs_status gs_expert_combine_bwd(const void *source, const int32_t *offsets, cons
  * update, out [batch, m, n] of dtype; out may be update. The norm's sums are float64. X, A and b A + c A A are held
  * as pairs of float16 (high and low part, 22 bits together, scaled by a power of two), for every type and in every step;
  * a product leaves out what the two low parts give, 2^-22 of it, and sums in float32. Every singular value must
- * stay below 16 and every entry of b A + c A A below 64 in magnitude, as they do for coefficients that converge.
+ * stay below 15.9, so that those of A stay below 253, and every entry of b A + c A A below 255 in magnitude, as they do for
+ * coefficients that move the singular values towards 1.
  * A matrix that holds an infinity or NaN gives NaN; others in the batch are not affected.
  * Limits: 0 <= batch <= 65535, 1 <= m, n <= 65536, batch * m * n < 2^40, 0 <= steps <= 100. Asynchronous.
  * workspace: gs_orthogonalize_workspace_bytes(batch, m, n) bytes (0 for sizes out of range, and for matrices small

@@ -32,3 +32,17 @@ def test_gradient_of_a_large_constant_row(dim, name):
     bound = tu.layer_norm_grad_bound(x, w, mean, rstd, gy)
     for part, a, b, c in zip(("x", "weight", "bias"), (got.x, got.weight, got.bias), want, bound):
         tu.assert_within(a, b, c, f"grad {part}")
+
+
+@pytest.mark.parametrize("shape", [(1, 50), (1, 9000), (2000, 1)])
+def test_singular_values_up_to_the_limit(shape):
+    """A matrix of one row has one singular value, here moved to 10 and near it: A is its square, in one entry."""
+    u = torch.randn(shape, generator=torch.Generator().manual_seed(3))
+    for limit, steps in ((10.0, 40), (15.0, 60)):
+        coefficients = (1.5, -0.5 / limit ** 2, 0.0)  # s -> 1.5 s - 0.5 s^3 / limit^2
+        want = tu.orthogonalize(u, steps=steps, coefficients=coefficients)
+        assert abs(want.norm().item() - limit) < 1e-6
+        got = binding.gs_orthogonalize(u.cuda(), steps=steps, coefficients=coefficients).cpu().double()
+        # the fixed point takes the size's errors back; a step's own roundings, at most ten of 2^-22, stay, and
+        # the direction's add up over the steps
+        assert (got - want).norm().item() <= 10 * 2.0 ** -22 * steps * limit

@@ -9,8 +9,9 @@
 // large float16 library product; its clock falls under the load). Small and middling ones are launches and the latency of
 // their chains.
 //
-// X holds values scaled by 2^12 and the Gram side by 2^10: entries of X are at most its largest singular value, and
-// the scale keeps the low parts of the smallest ones out of float16's subnormals.
+// X holds values scaled by 2^12 and the Gram side by 2^8: entries of X are at most its largest singular value and those of
+// A its square, so both reach float16's largest value at singular values of 16, and the scale keeps the low parts of all
+// but the smallest ones out of float16's subnormals.
 #include <type_traits>
 
 #include "gs_types.hpp"
@@ -25,7 +26,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kScaleX = 4096.0f;
-constexpr float kScaleA = 1024.0f;
+constexpr float kScaleA = 256.0f;
 constexpr int kThreads = 256;
 constexpr int kNormBlocks = 512;  // workgroups that share a matrix's norm, at most
 constexpr int kPanel = 32;   // rows of a panel; planes are padded to it with zeros both ways
