@@ -46,3 +46,20 @@ def test_singular_values_up_to_the_limit(shape):
         # the fixed point takes the size's errors back; a step's own roundings, at most ten of 2^-22, stay, and
         # the direction's add up over the steps
         assert (got - want).norm().item() <= 10 * 2.0 ** -22 * steps * limit
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n", [(60, 90), (300, 200), (333, 1000)])
+def test_a_matrix_far_smaller_than_the_guard(m, n, name):
+    """X = update / (|update| + eps) is then about update / eps, with entries far below a half's smallest value."""
+    dtype = tu.DTYPES[name]
+    g = torch.Generator().manual_seed(m)
+    u = torch.randn(m, n, generator=g)
+    u = u / u.norm()
+    for size, eps in ((1e-3, 1.0), (1e-6, 1.0), (1e-9, 1.0), (1e-11, 1e-2), (1e-17, 1e-7)):
+        v = (u * size).to(dtype)
+        want = tu.orthogonalize(v, eps=eps)
+        got = binding.gs_orthogonalize(v.cuda(), eps=eps).cpu().double()
+        own = (want.to(dtype).double() - want).norm().item()
+        # five steps of at most ten roundings of 2^-22 that grow as the matrix does
+        assert (got - want).norm().item() <= own + 50 * 2.0 ** -22 * want.norm().item(), (size, eps)

@@ -11,7 +11,8 @@
 //
 // X holds values scaled by 2^12 and the Gram side by 2^8: entries of X are at most its largest singular value and those of
 // A its square, so both reach float16's largest value at singular values of 16, and the scale keeps the low parts of all
-// but the smallest ones out of float16's subnormals.
+// but the smallest ones out of float16's subnormals. A matrix whose norm is far below eps stays small through all steps;
+// its X takes a larger scale (x_scale). Its A may then underflow, which counts for nothing next to a.
 #include <type_traits>
 
 #include "gs_types.hpp"
@@ -70,6 +71,25 @@ __device__ __forceinline__ void split(const float *v, H &hi, H &lo) {
         lo[j] = static_cast<_Float16>(__builtin_fmaf(static_cast<float>(hi[j]), -1.0f, v[j]));
 }
 
+// The scale of a large matrix's X, a power of two: 2^12, or more where a bound of its singular values over all steps
+// leaves room below 8 (no bound, NaN among them: 2^12). Up to 2^60, so that its square stays in float32.
+__device__ __forceinline__ float x_scale(double norm, double eps, int steps, float a, float b, float c) {
+    double s = norm / (norm + eps), most = s;
+    for (int k = 0; k < steps && most < 8.0; ++k) {
+        s *= fabs(static_cast<double>(a)) +
+             s * s * (fabs(static_cast<double>(b)) + s * s * fabs(static_cast<double>(c)));
+        if (!(s <= most)) most = s;
+    }
+    const int room = most < 8.0 ? ilogb(8.0 / most) : 0;
+    return ldexpf(kScaleX, room < 48 ? room : 48);
+}
+
+// What the products of a matrix take of its scale s.
+struct Scales {
+    float gram;  // kScaleA / s^2: of the Gram product's sums
+    float out;   // 1 / s: of the result
+};
+
 // The sum over the workgroup's threads, in every thread.
 __device__ __forceinline__ double workgroup_sum(double v, double *s_part) {
 #pragma unroll
@@ -104,12 +124,13 @@ __global__ __launch_bounds__(kThreads) void ortho_norm_kernel(const T *__restric
 }
 
 // X = update / (norm + eps) in both orders: `direct` holds the update's rows, `turned` its columns; 64 x 64 elements
-// a workgroup, zeros in the padding. Bound by memory: 4096 x 4096 bf16 33 us for 168 MB (5.0 TB/s).
+// a workgroup, zeros in the padding. Writes the matrix's scales. Bound by memory: 4096 x 4096 bf16 33 us for 168 MB (5.0 TB/s).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restrict__ update,
                                                                const double *__restrict__ partial, int parts, int m,
-                                                               int n, int pm, int pn, float eps, Planes direct,
-                                                               Planes turned) {
+                                                               int n, int pm, int pn, int steps, float a, float b,
+                                                               float c, float eps, Planes direct, Planes turned,
+                                                               Scales *__restrict__ scales) {
     constexpr int kTile = 64;
     __shared__ float s_tile[kTile][kTile + 1];
     __shared__ double s_part[kThreads / kWave];
@@ -125,8 +146,10 @@ __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restri
     }
     double sum = 0.0;
     for (int i = threadIdx.x; i < parts; i += kThreads) sum += partial[blockIdx.z * parts + i];
-    const double scale =
-        static_cast<double>(kScaleX) / (sqrt(workgroup_sum(sum, s_part)) + static_cast<double>(eps));
+    const double norm = sqrt(workgroup_sum(sum, s_part)), guard = static_cast<double>(eps);
+    const float x = x_scale(norm, guard, steps, a, b, c);
+    const double scale = static_cast<double>(x) / (norm + guard);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) scales[blockIdx.z] = {kScaleA / (x * x), 1.0f / x};
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
         const int row = tr + i * (kThreads / kTile);
@@ -158,7 +181,7 @@ __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restri
     }
 }
 
-// out = scale_acc P Q^T + scale_add add, P [rows][depth], Q [cols][depth].
+// out = scale_acc P Q^T + scale_add add, P [rows][depth], Q [cols][depth]; a Gram product's scale_acc is the matrix's own.
 struct ProductArgs {
     Planes p, q;
     Planes add;       // [cols][rows], as `turned`; hi NULL: nothing is added
@@ -167,6 +190,7 @@ struct ProductArgs {
     int rows, cols, depth;  // multiples of 32
     int tile_rows, tile_cols;
     int symmetric;    // P = Q and the result is symmetric: tiles of the lower triangle, written to both sides
+    const Scales *scales;  // of each matrix
     float scale_acc, scale_add;
     // the last step's: the result itself, [out_rows][out_cols] of out_type for each matrix, in place of planes
     void *out;
@@ -296,18 +320,19 @@ __device__ __forceinline__ void store_out(const ProductArgs &a, size_t batch, in
         if (col + k < a.out_cols) to[k] = static_cast<T>(v[k]);
 }
 
-// Four sums on their way out. both: to `turned` too.
-__device__ __forceinline__ void finish_four(const ProductArgs &a, size_t batch, int mp, int np, int g, float *v,
-                                            const Four &add, int lane, bool both) {
+// Four sums on their way out. both: to `turned` too. of: the matrix's scales, read before the first store.
+__device__ __forceinline__ void finish_four(const ProductArgs &a, const Scales &of, size_t batch, int mp, int np, int g,
+                                            float *v, const Four &add, int lane, bool both) {
     const size_t at = four_at(a, batch, mp, np, g, lane);
+    const float scale_acc = a.symmetric && !a.add.hi ? of.gram : a.scale_acc;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         v[k] = __builtin_fmaf(a.scale_add, static_cast<float>(add.hi[k]) + static_cast<float>(add.lo[k]),
-                              v[k] * a.scale_acc);
+                              v[k] * scale_acc);
     if (a.out) {
         float r[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) r[k] = v[k] * (1.0f / kScaleX);
+        for (int k = 0; k < 4; ++k) r[k] = v[k] * of.out;
         int row = mp * kPanel + g * 8 + lane / 32 * 4, col = np * kPanel + lane % 32;
         if (a.out_turned) {
             const int down = row;
@@ -429,6 +454,7 @@ __global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (T <= 128 ? 2 : 1)) voi
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     const bool both = !a.symmetric || ti != tj;  // a tile on the diagonal is its own mirror
+    const Scales of = a.scales[batch];
 #pragma unroll
     for (int i = 0; i < FR; ++i) {
         const int mp = ti * kPanels + wr * FR + i;
@@ -451,7 +477,7 @@ __global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (T <= 128 ? 2 : 1)) voi
                 float v[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] = acc[i][j][g * 4 + k];
-                finish_four(a, batch, mp, np, g, v, add[j][g], lane, both);
+                finish_four(a, of, batch, mp, np, g, v, add[j][g], lane, both);
             }
         }
     }
@@ -463,12 +489,12 @@ __device__ __forceinline__ Four load_part_four(const ProductArgs &a, size_t batc
     const int mp = ti * 2 + i, np = tj * 2 + wave / 4, rows = a.rows / kPanel, cols = a.cols / kPanel;
     return load_four(a, four_at(a, batch, mp < rows ? mp : rows - 1, np < cols ? np : cols - 1, wave % 4, lane));
 }
-__device__ __forceinline__ void finish_part_four(const ProductArgs &a, size_t batch, int ti, int tj, int i, int wave,
-                                                 int lane, f32x4 sum, const Four &add, bool both) {
+__device__ __forceinline__ void finish_part_four(const ProductArgs &a, const Scales &of, size_t batch, int ti, int tj,
+                                                 int i, int wave, int lane, f32x4 sum, const Four &add, bool both) {
     float v[4] = {sum[0], sum[1], sum[2], sum[3]};
     const int mp = ti * 2 + i, np = tj * 2 + wave / 4;
     if (mp < a.rows / kPanel && np < a.cols / kPanel)
-        finish_four(a, batch, mp, np, wave % 4, v, add, lane, both);
+        finish_four(a, of, batch, mp, np, wave % 4, v, add, lane, both);
 }
 __device__ __forceinline__ f32x4 *part_at(const ProductArgs &a, size_t tile, int split, int i, int wave, int lane) {
     return reinterpret_cast<f32x4 *>(a.parts) + ((tile * a.splits + split) * 16 + i * 8 + wave) * kWave + lane;
@@ -556,6 +582,7 @@ __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(Prod
             if (k + d < to) multiply(d);
     }
     const bool both = !a.symmetric || ti != tj;
+    const Scales of = a.scales[batch];
     Four add[kPanels];
 #pragma unroll
     for (int i = 0; i < kPanels; ++i) add[i] = load_part_four(a, batch, ti, tj, i, wave, lane);
@@ -576,7 +603,7 @@ __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(Prod
         if (SHARED)
             *part_at(a, batch * gridDim.x + blockIdx.x, blockIdx.z, i, wave, lane) = sum;
         else
-            finish_part_four(a, batch, ti, tj, i, wave, lane, sum, add[i], both);
+            finish_part_four(a, of, batch, ti, tj, i, wave, lane, sum, add[i], both);
     }
 }
 
@@ -587,16 +614,17 @@ __global__ __launch_bounds__(8 *kWave) void ortho_join_kernel(ProductArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave, i = blockIdx.z;
     const size_t batch = blockIdx.y, tile = batch * gridDim.x + blockIdx.x;
     const Four add = load_part_four(a, batch, ti, tj, i, wave, lane);
+    const Scales of = a.scales[batch];
     f32x4 sum = *part_at(a, tile, 0, i, wave, lane);
 #pragma unroll 4
     for (int p = 1; p < a.splits; ++p) sum += *part_at(a, tile, p, i, wave, lane);
-    finish_part_four(a, batch, ti, tj, i, wave, lane, sum, add, !a.symmetric || ti != tj);
+    finish_part_four(a, of, batch, ti, tj, i, wave, lane, sum, add, !a.symmetric || ti != tj);
 }
 
 // out [batch][m][n] from the planes that hold its rows, where there are no steps.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, int m, int n, int pm, int pn,
-                                                                T *__restrict__ out) {
+__global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, const Scales *__restrict__ scales, int m,
+                                                                int n, int pm, int pn, T *__restrict__ out) {
     // a wave: 8 rows, 64 columns
     const int lane = threadIdx.x % kWave;
     const int row = blockIdx.y * 32 + threadIdx.x / kWave * 8 + lane % 8, col = blockIdx.x * 64 + lane / 8 * 8;
@@ -604,13 +632,14 @@ __global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, int m,
     const size_t at = blockIdx.z * (static_cast<size_t>(pm) * pn) + eight_at(row, col, pm);
     const h16x8 h = *reinterpret_cast<const h16x8 *>(x.hi + at), l = *reinterpret_cast<const h16x8 *>(x.lo + at);
     T *to = out + (static_cast<size_t>(blockIdx.z) * m + row) * n;
+    const float scale = scales[blockIdx.z].out;
     constexpr int N = Pack<T>::kN;
 #pragma unroll
     for (int i = 0; i < 8 / N; ++i) {
         typename Pack<T>::V v;
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            v[j] = static_cast<T>((static_cast<float>(h[i * N + j]) + static_cast<float>(l[i * N + j])) / kScaleX);
+            v[j] = static_cast<T>((static_cast<float>(h[i * N + j]) + static_cast<float>(l[i * N + j])) * scale);
         if (col + i * N < n) store_pack(to, col + i * N, n, v);
     }
 }
@@ -926,6 +955,7 @@ constexpr int kUnits = 256;  // compute units
 
 struct Layout {
     double *partial;
+    Scales *scales;
     float *parts;
     Planes x, xt[2], gram, poly;
     size_t bytes;
@@ -953,6 +983,7 @@ Layout lay_out(void *workspace, int64_t batch, int64_t m, int64_t n) {
     Carver c(workspace);
     Layout l;
     l.partial = c.take<double>(static_cast<size_t>(batch) * kNormBlocks);
+    l.scales = c.take<Scales>(static_cast<size_t>(batch));
     // the Gram product's parts; the others' sums are as long as it has rows, too short to share where tiles are few
     const int m32 = static_cast<int>(padded(M));
     const int64_t tiles = tile_count(batch, m32, m32, 64, true);
@@ -1072,16 +1103,16 @@ gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps
     GS_LAUNCH_TRY("ortho_norm_kernel");
     int at = 0;  // which transposed copy is current
     hipLaunchKernelGGL((ortho_split_kernel<T>), dim3((pn + 63) / 64, (pm + 63) / 64, z), dim3(kThreads), 0, stream, u,
-                       l.partial, static_cast<int>(parts), static_cast<int>(m), static_cast<int>(n), pm, pn, eps,
-                       tall ? l.xt[at] : l.x, tall ? l.x : l.xt[at]);
+                       l.partial, static_cast<int>(parts), static_cast<int>(m), static_cast<int>(n), pm, pn, steps, a, b,
+                       c, eps, tall ? l.xt[at] : l.x, tall ? l.x : l.xt[at], l.scales);
     GS_LAUNCH_TRY("ortho_split_kernel");
     for (int s = 0; s < steps; ++s) {
         ProductArgs ops[3] = {
-            {l.x, l.x, {}, l.gram, l.gram, M, M, N, 0, 0, 1, kScaleA / (kScaleX * kScaleX), 0.0f, nullptr, 0, 0, 0, 0, 1,
-             l.parts},
-            {l.gram, l.gram, l.gram, l.poly, l.poly, M, M, M, 0, 0, 1, c / kScaleA, b, nullptr, 0, 0, 0, 0, 1, nullptr},
-            {l.poly, l.xt[at], l.xt[at], l.x, l.xt[1 - at], M, N, M, 0, 0, 0, 1.0f / kScaleA, a, nullptr, 0, 0, 0, 0, 1,
-             nullptr}};
+            {l.x, l.x, {}, l.gram, l.gram, M, M, N, 0, 0, 1, l.scales, 0.0f, 0.0f, nullptr, 0, 0, 0, 0, 1, l.parts},
+            {l.gram, l.gram, l.gram, l.poly, l.poly, M, M, M, 0, 0, 1, l.scales, c / kScaleA, b, nullptr, 0, 0, 0, 0, 1,
+             nullptr},
+            {l.poly, l.xt[at], l.xt[at], l.x, l.xt[1 - at], M, N, M, 0, 0, 0, l.scales, 1.0f / kScaleA, a, nullptr, 0, 0,
+             0, 0, 1, nullptr}};
         if (s == steps - 1) {
             ops[2].out = out;
             ops[2].out_type = std::is_same<T, float>::value ? GS_F32 : std::is_same<T, __bf16>::value ? GS_BF16 : GS_F16;
@@ -1097,7 +1128,7 @@ gs_status run(const void *update, int64_t batch, int64_t m, int64_t n, int steps
     }
     if (steps > 0) return ok();
     hipLaunchKernelGGL((ortho_finish_kernel<T>), dim3((pn + 63) / 64, pm / 32, z), dim3(kThreads), 0, stream,
-                       tall ? l.xt[at] : l.x, static_cast<int>(m), static_cast<int>(n), pm, pn,
+                       tall ? l.xt[at] : l.x, l.scales, static_cast<int>(m), static_cast<int>(n), pm, pn,
                        static_cast<T *>(out));
     GS_LAUNCH_TRY("ortho_finish_kernel");
     return ok();
