@@ -63,3 +63,18 @@ def test_a_matrix_far_smaller_than_the_guard(m, n, name):
         own = (want.to(dtype).double() - want).norm().item()
         # five steps of at most ten roundings of 2^-22 that grow as the matrix does
         assert (got - want).norm().item() <= own + 50 * 2.0 ** -22 * want.norm().item(), (size, eps)
+
+
+@pytest.mark.parametrize("rows,dim", [(5000, 1), (5000, 3), (200000, 7), (1 << 22, 1), (1 << 21, 3)])
+def test_column_sums_of_many_narrow_rows(rows, dim):
+    """Terms that are all the same round the same way in every addition of a chain: the worst for a long one. A chain is
+    at most: a thread's share (768 workgroups take 256 / 7 rows or more at a time), a workgroup's 256 threads, and 64
+    to join the workgroups; 8 for the terms."""
+    x, gy = torch.full((rows, dim), 0.7), torch.full((rows, dim), 0.1)
+    mean, rstd = torch.zeros(rows), torch.ones(rows)  # xh = x
+    w = torch.ones(dim)
+    got = binding.gs_layer_norm_bwd(x.cuda(), w.cuda(), mean.cuda(), rstd.cuda(), gy.cuda())
+    want = tu.layer_norm_grad(x, w, mean, rstd, gy)
+    depth = rows / (768 * (256 // 7)) + 256 + 64 + 8
+    for part, a, b in (("weight", got.weight, want[1]), ("bias", got.bias, want[2])):
+        tu.assert_within(a, b, depth * tu.U * b.abs(), f"grad {part}")

@@ -289,8 +289,8 @@ __global__ __launch_bounds__(row_threads(G)) void norm_bwd_kernel(const T *__res
         }
 }
 
-// Rows wider than the registers hold: grad_x by one workgroup a row (two reads), and the column sums by a thread a
-// column over the rows of one slice (a third).
+// Rows wider than the registers hold, or shorter than a pack: grad_x by one workgroup a row (two reads), and the column
+// sums over the rows of one slice (a third).
 template <typename T, typename W>
 __global__ __launch_bounds__(kThreads) void norm_bwd_wide_kernel(const T *__restrict__ x, const W *__restrict__ weight,
                                                                  const float *__restrict__ mean,
@@ -332,18 +332,31 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_wide_kernel(const T *__rest
     }
 }
 
+// A workgroup has `cols` columns, kThreads or all of a row that is shorter; its threads left over share the rows of the
+// slice, so that the sums of very many narrow rows are no long chains of additions, and are joined through LDS in order.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void norm_columns_kernel(const T *__restrict__ x, const float *__restrict__ mean,
                                                                 const float *__restrict__ rstd,
                                                                 const T *__restrict__ grad_y, int64_t rows,
-                                                                int64_t dim, float *__restrict__ partial) {
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (col >= dim) return;
+                                                                int64_t dim, int cols, float *__restrict__ partial) {
+    __shared__ float2 s_part[kThreads];
+    const int shares = kThreads / cols, share = threadIdx.x / cols;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * cols + threadIdx.x % cols;
+    const bool mine = share < shares && col < dim;
     float dw = 0.0f, db = 0.0f;
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-        const float g = static_cast<float>(grad_y[r * dim + col]);
-        dw = __builtin_fmaf(g, (static_cast<float>(x[r * dim + col]) - mean[r]) * rstd[r], dw);
-        db += g;
+    if (mine)
+        for (int64_t r = static_cast<int64_t>(blockIdx.y) * shares + share; r < rows;
+             r += static_cast<int64_t>(gridDim.y) * shares) {
+            const float g = static_cast<float>(grad_y[r * dim + col]);
+            dw = __builtin_fmaf(g, (static_cast<float>(x[r * dim + col]) - mean[r]) * rstd[r], dw);
+            db += g;
+        }
+    s_part[threadIdx.x] = make_float2(dw, db);
+    __syncthreads();
+    if (!mine || share > 0) return;
+    for (int i = 1; i < shares; ++i) {
+        dw += s_part[i * cols + threadIdx.x].x;
+        db += s_part[i * cols + threadIdx.x].y;
     }
     float *out = partial + static_cast<int64_t>(blockIdx.y) * 2 * partial_width(dim);
     out[col] = dw;
@@ -461,7 +474,10 @@ gs_status run_bwd(const void *x, const void *weight, const float *mean, const fl
     const T *tx = static_cast<const T *>(x), *tg = static_cast<const T *>(grad_y);
     const W *tw = static_cast<const W *>(weight);
     T *to = static_cast<T *>(grad_x);
-    int64_t parts = rows < kWideBwdParts ? rows : kWideBwdParts;
+    // slices of the rows: of short rows as many as the workspace has room for, each of whole turns of a workgroup
+    const int cols = static_cast<int>(dim < kThreads ? dim : kThreads);
+    const int64_t turns = (rows + kThreads / cols - 1) / (kThreads / cols), most = dim < kThreads ? kBwdBlocks : kWideBwdParts;
+    int64_t parts = turns < most ? turns : most;
 #define GS_NORM_BWD(G, V)                                                                                           \
     if (shape.lanes == G && shape.packs == V) {                                                                     \
         parts = bwd_blocks(rows, G);                                                                                \
@@ -487,8 +503,8 @@ gs_status run_bwd(const void *x, const void *weight, const float *mean, const fl
                            stream, tx, tw, mean, rstd, tg, rows, dim, to);
         GS_LAUNCH_TRY("norm_bwd_wide_kernel");
         hipLaunchKernelGGL((norm_columns_kernel<T>),
-                           dim3(static_cast<unsigned>((dim + kThreads - 1) / kThreads), static_cast<unsigned>(parts)),
-                           dim3(kThreads), 0, stream, tx, mean, rstd, tg, rows, dim, partial);
+                           dim3(static_cast<unsigned>((dim + cols - 1) / cols), static_cast<unsigned>(parts)),
+                           dim3(kThreads), 0, stream, tx, mean, rstd, tg, rows, dim, cols, partial);
         GS_LAUNCH_TRY("norm_columns_kernel");
     }
     hipLaunchKernelGGL((norm_reduce_kernel<W>),
