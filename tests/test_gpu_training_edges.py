@@ -78,3 +78,19 @@ def test_column_sums_of_many_narrow_rows(rows, dim):
     depth = rows / (768 * (256 // 7)) + 256 + 64 + 8
     for part, a, b in (("weight", got.weight, want[1]), ("bias", got.bias, want[2])):
         tu.assert_within(a, b, depth * tu.U * b.abs(), f"grad {part}")
+
+
+def test_a_row_of_more_columns_than_a_launch_has_threads_for():
+    """2^28 + 70 columns: one row, whose column sums are its terms."""
+    dim = (1 << 28) + 70
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, gy = (torch.randn(1, dim, generator=g, device="cuda").half() for _ in range(2))
+    w = torch.ones(dim, dtype=torch.float16, device="cuda")
+    got = binding.gs_layer_norm_bwd(x, w, torch.zeros(1, device="cuda"), torch.ones(1, device="cuda"), gy)
+    assert torch.equal(got.bias, gy[0])
+    assert torch.equal(got.weight, (gy[0].float() * x[0].float()).half())
+    # both sums' means are of at most 2^20 terms a thread and far below one, so grad_x is grad_y within a rounding of
+    # each of four operations on values below 8, and the means themselves
+    s1, s2 = gy.float().mean().abs().item(), (gy.float() * x.float()).mean().abs().item()
+    off = (got.x.float() - gy.float()).abs().max().item()
+    assert off <= 8 * 2.0 ** -10 + s1 + 8 * s2 + 1e-3

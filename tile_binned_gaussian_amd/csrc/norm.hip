@@ -21,6 +21,7 @@ constexpr int kWideFwdBlocks = 2048;
 constexpr int kWideBwdParts = 64;
 constexpr int kBwdBlocks = 768;       // at most: the rows of column sums that the workspace holds
 constexpr int kReduceThreads = 1024;
+constexpr int kReduceBlocks = 1 << 20;  // at most: a launch has fewer than 2^32 threads
 
 // Floats of a row of column sums in the workspace: whole packs of 16 bytes and cache lines.
 __host__ __device__ constexpr int64_t partial_width(int64_t dim) { return (dim + 31) / 32 * 32; }
@@ -372,19 +373,22 @@ __global__ __launch_bounds__(kReduceThreads) void norm_reduce_kernel(const float
     constexpr int kWaves = kReduceThreads / kWave;
     __shared__ float s_part[kWaves][kWave];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * kWave + lane;
-    float s = 0.0f;
-    if (col < dim) {
-        const int64_t width = partial_width(dim);
-        const float *p = partial + blockIdx.y * width + col;
+    const int64_t width = partial_width(dim);
+    for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kWave; c0 < dim; c0 += static_cast<int64_t>(gridDim.x) * kWave) {
+        const int64_t col = c0 + lane;
+        float s = 0.0f;
+        if (col < dim) {
+            const float *p = partial + blockIdx.y * width + col;
 #pragma unroll 8
-        for (int i = wave; i < parts; i += kWaves) s += p[static_cast<int64_t>(i) * 2 * width];
-    }
-    s_part[wave][lane] = s;
-    __syncthreads();
-    if (wave == 0 && col < dim) {
-        for (int i = 1; i < kWaves; ++i) s += s_part[i][lane];
-        (blockIdx.y ? grad_bias : grad_weight)[col] = static_cast<W>(s);
+            for (int i = wave; i < parts; i += kWaves) s += p[static_cast<int64_t>(i) * 2 * width];
+        }
+        __syncthreads();  // the columns before are stored
+        s_part[wave][lane] = s;
+        __syncthreads();
+        if (wave == 0 && col < dim) {
+            for (int i = 1; i < kWaves; ++i) s += s_part[i][lane];
+            (blockIdx.y ? grad_bias : grad_weight)[col] = static_cast<W>(s);
+        }
     }
 }
 
@@ -507,8 +511,9 @@ gs_status run_bwd(const void *x, const void *weight, const float *mean, const fl
                            dim3(kThreads), 0, stream, tx, mean, rstd, tg, rows, dim, cols, partial);
         GS_LAUNCH_TRY("norm_columns_kernel");
     }
+    const int64_t blocks = (dim + kWave - 1) / kWave;
     hipLaunchKernelGGL((norm_reduce_kernel<W>),
-                       dim3(static_cast<unsigned>((dim + kWave - 1) / kWave), grad_bias ? 2u : 1u),
+                       dim3(static_cast<unsigned>(blocks < kReduceBlocks ? blocks : kReduceBlocks), grad_bias ? 2u : 1u),
                        dim3(kReduceThreads), 0, stream, partial, static_cast<int>(parts), dim,
                        static_cast<W *>(grad_weight), static_cast<W *>(grad_bias));
     GS_LAUNCH_TRY("norm_reduce_kernel");
