@@ -20,6 +20,13 @@ constexpr int kMaxExperts = 4096;
 constexpr int kPlanThreads = 1024;   // up to kWideExperts experts
 constexpr int kWideThreads = 256;    // above: one LDS counter per expert and wave has to fit
 constexpr int kWideExperts = 1024;
+// LDS of expert_place_kernel: a counter for every wave and two more for every expert. The most is the kernel's attribute,
+// whatever a call needs, so that calls from several host threads set one value.
+constexpr size_t plan_lds(int threads, int experts) {
+    return static_cast<size_t>(threads / kWave + 2) * static_cast<size_t>(experts) * sizeof(int32_t);
+}
+constexpr size_t kPlanLds = plan_lds(kWideThreads, kMaxExperts);
+static_assert(kPlanLds >= plan_lds(kPlanThreads, kWideExperts) && kPlanLds <= 159 * 1024, "both fit");
 // Pairs that one workgroup takes alone, in one launch: 4096 pairs of 8 to 256 experts 7.1 to 8.8 us in one launch and 7.3
 // to 7.9 in two, whose second costs the host 3.5 us more; 8192 pairs 10.4 to 13.4 us alone, 8.4 to 9.1 in two.
 constexpr int64_t kPlanAlone = 4096;
@@ -411,10 +418,10 @@ extern "C" gs_status gs_expert_plan(const int32_t *ids, int64_t tokens, int64_t 
                            ids, n, chunk, experts, counts);
         GS_LAUNCH_TRY("expert_count_kernel");
     }
-    const size_t lds = static_cast<size_t>(threads / kWave + 2) * static_cast<size_t>(experts) * sizeof(int32_t);
+    const size_t lds = plan_lds(threads, experts);
     if (lds + 1024 > 65536)
         GS_HIP_TRY(hipFuncSetAttribute(reinterpret_cast<const void *>(expert_place_kernel),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds)));
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPlanLds)));
     hipLaunchKernelGGL(expert_place_kernel, grid, block, lds, stream, ids, n, chunk, experts, bits_for(experts),
                        chunks == 1 ? 1 : 0, counts, offsets, rows, pairs);
     GS_LAUNCH_TRY("expert_place_kernel");
