@@ -351,7 +351,8 @@ gs_status gs_rasterize_bwd(const float *means2d, const float *conics, const floa
  * Training operators of a layer of experts. Their arrays hold one of three element types, named by a gs_dtype;
  * sums and statistics are formed in float32 or wider and rounded once where they are stored; so are products, but for
  * gs_orthogonalize's, whose operands are held as it says. The order of every sum depends on the sizes alone: the same
- * inputs give the same bits on every run. Rows may start at any multiple of the element's size.
+ * inputs give the same bits on every run. Rows may start at any multiple of the element's size. Outputs and workspaces
+ * may overlap neither an input nor each other (GS_ERR_INVALID_ARG), but for gs_orthogonalize's out, which may be update.
  */
 typedef enum gs_dtype {
     GS_F32 = 0,
@@ -363,7 +364,7 @@ typedef enum gs_dtype {
  *
  * For each row x of `rows` rows of `dim` elements: mean = sum(x) / dim, rstd = 1 / sqrt(sum((x - mean)^2) / dim +
  * eps), y = (x - mean) * rstd * weight + bias.
- * x, y              [rows, dim] of dtype; may not overlap
+ * x, y              [rows, dim] of dtype
  * weight, bias      [dim] of weight_dtype (dtype or GS_F32); bias may be NULL: no bias
  * mean, rstd        [rows] float32, the backward's inputs; both may be NULL (inference)
  * Limits: 0 <= rows < 2^31, 1 <= dim < 2^31, eps >= 0. rows = 0 launches nothing. Asynchronous.
@@ -375,7 +376,7 @@ gs_status gs_layer_norm_fwd(const void *x, const void *weight, const void *bias,
  *   grad_x = rstd * (g - sum(g) / dim - xh * sum(g * xh) / dim)   (per row)
  *   grad_weight = sum over rows of grad_y * xh,   grad_bias = sum over rows of grad_y.
  * grad_x has x's type, grad_weight and grad_bias the weight's. grad_bias may be NULL (not computed). With rows = 0
- * the two sums are zeros. All outputs are overwritten; grad_x may not overlap an input.
+ * the two sums are zeros. All outputs are overwritten.
  * workspace: gs_layer_norm_bwd_workspace_bytes(rows, dim) bytes (0 for sizes out of range),
  * float32 partial sums. Limits as the forward's. Asynchronous.
  */
@@ -434,7 +435,7 @@ gs_status gs_expert_combine_bwd(const void *source, const int32_t *offsets, cons
  * X = update / (|update| + eps) with the Frobenius norm of each matrix; `steps` times A = X X^T, X = a X +
  * (b A + c A A) X, with (a, b, c) = coefficients (X transposed around the steps where m > n, which gives the same
  * result with the smaller products). out = X, in update's type.
- * update, out [batch, m, n] of dtype; out may be update. The norm's sums are float64. X, A and b A + c A A are held
+ * update, out [batch, m, n] of dtype; out may be update itself. The norm's sums are float64. X, A and b A + c A A are held
  * as pairs of float16 (high and low part, 22 bits together, scaled by a power of two), for every type and in every step;
  * a product leaves out what the two low parts give, 2^-22 of it, and sums in float32. Every singular value must
  * stay below 15.9, so that those of A stay below 253, and every entry of b A + c A A below 255 in magnitude, as they do for

@@ -24,6 +24,15 @@ int hipLaunchKernel(const void *f, dim3_t grid, dim3_t block, void **args, size_
     fflush(stdout);
     return 0;
 }
+static struct { dim3_t grid, block; size_t lds; void *stream; } held;
+int __hipPushCallConfiguration(dim3_t grid, dim3_t block, size_t lds, void *stream) {
+    held.grid = grid; held.block = block; held.lds = lds; held.stream = stream;
+    return 0;
+}
+int __hipPopCallConfiguration(dim3_t *grid, dim3_t *block, size_t *lds, void **stream) {
+    *grid = held.grid; *block = held.block; *lds = held.lds; *stream = held.stream;
+    return 0;
+}
 int hipGetLastError(void) { return 0; }
 int hipPeekAtLastError(void) { return 0; }
 """
@@ -68,5 +77,6 @@ for m, n in ((96, 160), (128, 128), (32, 1000), (128, 96)):
             largest.setdefault(line[1], set()).add(int(line[3]))
         elif int(line[6]) + 1024 > 65536:
             assert line[1] in largest and int(line[6]) <= max(largest[line[1]])
+    assert sum(line[0] == "launch" for line in lines) == 11
     assert len(largest) >= 2, "no kernel here needs more than 64 KB"
     assert all(len(sizes) == 1 for sizes in largest.values()), largest

@@ -408,6 +408,12 @@ extern "C" gs_status gs_expert_plan(const int32_t *ids, int64_t tokens, int64_t 
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(GS_ERR_WORKSPACE, "gs_expert_plan: need %zu workspace bytes, got %zu", need,
                     workspace ? workspace_bytes : 0);
+    const size_t bytes = static_cast<size_t>(n) * sizeof(int32_t);
+    const gs_status over = check_apart("gs_expert_plan",
+                                       {{"offsets", offsets, (experts + size_t(1)) * sizeof(int32_t)},
+                                        {"rows", rows, bytes}, {"pairs", pairs, bytes}, {"workspace", workspace, need}},
+                                       {{"ids", ids, bytes}});
+    if (over != GS_OK) return over;
     hipStream_t stream = static_cast<hipStream_t>(stream_handle);
     const int64_t chunk = plan_chunk(n), chunks = plan_chunks(n);
     const int threads = experts <= kWideExperts ? kPlanThreads : kWideThreads;
@@ -436,6 +442,12 @@ extern "C" gs_status gs_expert_dispatch(const void *x, const int32_t *offsets, c
     if (tokens == 0) return ok();
     if (!x || !offsets || !rows || !sent)
         return fail(GS_ERR_INVALID_ARG, "gs_expert_dispatch: a required pointer is NULL");
+    const size_t row = static_cast<size_t>(dim) * dtype_size(dtype), pairs = static_cast<size_t>(tokens) * choices;
+    const gs_status over = check_apart("gs_expert_dispatch", {{"sent", sent, pairs * row}},
+                                       {{"x", x, tokens * row},
+                                        {"offsets", offsets, (experts + size_t(1)) * sizeof(int32_t)},
+                                        {"rows", rows, pairs * sizeof(int32_t)}});
+    if (over != GS_OK) return over;
     hipStream_t stream = static_cast<hipStream_t>(stream_handle);
     const int32_t *kept = offsets + experts;
     // the copy is of bits, so two instances serve the three types
@@ -455,6 +467,11 @@ extern "C" gs_status gs_expert_combine(const void *source, const int32_t *rows, 
     if (bad != GS_OK) return bad;
     if (tokens == 0) return ok();
     if (!source || !rows || !y) return fail(GS_ERR_INVALID_ARG, "gs_expert_combine: a required pointer is NULL");
+    const size_t row = static_cast<size_t>(dim) * dtype_size(dtype), pairs = static_cast<size_t>(tokens) * choices;
+    const gs_status over = check_apart("gs_expert_combine", {{"y", y, tokens * row}},
+                                       {{"source", source, pairs * row}, {"rows", rows, pairs * sizeof(int32_t)},
+                                        {"weights", weights, pairs * sizeof(float)}});
+    if (over != GS_OK) return over;
     hipStream_t stream = static_cast<hipStream_t>(stream_handle);
 #define GS_COMBINE(T)                                                                                                \
     do {                                                                                                             \
@@ -477,6 +494,15 @@ extern "C" gs_status gs_expert_combine_bwd(const void *source, const int32_t *of
     if (tokens == 0) return ok();
     if (!source || !offsets || !rows || !weights || !grad_y || !grad_source || !grad_weights)
         return fail(GS_ERR_INVALID_ARG, "gs_expert_combine_bwd: a required pointer is NULL");
+    const size_t row = static_cast<size_t>(dim) * dtype_size(dtype), pairs = static_cast<size_t>(tokens) * choices;
+    const gs_status over = check_apart("gs_expert_combine_bwd",
+                                       {{"grad_source", grad_source, pairs * row},
+                                        {"grad_weights", grad_weights, pairs * sizeof(float)}},
+                                       {{"source", source, pairs * row},
+                                        {"offsets", offsets, (experts + size_t(1)) * sizeof(int32_t)},
+                                        {"rows", rows, pairs * sizeof(int32_t)},
+                                        {"weights", weights, pairs * sizeof(float)}, {"grad_y", grad_y, tokens * row}});
+    if (over != GS_OK) return over;
     hipStream_t stream = static_cast<hipStream_t>(stream_handle);
     const int32_t *kept = offsets + experts;
 #define GS_COMBINE_BWD(T)                                                                                        \

@@ -2,6 +2,8 @@
 // of rows that start at any element, and conversions to and from float32.
 #pragma once
 
+#include <initializer_list>
+
 #include "gs_internal.hpp"
 
 namespace gs {
@@ -101,6 +103,31 @@ __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
     for (int d = G / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, kWave);
     return v;
+}
+
+// An argument's bytes; none: an argument that is not given.
+struct Span {
+    const char *name;
+    const void *at;
+    size_t bytes;
+};
+
+// Refuses outputs (a workspace among them) that overlap an input or each other: the kernels read and write them in any
+// order, and a count that changes between two reads would lead a store out of its array.
+inline gs_status check_apart(const char *name, std::initializer_list<Span> outputs,
+                             std::initializer_list<Span> inputs) {
+    const auto apart = [](const Span &a, const Span &b) {
+        if (!a.at || !b.at || a.bytes == 0 || b.bytes == 0) return true;
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+        return x < y ? y - x >= a.bytes : x - y >= b.bytes;
+    };
+    for (const Span *o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Span &i : inputs)
+            if (!apart(*o, i)) return fail(GS_ERR_INVALID_ARG, "%s: %s overlaps %s", name, o->name, i.name);
+        for (const Span *p = outputs.begin(); p != o; ++p)
+            if (!apart(*o, *p)) return fail(GS_ERR_INVALID_ARG, "%s: %s overlaps %s", name, o->name, p->name);
+    }
+    return GS_OK;
 }
 
 inline bool known_dtype(int dtype) { return dtype == GS_F32 || dtype == GS_BF16 || dtype == GS_F16; }

@@ -555,6 +555,12 @@ extern "C" gs_status gs_layer_norm_fwd(const void *x, const void *weight, const 
         return fail(GS_ERR_INVALID_ARG, "gs_layer_norm_fwd: mean and rstd go together");
     if (rows == 0) return ok();
     if (!x || !weight || !y) return fail(GS_ERR_INVALID_ARG, "gs_layer_norm_fwd: a required pointer is NULL");
+    const size_t bytes = static_cast<size_t>(rows) * dim * dtype_size(dtype), wbytes = dim * dtype_size(weight_dtype);
+    const gs_status over = check_apart("gs_layer_norm_fwd",
+                                       {{"y", y, bytes}, {"mean", mean, rows * sizeof(float)},
+                                        {"rstd", rstd, rows * sizeof(float)}},
+                                       {{"x", x, bytes}, {"weight", weight, wbytes}, {"bias", bias, wbytes}});
+    if (over != GS_OK) return over;
     hipStream_t stream = static_cast<hipStream_t>(stream_handle);
     GS_NORM_TYPES(run_fwd, x, weight, bias, rows, dim, eps, y, mean, rstd, stream);
 }
@@ -576,6 +582,14 @@ extern "C" gs_status gs_layer_norm_bwd(const void *x, const void *weight, const 
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(GS_ERR_WORKSPACE, "gs_layer_norm_bwd: need %zu workspace bytes, got %zu", need,
                     workspace ? workspace_bytes : 0);
+    const size_t bytes = static_cast<size_t>(rows) * dim * dtype_size(dtype), wbytes = dim * dtype_size(weight_dtype);
+    const gs_status over =
+        check_apart("gs_layer_norm_bwd",
+                    {{"grad_x", grad_x, bytes}, {"grad_weight", grad_weight, wbytes}, {"grad_bias", grad_bias, wbytes},
+                     {"workspace", workspace, need}},
+                    {{"x", x, bytes}, {"weight", weight, wbytes}, {"mean", mean, rows * sizeof(float)},
+                     {"rstd", rstd, rows * sizeof(float)}, {"grad_y", grad_y, bytes}});
+    if (over != GS_OK) return over;
     hipStream_t stream = static_cast<hipStream_t>(stream_handle);
     GS_NORM_TYPES(run_bwd, x, weight, mean, rstd, grad_y, rows, dim, grad_x, grad_weight, grad_bias,
                   static_cast<float *>(workspace), stream);

@@ -1159,6 +1159,10 @@ extern "C" gs_status gs_orthogonalize(const void *update, int64_t batch, int64_t
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(GS_ERR_WORKSPACE, "gs_orthogonalize: need %zu workspace bytes, got %zu", need,
                     workspace ? workspace_bytes : 0);
+    const size_t bytes = static_cast<size_t>(batch) * m * n * dtype_size(dtype);
+    const gs_status over = check_apart("gs_orthogonalize", {{"out", out, bytes}, {"workspace", workspace, need}},
+                                       {{"update", out == update ? nullptr : update, bytes}});
+    if (over != GS_OK) return over;
     hipStream_t stream = static_cast<hipStream_t>(stream_handle);
     if (dtype == GS_F32) return run<float>(update, batch, m, n, steps, a, b, c, eps, out, workspace, stream);
     if (dtype == GS_BF16) return run<__bf16>(update, batch, m, n, steps, a, b, c, eps, out, workspace, stream);
