@@ -202,10 +202,11 @@ struct ProductArgs {
 };
 
 // One block from memory to LDS, 16 bytes a lane, without registers in between. lds: byte address, the same in the
-// whole wave. The load counts in vmcnt; only LDS is written, so no register waits for it.
+// whole wave; the instruction takes it from m0, which the compiler sets (a write of the statement's own it would not know
+// of: m0 is no register that can be named as clobbered). The load counts in vmcnt; only LDS is written, so no register
+// waits for it.
 __device__ __forceinline__ void load_block(const _Float16 *src, uint32_t lane_bytes, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(lane_bytes), "s"(src)
-                 : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(lds), "v"(lane_bytes), "s"(src) : "memory");
 }
 
 // Until at most OUTSTANDING of this wave's loads are under way and its reads of LDS are done, and until every wave of the
