@@ -4,7 +4,7 @@
 tokens are sorted by expert, every expert is a two-layer perceptron on its own rows, and the weighted results return
 to their tokens. The backward is written out call by call; weight matrices move by their orthogonalised momentum.
 The experts' own products are plain library products, one per expert and direction. ``ColorHead`` maps features to
-colours in (0, 1). Both keep float32 parameters and compute in the type they are given.
+colours in (0, 1). Both keep float32 parameters; the layer computes in the type it is made for, the head in float32.
 """
 from __future__ import annotations
 
@@ -68,7 +68,10 @@ class ExpertLayer(_Momentum):
         return out
 
     def forward(self, x):
-        """(y, what the backward needs) of x [tokens, dim]. Synchronises once, for the experts' row counts."""
+        """(y, what the backward needs) of x [tokens, dim] of the layer's type. Synchronises once, for the experts' row
+        counts."""
+        if x.dtype != self.dtype:
+            raise TypeError(f"x must be {self.dtype}, the layer's type (got {x.dtype})")
         p, T, K = self.parameters, x.shape[0], self.choices
         norm = binding.gs_layer_norm_fwd(x, p["norm_weight"], p["norm_bias"])
         best, ids = (norm.y.float() @ p["router"]).topk(K, dim=1)
