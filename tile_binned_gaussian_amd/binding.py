@@ -606,6 +606,14 @@ def _arg(t, name, dtype, device, shape):
     return t.data_ptr()
 
 
+def _int32(v, name):
+    """v as a C int; ctypes would cut it to 32 bits."""
+    v = int(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits (got {v})")
+    return v
+
+
 def _stream_int(stream):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
@@ -736,7 +744,7 @@ def gs_expert_plan(ids, experts, out=None, stream=None, workspace=None) -> Exper
     if ids.dim() != 2 or ids.shape[1] < 1:
         raise ValueError("ids must be [tokens, choices]")
     dev = ids.device
-    (T, K), E = ids.shape, int(experts)
+    (T, K), E = ids.shape, _int32(experts, "experts")
     if E < 1:
         raise ValueError("experts must be >= 1")
     if out is None:
@@ -832,13 +840,13 @@ def gs_orthogonalize(update, steps=5, coefficients=(3.4445, -4.7750, 2.0315), ep
     pu = _arg(update, "update", update.dtype, dev, update.shape)
     m, n = update.shape[-2], update.shape[-1]
     B = update.shape[0] if update.dim() == 3 else 1
-    a, b, c = coefficients
+    (a, b, c), steps = coefficients, _int32(steps, "steps")
     if out is None:
         out = torch.empty_like(update)
     else:
         _arg(out, "out", update.dtype, dev, update.shape)
     ws, pws, room = _room(lib.gs_orthogonalize_workspace_bytes(B, m, n), dev) if workspace is None \
         else _given_room(workspace, dev)
-    _check(lib.gs_orthogonalize(pu, B, m, n, int(steps), a, b, c, eps, code, out.data_ptr(), pws, room,
+    _check(lib.gs_orthogonalize(pu, B, m, n, steps, a, b, c, eps, code, out.data_ptr(), pws, room,
                                 _stream_int(stream)))
     return out
