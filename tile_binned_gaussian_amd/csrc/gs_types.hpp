@@ -64,20 +64,16 @@ __device__ __forceinline__ void store_pack(T *__restrict__ row, int64_t col, int
         if (col + j < dim) row[col + j] = v[j];
 }
 
-// N consecutive float32 values of an array of T at col (0 past the end), N a multiple or divisor of Pack<T>::kN.
+// N consecutive values of an array of T at col as float32 (0 past the end), whole packs.
 template <int N, typename T>
 __device__ __forceinline__ void load_floats(const T *__restrict__ row, int64_t col, int64_t dim, float *out) {
     constexpr int P = Pack<T>::kN;
-    if constexpr (N >= P) {
+    static_assert(N % P == 0, "whole packs");
 #pragma unroll
-        for (int i = 0; i < N / P; ++i) {
-            const typename Pack<T>::V v = load_pack(row, col + i * P, dim);
+    for (int i = 0; i < N / P; ++i) {
+        const typename Pack<T>::V v = load_pack(row, col + i * P, dim);
 #pragma unroll
-            for (int j = 0; j < P; ++j) out[i * P + j] = static_cast<float>(v[j]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) out[j] = col + j < dim ? static_cast<float>(row[col + j]) : 0.0f;
+        for (int j = 0; j < P; ++j) out[i * P + j] = static_cast<float>(v[j]);
     }
 }
 
