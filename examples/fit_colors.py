@@ -1,5 +1,8 @@
 """Trains a layer of experts to give the colours of a seeded scene's splats from their features, by rendering.
 
+The features hold the colours themselves (and the places), as an encoder's would: the example shows the training path
+and that its gradients are right, not what can be learned from less.
+
 Each step: features -> expert layer -> colour head -> gs_rasterize_fwd; the image's squared error against the scene's
 own rendering goes back through gs_rasterize_bwd, the head and the layer, and the weights take orthogonalised updates.
 

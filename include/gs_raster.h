@@ -352,7 +352,8 @@ gs_status gs_rasterize_bwd(const float *means2d, const float *conics, const floa
  * sums and statistics are formed in float32 or wider and rounded once where they are stored; so are products, but for
  * gs_orthogonalize's, whose operands are held as it says. The order of every sum depends on the sizes alone: the same
  * inputs give the same bits on every run. Rows may start at any multiple of the element's size. Outputs and workspaces
- * may overlap neither an input nor each other (GS_ERR_INVALID_ARG), but for gs_orthogonalize's out, which may be update.
+ * may overlap neither an input nor each other (GS_ERR_INVALID_ARG), but for gs_orthogonalize's out, which may be
+ * update.
  */
 typedef enum gs_dtype {
     GS_F32 = 0,
@@ -435,11 +436,12 @@ gs_status gs_expert_combine_bwd(const void *source, const int32_t *offsets, cons
  * X = update / (|update| + eps) with the Frobenius norm of each matrix; `steps` times A = X X^T, X = a X +
  * (b A + c A A) X, with (a, b, c) = coefficients (X transposed around the steps where m > n, which gives the same
  * result with the smaller products). out = X, in update's type.
- * update, out [batch, m, n] of dtype; out may be update itself. The norm's sums are float64. X, A and b A + c A A are held
- * as pairs of float16 (high and low part, 22 bits together, scaled by a power of two), for every type and in every step;
- * a product leaves out what the two low parts give, 2^-22 of it, and sums in float32. Every singular value must
- * stay below 15.9, so that those of A stay below 253, and every entry of b A + c A A below 255 in magnitude, as they do for
- * coefficients that move the singular values towards 1.
+ * update, out [batch, m, n] of dtype; out may be update itself. The norm's sums are float64. X, A and b A + c A A are
+ * held as pairs of float16 (high and low part, 22 bits together, scaled by a power of two), for every type and in every
+ * step; entries of X below 2^-15 to 2^-37 instead, of the other two below 2^-11 to 2^-33. A product leaves out what
+ * the two low parts give, 2^-22 of it, and sums in float32. Every singular value must stay below 15.9, so that those of
+ * A stay below 253, and every entry of b A + c A A below 255 in magnitude, as they do for coefficients that move the
+ * singular values towards 1.
  * A matrix that holds an infinity or NaN gives NaN; others in the batch are not affected.
  * Limits: 0 <= batch <= 65535, 1 <= m, n <= 65536, batch * m * n < 2^40, 0 <= steps <= 100. Asynchronous.
  * workspace: gs_orthogonalize_workspace_bytes(batch, m, n) bytes (0 for sizes out of range, and for matrices small

@@ -45,9 +45,9 @@ SETTLING = (1.875, -1.25, 0.375)  # moves every singular value to 1 and stays th
 def test_the_error_is_the_results_rounding(m, n, kind, name):
     """Operands of 22 bits are off by 2^-22, which is 2^-11 of a float16 result's rounding (2^-14 of bfloat16's). Twelve
     steps with the default coefficients let a singular value's relative error grow by up to 122 (the product of
-    f'(s) s / f(s) along its orbit), and by 7 in the mean square; fewer steps and the other coefficients by less. 122 * 2^-11
-    is 0.06 of the rounding and, added in squares, 0.18% of it; ten such roundings make 1.8% at the most. The rounding's
-    own 2-norm is taken as it is: of the exact result, rounded."""
+    f'(s) s / f(s) along its orbit), and by 7 in the mean square; fewer steps and the other coefficients by less. 122 *
+    2^-11 is 0.06 of the rounding and, added in squares, 0.18% of it; ten such roundings make 1.8% at the most. The
+    rounding's own 2-norm is taken as it is: of the exact result, rounded."""
     dtype = tu.DTYPES[name]
     u = matrix(kind, m, n, m + len(kind)).to(dtype)
     for steps, coefficients in ((5, tu.COEFFICIENTS), (9, tu.COEFFICIENTS), (12, tu.COEFFICIENTS), (12, SETTLING)):

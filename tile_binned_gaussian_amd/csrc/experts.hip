@@ -6,7 +6,7 @@
 // the bytes, are each read or written once. No atomics on memory: results do not depend on the order of workgroups.
 //
 // All of it is bound by memory. 32768 tokens, 8 choices of 64 experts, rows of 2048 bf16 (2.4 GB): plan 13 us, dispatch
-// 208 to 230 us (5.3 to 5.8 TB/s), combine 207 us (5.8 TB/s, what plain reads reach); 16384 x 2 rows of 4096 bf16: combine's
+// 231 us (5.2 TB/s), combine 205 us (5.9 TB/s, near what plain reads reach); 16384 x 2 rows of 4096 bf16: combine's
 // backward 128 us (5.1 TB/s). A large copy runs at 4.8 TB/s. Few tokens are three launches of 3 to 4 us each.
 #include "gs_types.hpp"
 
@@ -180,8 +180,9 @@ __device__ __forceinline__ RowItem row_item(int64_t i, int parts) {
 }
 
 // ONCE: the row is read or written this one time, and takes no room in the caches from what is read again (a choice by
-// measurement: with it the combine of 32768 x 8 rows of 2048 bf16 takes 230 us instead of 266, and its backward's stores of
-// 30000 x 2 rows of 2000 float32 save 5%; the dispatch's stores and the backward's loads are better without. Rows that fit the caches cost it up to 0.7 us a call).
+// measurement: with it in its loads the combine of 32768 x 8 rows of 2048 bf16 takes 205 us instead of 221, and in its
+// stores the backward of 30000 x 2 rows of 2000 float32 232 instead of 254; the dispatch's stores and the backward's
+// loads are better without. Rows that fit the caches cost it up to 0.7 us a call).
 template <typename T, int V, bool ONCE = false>
 __device__ __forceinline__ void load_row(const T *row, int64_t col, int64_t dim, typename Pack<T>::V *v) {
 #pragma unroll
@@ -298,7 +299,7 @@ __global__ __launch_bounds__(kRowThreads) void expert_combine_kernel(const T *__
 
 // One wave a token, all of its columns in turn: the dot products need whole rows. The choices follow each other: the
 // token's gradient comes from L1 for all but the first, and with several choices' rows under way at once fewer waves fit
-// (16384 x 2 rows of 4096 bf16, with its combine: 208 us, four at once 257, two at once 211).
+// (16384 x 2 rows of 4096 bf16, with its combine: four at once took a quarter longer, two at once 1%).
 template <typename T, int V>
 __global__ __launch_bounds__(kRowThreads) void expert_combine_bwd_kernel(
     const T *__restrict__ source, const int32_t *__restrict__ kept, const int32_t *__restrict__ rows,
@@ -356,7 +357,8 @@ gs_status check_rows(const char *name, int64_t tokens, int64_t choices, int expe
 }
 
 // Packs a lane holds at once, and the parts of a row that make: as many as the row has, up to four, so that a token's
-// whole row is under way at once (32768 x 8 rows of 2048 bf16 with four packs 507 us, with two 528, with one 533).
+// whole row is under way at once (32768 x 8 rows of 2048 bf16: the combine with four packs 205 us, with two 211, with
+// one 212; the dispatch 236, 228 and 230; combine's backward of 16384 x 2 rows of 4096 bf16 127, 129 and 137).
 inline int row_packs(int64_t dim, int pack) {
     const int64_t packs = (dim + pack - 1) / pack;
     return packs <= kWave ? 1 : packs <= 2 * kWave ? 2 : 4;

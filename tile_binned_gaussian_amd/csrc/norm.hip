@@ -7,9 +7,9 @@
 // workspace and a second kernel adds them in a fixed order. Wider rows than the registers hold take the kernels that
 // read the row again from L2.
 //
-// Both directions are bound by memory: the forward moves two arrays of x's size and the backward three, and a large copy
-// on this card runs at 4.8 TB/s. 32768 x 2048 bf16 forward 48 us (5.5 TB/s), 32768 x 4096 bf16 backward 146 us (5.5 TB/s, 7 us
-// of it the second kernel). Below some hundred rows a call is its launches and the host's work.
+// Both directions are bound by memory: the forward moves two arrays of x's size and the backward three, and a large
+// copy on this card runs at 4.8 TB/s. 32768 x 2048 bf16 forward 48 us (5.5 TB/s), 32768 x 4096 bf16 backward 148 us
+// (5.4 TB/s, 7 us of it the second kernel). Below some hundred rows a call is its launches and the host's work.
 #include "gs_types.hpp"
 
 namespace gs {
@@ -203,7 +203,8 @@ __global__ __launch_bounds__(row_threads(G)) void norm_bwd_kernel(const T *__res
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
     int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + group;
     // The next row is on its way while one is worked on: too few rows are in flight on a CU otherwise. Rows pass the
-    // caches by (16384 x 4096 float32 127 us, through them 147; the forward, with one array less, is faster through them).
+    // caches by (16384 x 4096 float32 129 us, through them 144; the forward, with one array less, is faster through
+    // them).
     typename Pack<T>::V px[V], pg[V];
     float pm = 0.0f, pr = 0.0f;
     const auto fetch = [&](int64_t at) {
@@ -463,8 +464,8 @@ gs_status run_fwd(const void *x, const void *weight, const void *bias, int64_t r
     }
 #undef GS_NORM_FWD
     hipLaunchKernelGGL((norm_fwd_wide_kernel<T, W>),
-                       dim3(static_cast<unsigned>(rows < kWideFwdBlocks ? rows : kWideFwdBlocks)), dim3(kThreads), 0, stream,
-                       static_cast<const T *>(x), static_cast<const W *>(weight), static_cast<const W *>(bias), rows,
+                       dim3(static_cast<unsigned>(rows < kWideFwdBlocks ? rows : kWideFwdBlocks)), dim3(kThreads), 0,
+                       stream, static_cast<const T *>(x), static_cast<const W *>(weight), static_cast<const W *>(bias), rows,
                        dim, eps, static_cast<T *>(y), mean, rstd);
     GS_LAUNCH_TRY("norm_fwd_wide_kernel");
     return ok();
@@ -480,7 +481,8 @@ gs_status run_bwd(const void *x, const void *weight, const float *mean, const fl
     T *to = static_cast<T *>(grad_x);
     // slices of the rows: of short rows as many as the workspace has room for, each of whole turns of a workgroup
     const int cols = static_cast<int>(dim < kThreads ? dim : kThreads);
-    const int64_t turns = (rows + kThreads / cols - 1) / (kThreads / cols), most = dim < kThreads ? kBwdBlocks : kWideBwdParts;
+    const int64_t turns = (rows + kThreads / cols - 1) / (kThreads / cols);
+    const int64_t most = dim < kThreads ? kBwdBlocks : kWideBwdParts;
     int64_t parts = turns < most ? turns : most;
 #define GS_NORM_BWD(G, V)                                                                                           \
     if (shape.lanes == G && shape.packs == V) {                                                                     \
@@ -513,7 +515,8 @@ gs_status run_bwd(const void *x, const void *weight, const float *mean, const fl
     }
     const int64_t blocks = (dim + kWave - 1) / kWave;
     hipLaunchKernelGGL((norm_reduce_kernel<W>),
-                       dim3(static_cast<unsigned>(blocks < kReduceBlocks ? blocks : kReduceBlocks), grad_bias ? 2u : 1u),
+                       dim3(static_cast<unsigned>(blocks < kReduceBlocks ? blocks : kReduceBlocks),
+                            grad_bias ? 2u : 1u),
                        dim3(kReduceThreads), 0, stream, partial, static_cast<int>(parts), dim,
                        static_cast<W *>(grad_weight), static_cast<W *>(grad_bias));
     GS_LAUNCH_TRY("norm_reduce_kernel");
@@ -567,7 +570,8 @@ extern "C" gs_status gs_layer_norm_fwd(const void *x, const void *weight, const 
 
 extern "C" size_t gs_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
     if (rows < 0 || rows >= kLimit || dim < 1 || dim >= kLimit) return 0;
-    return static_cast<size_t>(rows < kBwdBlocks ? rows : kBwdBlocks) * 2 * static_cast<size_t>(partial_width(dim)) * sizeof(float);
+    return static_cast<size_t>(rows < kBwdBlocks ? rows : kBwdBlocks) * 2 *
+           static_cast<size_t>(partial_width(dim)) * sizeof(float);
 }
 
 extern "C" gs_status gs_layer_norm_bwd(const void *x, const void *weight, const float *mean, const float *rstd,

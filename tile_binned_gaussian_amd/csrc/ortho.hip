@@ -3,16 +3,18 @@
 // float32 has no matrix-core rate to speak of next to float16's (157 against 2500 TFLOP/s), so every operand is held
 // as a pair of float16, high and low part (22 bits together), and a product of two operands is three matrix products,
 // high high + high low + low high, summed in float32. The term left out is 2^-22 of the product.
-// Every step takes both halves, whatever the result's type: with the default coefficients an error of an operand grows by
-// up to 122 in twelve steps, and steps on the high halves alone left float16 results up to 50 times their own rounding off.
-// The time of large matrices is the products' (4096 x 4096: all but 0.05 of 3.4 ms, 1.2 PFLOP/s, the rate of this card's
-// large float16 library product; its clock falls under the load). Small and middling ones are launches and the latency of
-// their chains.
+// Every step takes both halves, whatever the result's type: with the default coefficients an error of an operand grows
+// by up to 122 in twelve steps, and steps on the high halves alone left float16 results up to 50 times their own
+// rounding off.
+// The time of large matrices is the products' (4096 x 4096: all but 0.05 of 3.5 ms, at 1.2 PFLOP/s, the rate of this
+// card's large float16 library product; its matrix cores are busy 0.82 of the time, and its clock falls under the load).
+// Small and middling ones are launches and the latency of their chains.
 //
-// X holds values scaled by 2^12 and the Gram side by 2^8: entries of X are at most its largest singular value and those of
-// A its square, so both reach float16's largest value at singular values of 16, and the scale keeps the low parts of all
-// but the smallest ones out of float16's subnormals. A matrix whose norm is far below eps stays small through all steps;
-// its X takes a larger scale (x_scale). Its A may then underflow, which counts for nothing next to a.
+// X holds values scaled by 2^12 and the Gram side by 2^8: entries of X are at most its largest singular value and those
+// of A its square, so both reach float16's largest value at singular values of 16. The low parts of entries below 2^-15
+// of X are float16's subnormals: they are held to 2^-37 itself, not to 22 bits of their own, which is as exact next to
+// a norm of 1. A matrix whose norm is far below eps stays small through all steps; its X takes a larger scale
+// (x_scale). Its A may then underflow, which counts for nothing next to a.
 #include <type_traits>
 
 #include "gs_types.hpp"
@@ -102,7 +104,7 @@ __device__ __forceinline__ double workgroup_sum(double v, double *s_part) {
     return v;
 }
 
-// Partial sums of squares of matrix blockIdx.y in float64. 4096 x 4096 bf16: 13 us (2.6 TB/s), 0.6% of the call.
+// Partial sums of squares of matrix blockIdx.y in float64. 4096 x 4096 bf16: 13 us (2.6 TB/s), 0.4% of the call.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_norm_kernel(const T *__restrict__ update, int64_t count,
                                                               double *__restrict__ partial) {
@@ -124,7 +126,8 @@ __global__ __launch_bounds__(kThreads) void ortho_norm_kernel(const T *__restric
 }
 
 // X = update / (norm + eps) in both orders: `direct` holds the update's rows, `turned` its columns; 64 x 64 elements
-// a workgroup, zeros in the padding. Writes the matrix's scales. Bound by memory: 4096 x 4096 bf16 33 us for 168 MB (5.0 TB/s).
+// a workgroup, zeros in the padding. Writes the matrix's scales. Bound by memory: 4096 x 4096 bf16 30 us for 168 MB (5.6
+// TB/s).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ortho_split_kernel(const T *__restrict__ update,
                                                                const double *__restrict__ partial, int parts, int m,
@@ -365,8 +368,9 @@ __device__ __forceinline__ void finish_four(const ProductArgs &a, const Scales &
 // A workgroup of WR x WC waves makes a T x T tile, each wave its part of it. A stage of the LDS ring holds 16 columns of
 // both halves; while one is multiplied the next is there already (its operands are read ahead of the barrier) and two
 // more are on their way.
-// Two or three waves a SIMD, so that one has products to issue where another waits at the barrier (8 x 1024 x 1024 732 us).
-// The reads of LDS that smaller parts cost are a third of its rate.
+// Two or three waves a SIMD, so that one has products to issue where another waits at the barrier: matrix cores busy
+// 0.82 of the time with 256 and 192, 0.53 with 180 tiles of 128, where a launch's start and end weigh more. LDS is busy
+// 0.21, 0.37 and 0.27 of it, without bank conflicts.
 template <int T, int WR, int WC>
 __global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (T <= 128 ? 2 : 1)) void ortho_product_kernel(ProductArgs a) {
     constexpr int kStages = 4;
@@ -502,12 +506,13 @@ __device__ __forceinline__ f32x4 *part_at(const ProductArgs &a, size_t tile, int
 }
 
 // A 64 x 64 tile by WAVES waves that share its sum: each takes its own range of the columns, for the whole tile, with
-// operands straight from memory into registers, whose order a block has (2500 x 1111 f32: 322 us next to 341 with these tiles
-// through LDS in eight stages; 171 tiles of depth 2528 take 21 us, 13 TB/s out of L2). No wave waits for another until the sums
-// are joined through LDS, in order, so the time of a few tiles is not the latency of a barrier at every stage.
-// Where there are few tiles, several workgroups share one's columns, because a unit draws only so much from L2 (300 x 4000:
-// 15 tiles by 15 units 24 us). Each leaves its part in memory for the kernel that joins them. (Joined by the last workgroup
-// to come, a call was slower than without: making the parts visible to it costs every unit its L2.)
+// operands straight from memory into registers, whose order a block has (2500 x 1111 f32: 6% of the call less than with
+// these tiles through LDS in eight stages; 171 tiles of depth 2528 read 221 MB in 21 us, 10.5 TB/s, 0.74 of it from L2).
+// No wave waits for another until the sums are joined through LDS, in order, so the time of a few tiles is not the
+// latency of a barrier at every stage. Where there are few tiles, several workgroups share one's columns, because a unit
+// draws only so much from L2 (300 x 4000: 15 tiles by 15 units 24 us). Each leaves its part in memory for the kernel
+// that joins them. (Joined by the last workgroup to come, a call was slower than without: making the parts visible to it
+// costs every unit its L2.)
 template <int WAVES, bool SHARED>
 __global__ __launch_bounds__(WAVES *kWave) void ortho_product_direct_kernel(ProductArgs a) {
     constexpr int kTile = 64, kPanels = kTile / kPanel;
@@ -648,9 +653,10 @@ __global__ __launch_bounds__(kThreads) void ortho_finish_kernel(Planes x, const 
 // ------------------------------------------------------------------------------------------------------------
 // small matrices: one workgroup a matrix, all steps in one launch
 //
-// 16 x 96 x 160 f32 30 us, as launches of the kernels above 95; 128 x 128 37 and 99, 32 x 1000 27 and 87. A step is 5.4 us: six
-// phases with a barrier each. A SIMD's vector instructions take half of it (halves and addresses) and its matrix products
-// a third; LDS is busy a third of the time, without bank conflicts (with them, and addresses formed in full: 36 us).
+// 16 x 96 x 160 f32 30 us, as launches of the kernels above 95; 128 x 128 37 and 99, 32 x 1000 27 and 87. A step is 5.4
+// us: six phases with a barrier each. A SIMD's vector instructions take half of it (halves and addresses) and its matrix
+// products a third; LDS is busy a third of the time, without bank conflicts (with them, and addresses formed in full: 36
+// us).
 //
 // The 32 x 32 tiles of X are dealt to 16 waves, which keep theirs in float32 registers as the matrix cores leave a
 // result (lane: column lane % 32; register 4 g + k: row 8 g + lane / 32 * 4 + k). Once a step every wave puts its
@@ -965,8 +971,8 @@ struct Layout {
 int tile_edge(int64_t batch, int rows, int cols, bool symmetric);
 
 // Workgroups that share the sum of each tile of edge 64: as many as leave no unit without one, with four blocks or more
-// for each wave. 300 x 4000 f32: with shared tiles 184 us, without 240; 512 x 4000 208 and 258; 64 x 3000 bf16 115 and 142. By two the second
-// launch eats what it gives.
+// for each wave. 300 x 4000 f32: with shared tiles 180 us, without 240; 512 x 4000 207 and 258; 64 x 3000 bf16 103 and
+// 142. By two the second launch eats what it gives.
 int tile_splits(int64_t tiles, int depth) {
     const int64_t most = kUnits / tiles, work = depth / kDepth / 32;
     const int64_t n = most < work ? most : work;
@@ -1013,10 +1019,12 @@ gs_status check_sizes(int64_t batch, int64_t m, int64_t n) {
     return GS_OK;
 }
 
-// The tile edge of a product: least rounds of workgroups over the chip, times a tile's work, times what a tile of
-// that edge takes of the matrix cores' time next to the largest (its operands come through L2 and LDS more often). Measured
-// at depth 4096 with both halves, a round of tiles on all units: 324 us at 256, 196 at 192 (1.08 times the time of an
-// entry), about 75 at 128 (1.3) and 31 at 64 (2).
+// The tile edge of a product: least rounds of workgroups over the chip, times a tile's entries, times what an entry costs
+// in a tile of that edge next to the largest (its operands come through L2 and LDS more often). A round of 252 tiles at
+// depth 4096 takes 340 us at 256, 230 at 192, 146 at 128 and 46 at 64: 1.20, 1.71 and 2.18 times the time of an entry.
+// The costs are lower, because rounds are seldom full and a tile that has its unit's L2 and clock to itself is faster:
+// over 90 shapes for which it matters (130 to 4096 rows and columns, stacks of up to 16) calls took 0.3% longer with
+// 1.2, 1.6 and 2.4 and 2.8% longer with 1.2, 1.7 and 2.2 (2% less with 1.18, 1.41 and 3.0).
 int tile_edge(int64_t batch, int rows, int cols, bool symmetric) {
     int best = 0;
     double least = 0.0;
