@@ -312,6 +312,7 @@ __global__ __launch_bounds__(kRowThreads) void expert_combine_bwd_kernel(
         for (int64_t k = 0; k < choices; ++k) {
             const int64_t r = rows[t * choices + k];
             const bool valid = r >= 0 && r < pairs;
+            double total = 0.0;  // of the parts' sums: a row may be very long, and a long float32 chain drifts
             float dot = 0.0f;
             if (valid) {
                 const float w = weights[t * choices + k];
@@ -320,6 +321,7 @@ __global__ __launch_bounds__(kRowThreads) void expert_combine_bwd_kernel(
                     typename Pack<T>::V g[V], v[V];
                     load_row<T, V>(grad_y + t * dim, it.col, dim, g);
                     load_row<T, V>(source + r * dim, it.col, dim, v);
+                    dot = 0.0f;
 #pragma unroll
                     for (int a = 0; a < V; ++a)
 #pragma unroll
@@ -329,8 +331,9 @@ __global__ __launch_bounds__(kRowThreads) void expert_combine_bwd_kernel(
                             v[a][j] = static_cast<T>(w * gf);
                         }
                     store_row<T, V, true>(grad_source + r * dim, it.col, dim, v);
+                    total += static_cast<double>(dot);
                 }
-                dot = group_sum<kWave>(dot);
+                dot = group_sum<kWave>(static_cast<float>(total));
             }
             if (threadIdx.x % kWave == 0) grad_weights[t * choices + k] = dot;
         }
