@@ -243,13 +243,13 @@ def _own(s):
         return gs.gs_expert_route_bwd(s["logits"], gs.ExpertRoute(*s["route"]), s["grad_weights"], s["grad_loss"],
                                       renormalize=case["renormalize"])
     if op == "checkpoint":
-        return gs.gs_dequantize_f8(gs.gs_quantize_f8(s["x"]), dtype=dt)
+        return gs.gs_dequantize(gs.gs_quantize(s["x"]), dtype=dt)
     plan = gs.ExpertPlan(s["offsets"], s["rows"], s["pairs"])
     x = gs.Quantized(*s["x"], case["dim"])
     if op == "product":
-        return gs.gs_expert_product_f8(x, gs.Quantized(*s["weight"], case["dim"]), plan, gather=case["gather"],
+        return gs.gs_expert_product(x, gs.Quantized(*s["weight"], case["dim"]), plan, gather=case["gather"],
                                        relu=case["relu"], dtype=dt)
-    return gs.gs_expert_weight_grad_f8(x, s["grad"], plan, gather=case["gather"])
+    return gs.gs_expert_weight_grad(x, s["grad"], plan, gather=case["gather"])
 
 
 def run(state):
