@@ -13,7 +13,9 @@
  *                     gs_rasterize_fwd_bins.
  * The last group trains a layer of experts that predicts the splats' attributes (gs_rasterize_bwd gives the
  * gradient it starts from): gs_layer_norm_fwd and _bwd, gs_expert_plan, gs_expert_dispatch, gs_expert_combine and
- * _bwd, gs_orthogonalize.
+ * _bwd, gs_orthogonalize; gs_expert_route and _bwd (the router, its counts and its balance loss), gs_quantize and
+ * gs_dequantize (values held in 8 bits), gs_expert_product and gs_expert_weight_grad (the experts' products and
+ * their weights' gradient from such values).
  *
  * Definitions follow these pages:
  *   [gsplat]     gsplat 1.0.0 Ruby gem, native C extension, intersections.c (gs_tile_bits, gs_bounds,
@@ -452,6 +454,83 @@ size_t gs_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n);
 gs_status gs_orthogonalize(const void *update, int64_t batch, int64_t m, int64_t n, int steps, float a, float b,
                            float c, float eps, int dtype, void *out, void *workspace, size_t workspace_bytes,
                            void *stream);
+
+/* The router: each token's best experts, their weights, how many tokens every expert got, and the balance loss.
+ *
+ * With p = softmax(logits[t]) over the experts: ids[t, k] is the expert of the k-th largest logit (the lower index first
+ * among equal ones), weights[t, k] the softmax over the chosen logits (renormalize != 0) or p of that expert.
+ *   counts[e] = pairs of expert e,  kept = tokens that were routed,  shares[e] = sum over those tokens of p_e / kept,
+ *   loss = experts * sum_e counts[e] / sum(counts) * shares[e]   (1 where all are equal; 0 if no token was routed).
+ * logits [tokens, experts] of dtype; mask [tokens] bytes or NULL: a token whose byte is 0 is left out, and so is one whose
+ * logits are all minus infinity: ids -1, weights 0, in no count. A logit of minus infinity is never chosen: a token with
+ * fewer others than choices gets -1 and 0 in the rest. A NaN is chosen first; it, or an infinity, makes the token's
+ * weights, the shares and the loss NaN.
+ * ids [tokens, choices] int32, weights [tokens, choices], counts [experts] int32, shares [experts], loss and kept one value.
+ * Limits: 0 <= tokens, 1 <= choices <= experts <= 4096, tokens * choices < 2^31. Asynchronous.
+ * workspace: gs_expert_route_workspace_bytes(tokens, experts) bytes (0 for sizes out of range and for few tokens).
+ */
+size_t gs_expert_route_workspace_bytes(int64_t tokens, int experts);
+
+gs_status gs_expert_route(const void *logits, const uint8_t *mask, int64_t tokens, int experts, int64_t choices,
+                          int renormalize, int dtype, int32_t *ids, float *weights, int32_t *counts, float *shares,
+                          float *loss, int32_t *kept, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient of the logits for L = sum(grad_weights * weights) + grad_loss * loss; the counts are constants of it, as the
+ * choices are. With g = grad_weights[t], w = weights[t], p = softmax(logits[t]), f_e = counts[e] / sum(counts):
+ *   through the weights  [j = ids_k] w_k (g_k - sum_i g_i w_i),  not renormalized  [j = ids_k] w_k g_k - p_j sum_i g_i w_i
+ *   through the loss     grad_loss * experts / kept * p_j (f_j - sum_e f_e p_e);   zeros for a token that was left out.
+ * logits, ids, weights, counts, kept and renormalize as the forward's; grad_weights [tokens, choices] and grad_loss (one
+ * value) float32, each may be NULL: zero. grad_logits [tokens, experts] of dtype. Limits as the forward's. Asynchronous.
+ */
+gs_status gs_expert_route_bwd(const void *logits, const int32_t *ids, const float *weights, const int32_t *counts,
+                              const int32_t *kept, const float *grad_weights, const float *grad_loss, int64_t tokens,
+                              int experts, int64_t choices, int renormalize, int dtype, void *grad_logits, void *stream);
+
+/* Values held in 8 bits: e4m3 (OCP; 448 the largest, no infinity) and, for each block of 128 along a row, a byte b that
+ * stands for the scale 2^(b - 127). A row of `dim` values takes whole blocks, ceil(dim / 128) of them, zeros past its end:
+ * values [rows, blocks * 128], from a multiple of 16 bytes on, scales [rows, blocks].
+ *
+ * gs_quantize: b - 127 is the least e of [-126, 127] with |v| <= 448 * 2^e for the block's finite values (0 for a block
+ * of zeros); each value is v / 2^e to the nearest e4m3, ties to even. Infinities and NaN become NaN. x [batch, rows, dim]
+ * of dtype. transpose != 0: of the transposed matrices, blocks along the rows of x: values
+ * [batch, dim, ceil(rows / 128) * 128], scales [batch, dim, ceil(rows / 128)].
+ * gs_dequantize: x [rows, dim] = value * scale, rounded to dtype once; a finite value that would round to infinity
+ * becomes the largest of dtype.
+ * Limits: 0 <= batch * rows < 2^31, 1 <= dim < 2^31, with transpose batch * dim < 2^31. Asynchronous.
+ */
+gs_status gs_quantize(const void *x, int64_t batch, int64_t rows, int64_t dim, int transpose, int dtype,
+                         void *values, void *scales, void *stream);
+
+gs_status gs_dequantize(const void *values, const void *scales, int64_t rows, int64_t dim, int dtype, void *x,
+                           void *stream);
+
+/* Products of rows sorted by expert with the experts' weights, both held in 8 bits along the sum's axis:
+ *   out[r, n] = sum_k x[r, k] * weight[e, n, k] for the rows [offsets[e], offsets[e + 1]) of expert e, summed in float32;
+ *   relu != 0: max(0, .) of it; the rows from offsets[experts] on become zeros.
+ * x values and scales of [x_rows, dim]; weight of [experts, cols, dim]; out [rows, cols] of dtype. offsets as
+ * gs_expert_plan wrote them, or NULL: one expert has all rows. pairs NULL: x holds the sorted rows, x_rows = rows. pairs
+ * as gs_expert_plan wrote them: x holds the tokens, rows = x_rows * choices, and row r is token pairs[r] / choices.
+ * A byte 255 of scales makes its block NaN. Offsets and pairs out of range are taken to its ends.
+ * Limits: 0 <= rows < 2^31, 1 <= dim, cols < 2^31, 1 <= experts <= 4096. Asynchronous.
+ */
+gs_status gs_expert_product(const void *x, const void *x_scales, const void *weight, const void *weight_scales,
+                               const int32_t *offsets, const int32_t *pairs, int64_t rows, int64_t x_rows,
+                               int64_t choices, int experts, int64_t dim, int64_t cols, int relu, int dtype, void *out,
+                               void *stream);
+
+/* Gradient of the experts' weights, with the activations held in 8 bits:
+ *   out[e, k, n] = sum over the rows r of expert e of x[r, k] * grad[r, n], in float32; zeros for an expert without rows.
+ * x, offsets, pairs, rows, x_rows and choices as in gs_expert_product; grad [rows, cols] of dtype, whose rows from
+ * offsets[experts] on are not read; out [experts, dim, cols] float32. Every product is exact.
+ * workspace: gs_expert_weight_grad_workspace_bytes(rows, experts, dim, cols) bytes (0 for sizes out of range and where
+ * the experts' matrices alone fill the chip). Limits as gs_expert_product's. Asynchronous.
+ */
+size_t gs_expert_weight_grad_workspace_bytes(int64_t rows, int experts, int64_t dim, int64_t cols);
+
+gs_status gs_expert_weight_grad(const void *x, const void *x_scales, const void *grad, const int32_t *offsets,
+                                   const int32_t *pairs, int64_t rows, int64_t x_rows, int64_t choices, int experts,
+                                   int64_t dim, int64_t cols, int dtype, float *out, void *workspace,
+                                   size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

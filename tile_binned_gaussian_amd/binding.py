@@ -26,7 +26,10 @@ EXPORTS = ("gs_last_error", "gs_isect_workspace_bytes", "gs_isect_tiles", "gs_so
            "gs_project_fwd", "gs_bin_tiles", "gs_rasterize_fwd_bins", "gs_set_spin_limit", "gs_device_check",
            "gs_sort_keys_static", "gs_layer_norm_fwd", "gs_layer_norm_bwd_workspace_bytes", "gs_layer_norm_bwd",
            "gs_expert_plan_workspace_bytes", "gs_expert_plan", "gs_expert_dispatch", "gs_expert_combine",
-           "gs_expert_combine_bwd", "gs_orthogonalize_workspace_bytes", "gs_orthogonalize")
+           "gs_expert_combine_bwd", "gs_orthogonalize_workspace_bytes", "gs_orthogonalize",
+           "gs_expert_route_workspace_bytes", "gs_expert_route", "gs_expert_route_bwd", "gs_quantize",
+           "gs_dequantize", "gs_expert_product", "gs_expert_weight_grad_workspace_bytes",
+           "gs_expert_weight_grad")
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # gs_dtype
 
@@ -98,6 +101,19 @@ def load_library(path: str = LIB_PATH):
     lib.gs_orthogonalize_workspace_bytes.argtypes, lib.gs_orthogonalize_workspace_bytes.restype = [I64, I64, I64], SZ
     lib.gs_orthogonalize.argtypes = [P, I64, I64, I64, I32, F, F, F, F, I32, P, P, SZ, P]
     lib.gs_orthogonalize.restype = I32
+    lib.gs_expert_route_workspace_bytes.argtypes, lib.gs_expert_route_workspace_bytes.restype = [I64, I32], SZ
+    lib.gs_expert_route.argtypes = [P, P, I64, I32, I64, I32, I32, P, P, P, P, P, P, P, SZ, P]
+    lib.gs_expert_route.restype = I32
+    lib.gs_expert_route_bwd.argtypes = [P, P, P, P, P, P, P, I64, I32, I64, I32, I32, P, P]
+    lib.gs_expert_route_bwd.restype = I32
+    lib.gs_quantize.argtypes, lib.gs_quantize.restype = [P, I64, I64, I64, I32, I32, P, P, P], I32
+    lib.gs_dequantize.argtypes, lib.gs_dequantize.restype = [P, P, I64, I64, I32, P, P], I32
+    lib.gs_expert_product.argtypes = [P, P, P, P, P, P, I64, I64, I64, I32, I64, I64, I32, I32, P, P]
+    lib.gs_expert_product.restype = I32
+    lib.gs_expert_weight_grad_workspace_bytes.argtypes = [I64, I32, I64, I64]
+    lib.gs_expert_weight_grad_workspace_bytes.restype = SZ
+    lib.gs_expert_weight_grad.argtypes = [P, P, P, P, P, I64, I64, I64, I32, I64, I64, I32, P, P, SZ, P]
+    lib.gs_expert_weight_grad.restype = I32
     _lib = lib
     return lib
 
@@ -849,4 +865,209 @@ def gs_orthogonalize(update, steps=5, coefficients=(3.4445, -4.7750, 2.0315), ep
         else _given_room(workspace, dev)
     _check(lib.gs_orthogonalize(pu, B, m, n, steps, a, b, c, eps, code, out.data_ptr(), pws, room,
                                 _stream_int(stream)))
+    return out
+
+
+# ----------------------------------------------------------------------------------------------------------------
+# The router of a layer of experts
+
+
+@dataclass
+class ExpertRoute:
+    ids: torch.Tensor  # [tokens, choices] int32: the experts, best first; -1 where there is none
+    weights: torch.Tensor  # [tokens, choices] float32
+    counts: torch.Tensor  # [experts] int32: pairs of each expert
+    shares: torch.Tensor  # [experts] float32: mean probability over the routed tokens
+    loss: torch.Tensor  # [] float32: the balance loss
+    kept: torch.Tensor  # [1] int32: tokens that were routed
+
+
+def _logits(logits, choices):
+    code = _element(logits, "logits")
+    if logits.dim() != 2 or logits.shape[1] < 1:
+        raise ValueError(f"logits must be [tokens, experts] (got {tuple(logits.shape)})")
+    T, E = logits.shape
+    if not 1 <= choices <= E:
+        raise ValueError(f"choices must be in [1, experts = {E}] (got {choices})")
+    return code, logits.device, T, _int32(E, "experts"), _arg(logits, "logits", logits.dtype, logits.device, (T, E))
+
+
+@_stream_scoped
+def gs_expert_route(logits, choices, mask=None, renormalize=True, out=None, stream=None, workspace=None) -> ExpertRoute:
+    """Each token's `choices` best experts of logits [tokens, experts] with their weights (softmax over the chosen
+    logits; renormalize=False: over all), the experts' counts and mean probabilities and the balance loss, experts *
+    sum(counts / sum(counts) * shares). mask [tokens] bool: tokens to route; a logit of -inf is never chosen."""
+    lib = load_library()
+    K = int(choices)
+    code, dev, T, E, pl = _logits(logits, K)
+    pm = None if mask is None else _arg(mask, "mask", torch.bool, dev, (T,))
+    if out is None:
+        floats, ints = torch.empty((E + 1,), dtype=torch.float32, device=dev), \
+            torch.empty((E + 1,), dtype=torch.int32, device=dev)
+        out = ExpertRoute(torch.empty((T, K), dtype=torch.int32, device=dev),
+                          torch.empty((T, K), dtype=torch.float32, device=dev), ints[:E], floats[:E],
+                          floats[E], ints[E:])
+        po = [t.data_ptr() for t in (out.ids, out.weights, out.counts, out.shares, out.loss, out.kept)]
+    else:
+        po = [_arg(out.ids, "ids", torch.int32, dev, (T, K)), _arg(out.weights, "weights", torch.float32, dev, (T, K)),
+              _arg(out.counts, "counts", torch.int32, dev, (E,)), _arg(out.shares, "shares", torch.float32, dev, (E,)),
+              _arg(out.loss, "loss", torch.float32, dev, ()), _arg(out.kept, "kept", torch.int32, dev, (1,))]
+    ws, pws, room = _room(lib.gs_expert_route_workspace_bytes(T, E), dev) if workspace is None \
+        else _given_room(workspace, dev)
+    _check(lib.gs_expert_route(pl, pm, T, E, K, int(bool(renormalize)), code, *po, pws, room, _stream_int(stream)))
+    return out
+
+
+@_stream_scoped
+def gs_expert_route_bwd(logits, route, grad_weights=None, grad_loss=None, renormalize=True, out=None, stream=None):
+    """Gradient of sum(grad_weights * weights) + grad_loss * loss for the logits of gs_expert_route, in their type.
+    grad_weights [tokens, choices] and grad_loss [] float32 (None: zero); renormalize as the forward's."""
+    lib = load_library()
+    K = route.ids.shape[1] if route.ids.dim() == 2 else 0
+    code, dev, T, E, pl = _logits(logits, K)
+    pi, pw = _arg(route.ids, "ids", torch.int32, dev, (T, K)), _arg(route.weights, "weights", torch.float32, dev, (T, K))
+    pc, pk = _arg(route.counts, "counts", torch.int32, dev, (E,)), _arg(route.kept, "kept", torch.int32, dev, (1,))
+    pg = None if grad_weights is None else _arg(grad_weights, "grad_weights", torch.float32, dev, (T, K))
+    ps = None if grad_loss is None else _arg(grad_loss, "grad_loss", torch.float32, dev, ())
+    if out is None:
+        out = torch.empty_like(logits)
+    else:
+        _arg(out, "grad_logits", logits.dtype, dev, (T, E))
+    _check(lib.gs_expert_route_bwd(pl, pi, pw, pc, pk, pg, ps, T, E, K, int(bool(renormalize)), code, out.data_ptr(),
+                                   _stream_int(stream)))
+    return out
+
+
+# ----------------------------------------------------------------------------------------------------------------
+# Values held in 8 bits, and the experts' products of them
+
+
+@dataclass
+class Quantized:
+    values: torch.Tensor  # [..., rows, blocks * 128] float8_e4m3fn, zeros past a row's end
+    scales: torch.Tensor  # [..., rows, blocks] uint8: b stands for 2^(b - 127)
+    dim: int  # values of a row
+
+
+def _held(q, name, device=None):
+    """(device, shape without the last axis, dim, address of the values, address of the scales) of a Quantized."""
+    if not isinstance(q, Quantized):
+        raise TypeError(f"{name} must be a Quantized (as gs_quantize gives)")
+    if not isinstance(q.values, torch.Tensor):
+        raise TypeError(f"{name} values must be a torch.Tensor")
+    lead, dim = tuple(q.values.shape[:-1]), int(q.dim)
+    if dim < 1:
+        raise ValueError(f"{name} must have at least one column")
+    blocks, dev = (dim + 127) // 128, q.values.device if device is None else device
+    pv = _arg(q.values, f"{name} values", torch.float8_e4m3fn, dev, lead + (blocks * 128,))
+    return dev, lead, dim, pv, _arg(q.scales, f"{name} scales", torch.uint8, dev, lead + (blocks,))
+
+
+@_stream_scoped
+def gs_quantize(x, transpose=False, out=None, stream=None) -> Quantized:
+    """x [..., rows, dim] (float32, bfloat16 or float16) held in 8 bits: e4m3 with a power of two for each block of 128
+    along a row. transpose=True: of the transposed matrices, [..., dim, rows]."""
+    lib = load_library()
+    code, dev = _element(x, "x"), x.device
+    if x.dim() < (2 if transpose else 1) or x.shape[-1] < 1:
+        raise ValueError(f"x must be [{'..., rows' if transpose else '...'}, dim] (got {tuple(x.shape)})")
+    px, dim = _arg(x, "x", x.dtype, dev, x.shape), x.shape[-1]
+    if transpose:
+        rows, lead, along = x.shape[-2], x.shape[:-2] + (dim,), x.shape[-2]
+        if rows < 1:
+            raise ValueError("x must have at least one row to transpose")
+        batch = x.numel() // (rows * dim)
+    else:
+        batch, rows, lead, along = 1, x.numel() // dim, x.shape[:-1], dim
+    blocks = (along + 127) // 128
+    if out is None:
+        out = Quantized(torch.empty(lead + (blocks * 128,), dtype=torch.float8_e4m3fn, device=dev),
+                        torch.empty(lead + (blocks,), dtype=torch.uint8, device=dev), along)
+        pv, ps = out.values.data_ptr(), out.scales.data_ptr()
+    else:
+        _, got, got_dim, pv, ps = _held(out, "out", dev)
+        if got != tuple(lead) or got_dim != along:
+            raise ValueError(f"out must hold {tuple(lead) + (along,)} (got {got + (got_dim,)})")
+    _check(lib.gs_quantize(px, batch, rows, dim, int(bool(transpose)), code, pv, ps, _stream_int(stream)))
+    return out
+
+
+@_stream_scoped
+def gs_dequantize(q, dtype=torch.float32, out=None, stream=None):
+    """The values that q stands for, [..., dim] of dtype (float32, bfloat16 or float16)."""
+    lib = load_library()
+    dev, lead, dim, pv, ps = _held(q, "q")
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16 (got {dtype})")
+    if out is None:
+        out = torch.empty(lead + (dim,), dtype=dtype, device=dev)
+    else:
+        _arg(out, "out", dtype, dev, lead + (dim,))
+    _check(lib.gs_dequantize(pv, ps, q.scales.numel() // q.scales.shape[-1], dim, _DTYPES[dtype], out.data_ptr(),
+                                _stream_int(stream)))
+    return out
+
+
+def _plan_rows(lead, plan, gather, device):
+    """(rows, x_rows, choices, experts, address of offsets, address of pairs) of x's rows under a plan."""
+    if len(lead) != 1:
+        raise ValueError("x must be [rows, dim]")
+    n = lead[0]
+    if plan is None:
+        if gather:
+            raise ValueError("gather needs a plan")
+        return n, n, 1, 1, None, None
+    T, K, E, po, _ = _plan_inputs(plan, device)
+    if n != (T if gather else T * K):
+        raise ValueError(f"x must have {T if gather else T * K} rows (got {n})")
+    pp = _arg(plan.pairs, "pairs", torch.int32, device, (T * K,)) if gather else None
+    return T * K, n, K, E, po, pp
+
+
+@_stream_scoped
+def gs_expert_product(x, weight, plan=None, gather=False, relu=False, dtype=torch.bfloat16, out=None, stream=None):
+    """Every expert's rows times its weight: out[r] = x[r] @ weight[e(r)].T, [rows, cols] of dtype, zeros in the rows past
+    the plan's kept ones; relu=True: max(0, .).
+
+    x: Quantized rows in the plan's order, [tokens * choices, dim], or with gather=True the tokens themselves,
+    [tokens, dim]. weight: Quantized [experts, cols, dim]. plan=None: one weight [cols, dim] for all rows."""
+    lib = load_library()
+    dev, lead, dim, px, pxs = _held(x, "x")
+    rows, x_rows, K, E, po, pp = _plan_rows(lead, plan, gather, dev)
+    _, wide, wdim, pw, pws = _held(weight, "weight", dev)
+    if wdim != dim or len(wide) != (1 if plan is None else 2) or wide[-1] < 1 or (plan is not None and wide[0] != E):
+        raise ValueError(f"weight must hold [{'' if plan is None else f'{E}, '}cols, {dim}] (got {wide + (wdim,)})")
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16 (got {dtype})")
+    cols = wide[-1]
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+    else:
+        _arg(out, "out", dtype, dev, (rows, cols))
+    _check(lib.gs_expert_product(px, pxs, pw, pws, po, pp, rows, x_rows, K, E, dim, cols, int(bool(relu)),
+                                    _DTYPES[dtype], out.data_ptr(), _stream_int(stream)))
+    return out
+
+
+@_stream_scoped
+def gs_expert_weight_grad(x, grad, plan=None, gather=False, out=None, stream=None, workspace=None):
+    """Every expert's weight gradient, x[rows of e].T @ grad[rows of e]: [experts, dim, cols] float32 ([dim, cols] without
+    a plan). x as in gs_expert_product, grad [rows, cols] of float32, bfloat16 or float16; its rows past the plan's
+    kept ones are not read."""
+    lib = load_library()
+    dev, lead, dim, px, pxs = _held(x, "x")
+    rows, x_rows, K, E, po, pp = _plan_rows(lead, plan, gather, dev)
+    code = _element(grad, "grad")
+    if grad.dim() != 2 or grad.shape[0] != rows or grad.shape[1] < 1:
+        raise ValueError(f"grad must be [{rows}, cols] (got {tuple(grad.shape)})")
+    pg, cols = _arg(grad, "grad", grad.dtype, dev, grad.shape), grad.shape[1]
+    shape = (dim, cols) if plan is None else (E, dim, cols)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _arg(out, "out", torch.float32, dev, shape)
+    ws, pws, room = _room(lib.gs_expert_weight_grad_workspace_bytes(rows, E, dim, cols), dev) if workspace is None \
+        else _given_room(workspace, dev)
+    _check(lib.gs_expert_weight_grad(px, pxs, pg, po, pp, rows, x_rows, K, E, dim, cols, code, out.data_ptr(), pws,
+                                        room, _stream_int(stream)))
     return out

@@ -1,0 +1,43 @@
+// 8-bit values on gfx950: e4m3 (OCP: 448 the largest, no infinity) with a scale 2^(byte - 127) for each block of 128 along
+// a row. Rows are padded to whole blocks with zeros, so a block is always 128 bytes at a multiple of 16.
+#pragma once
+
+#include "gs_types.hpp"
+
+namespace gs {
+
+constexpr int kF8Block = 128;
+constexpr int kF8Bias = 127;
+
+__host__ __device__ constexpr int64_t f8_blocks(int64_t dim) { return (dim + kF8Block - 1) / kF8Block; }
+
+// The scale's byte for a block whose largest finite magnitude has these bits: the least e with amax <= 448 * 2^e, within
+// [-126, 127]; 0 for a block of zeros. 448 is 1.75 * 2^8.
+__device__ __forceinline__ int f8_scale(uint32_t amax_bits) {
+    if (amax_bits == 0) return kF8Bias;
+    // adding a quarter less one unit carries into the exponent where the fraction is above 1.75
+    const int byte = static_cast<int>((amax_bits + 0x1fffffu) >> 23) - 8;
+    return byte < 1 ? 1 : byte;  // at most 254 + 1 - 8
+}
+// 2^(byte - 127) and its inverse; byte in [1, 253].
+__device__ __forceinline__ float f8_step(int byte) { return __builtin_bit_cast(float, static_cast<uint32_t>(byte) << 23); }
+__device__ __forceinline__ float f8_inverse(int byte) {
+    return __builtin_bit_cast(float, static_cast<uint32_t>(254 - byte) << 23);
+}
+
+// The bits of a finite magnitude, 0 for infinities and NaN: they leave the scale to the rest of the block.
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v) & 0x7fffffffu;
+    return b < 0x7f800000u ? b : 0u;
+}
+
+// Four values times `inverse` as e4m3, nearest and to even; infinities become NaN, as e4m3 has none.
+__device__ __forceinline__ uint32_t f8_pack(float a, float b, float c, float d, float inverse) {
+    const auto scaled = [&](float v) {
+        return finite_bits(v) != 0 || v == 0.0f ? v * inverse : __builtin_nanf("");
+    };
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(scaled(a), scaled(b), 0, false);
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(scaled(c), scaled(d), w, true));
+}
+
+}  // namespace gs

@@ -1,0 +1,440 @@
+// Products of rows sorted by expert with the experts' 8-bit weights on gfx950:
+// out[r, n] = sum_k x[r, k] weight[e(r)][n, k], both operands e4m3 with a power of two for each block of 128 along k.
+//
+// The matrix cores take the powers of two themselves (one byte for each row and block, the same for the four blocks of 32
+// they would allow), so a product is the scaled instruction alone, summed in float32. The rows of an expert come from the
+// plan's offsets on the device: nothing waits for the host. With `gather` a sorted row is read at its token, so the rows
+// are never copied into sorted order.
+#include "gs_f8.hpp"
+
+namespace gs {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kDies = 8;
+constexpr int kBand = 8;         // row tiles that are worked on together, so that they share the weights' tiles
+constexpr int kStep = 64;        // columns of k of a stage
+constexpr int kScaleBlocks = 32;  // blocks of k whose scales are held in LDS at once
+
+struct ProductArgs {
+    const uint8_t *x, *x_scales, *w, *w_scales;
+    const int32_t *offsets, *pairs;  // NULL: one expert has all rows; sorted row r is row r of x
+    int64_t rows, x_rows;            // sorted rows; rows of x
+    int choices, experts;
+    int cols, blocks;                // n; blocks of k
+    int relu, out_type;
+    void *out;
+};
+
+// A run of rows of one expert (number `experts`: the rows past the kept ones, which become zeros).
+struct Run {
+    int expert;
+    int64_t begin, end;
+};
+
+__device__ __forceinline__ int64_t within(int64_t v, int64_t low, int64_t high) {
+    return v < low ? low : v > high ? high : v;
+}
+
+__device__ __forceinline__ Run run_of(const ProductArgs &a, int expert) {
+    if (!a.offsets) return {expert, 0, expert == 0 ? a.rows : 0};
+    Run r = {expert, within(a.offsets[expert], 0, a.rows), a.rows};
+    if (expert < a.experts) r.end = within(a.offsets[expert + 1], r.begin, a.rows);
+    return r;
+}
+
+// Tiles of `height` rows that all runs take.
+__device__ __forceinline__ int64_t count_tiles(const ProductArgs &a, int height) {
+    const int lane = threadIdx.x % kWave;
+    int64_t n = 0;
+    for (int e = lane; e <= a.experts; e += kWave) {
+        const Run r = run_of(a, e);
+        n += (r.end - r.begin + height - 1) / height;
+    }
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d >>= 1) n += __shfl_xor(n, d, kWave);
+    return n;
+}
+
+// Row tile number `tile` of them, cut to its rows.
+__device__ __forceinline__ Run find_tile(const ProductArgs &a, int height, int64_t tile) {
+    const int lane = threadIdx.x % kWave;
+    int64_t before = 0;
+    for (int first = 0; first <= a.experts; first += kWave) {
+        const int e = first + lane;
+        Run r = {e, 0, 0};
+        if (e <= a.experts) r = run_of(a, e);
+        const int64_t n = (r.end - r.begin + height - 1) / height;
+        const int64_t upto = before + wave_inclusive_sum(n);
+        const uint64_t past = __ballot(tile < upto);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            const int64_t start = __shfl(r.begin + (tile - (upto - n)) * height, at, kWave);
+            const int64_t end = __shfl(r.end, at, kWave);
+            return {__builtin_amdgcn_readfirstlane(first + at), start, start + height < end ? start + height : end};
+        }
+        before = __shfl(upto, kWave - 1, kWave);
+    }
+    return {a.experts, 0, 0};
+}
+
+// Four results of a row from column n on.
+template <typename T>
+__device__ __forceinline__ void store_four(T *row, int n, int cols, const float *v) {
+    typedef T V __attribute__((ext_vector_type(4)));
+    typedef V VU __attribute__((aligned(sizeof(T))));
+    V o;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = static_cast<T>(v[k]);
+    if (n + 4 <= cols) {
+        *reinterpret_cast<VU *>(row + n) = o;
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (n + k < cols) row[n + k] = o[k];
+}
+__device__ __forceinline__ void store_four(const ProductArgs &a, int64_t row, int n, const float *v) {
+    if (a.out_type == GS_F32) store_four(static_cast<float *>(a.out) + row * a.cols, n, a.cols, v);
+    else if (a.out_type == GS_BF16) store_four(static_cast<__bf16 *>(a.out) + row * a.cols, n, a.cols, v);
+    else store_four(static_cast<_Float16 *>(a.out) + row * a.cols, n, a.cols, v);
+}
+
+// The row of x that row i of a run's tile is: rows past the run's end repeat its last and are not stored.
+__device__ __forceinline__ int64_t x_row(const ProductArgs &a, const Run &run, int i) {
+    const int64_t r = run.begin + i < run.end ? run.begin + i : run.end - 1;
+    return a.pairs ? within(a.pairs[r] / a.choices, 0, a.x_rows - 1) : r;
+}
+__device__ __forceinline__ int64_t w_row(const ProductArgs &a, const Run &run, int n) {
+    return static_cast<int64_t>(run.expert) * a.cols + (n < a.cols ? n : a.cols - 1);
+}
+
+// This workgroup's tile of those from number `turn` on; false: it has none, nor later. Each of the 8 dies takes
+// neighbouring tiles, whose panels its L2 then holds.
+struct Place {
+    int64_t row_tile, col_tile;
+};
+__device__ __forceinline__ bool place_of(int64_t turn, int64_t tiles, int64_t row_tiles, int64_t col_tiles, Place &at) {
+    const int64_t now = tiles - turn < gridDim.x ? tiles - turn : gridDim.x;
+    const int64_t share = (now + kDies - 1) / kDies;
+    const int64_t j = blockIdx.x / kDies, place = blockIdx.x % kDies * share + j;
+    if (j >= share || place >= now) return false;
+    const int64_t tile = turn + place, band = tile / (kBand * col_tiles), rest = tile - band * kBand * col_tiles;
+    const int64_t height = row_tiles - band * kBand < kBand ? row_tiles - band * kBand : kBand;
+    at.row_tile = band * kBand + rest % height;
+    at.col_tile = rest / height;
+    return true;
+}
+
+// A wave's results: lane l has row l % 32 of each 32 x 32, and of its columns four from l / 32 * 4 on of every eight.
+template <int FR, int FC>
+__device__ __forceinline__ void store_tile(const ProductArgs &a, const Run &run, const f32x16 (&acc)[FR][FC], int row0,
+                                           int col0) {
+    const int lane = threadIdx.x % kWave;
+#pragma unroll
+    for (int i = 0; i < FR; ++i) {
+        const int64_t row = run.begin + row0 + i * 32 + lane % 32;
+        if (row >= run.end) continue;
+#pragma unroll
+        for (int k = 0; k < FC; ++k)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    v[q] = acc[i][k][g * 4 + q];
+                    if (a.relu) v[q] = v[q] < 0.0f ? 0.0f : v[q];  // NaN stays
+                }
+                const int n = col0 + k * 32 + g * 8 + lane / 32 * 4;
+                if (n < a.cols) store_four(a, row, n, v);
+            }
+    }
+}
+
+// 16 bytes a lane from memory to LDS, without registers in between. lds: byte address, the same in the whole wave; the
+// instruction takes it from m0, which the compiler sets. Counts in vmcnt; only LDS is written.
+__device__ __forceinline__ void load_slots(const uint8_t *src, uint32_t lds) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(lds), "v"(src) : "memory");
+}
+template <int OUTSTANDING>
+__device__ __forceinline__ void wait_and_meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(OUTSTANDING) : "memory");
+}
+
+// Where the 16-byte chunk c (of four) of a row of a stage lies among the row's four places: so that both 8 and 16 rows
+// that are read at one chunk lie in different banks.
+__device__ __forceinline__ int turn_of(int row) { return ((row >> 1) ^ (row >> 3)) & 3; }
+
+// Tile of BM rows and BN columns by WR x WC waves. A stage is 64 columns of k of all the tile's rows and of its weights'
+// rows; four stages are in LDS, loaded without registers in between while the products of the one before run.
+template <int BM, int BN, int WR, int WC>
+__global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (BM <= 128 ? 2 : 1)) void product_kernel(ProductArgs a) {
+    constexpr int kStages = 4, kRows = BM + BN, kWaves = WR * WC, kThreads = kWaves * kWave;
+    constexpr int FR = BM / 32 / WR, FC = BN / 32 / WC;
+    static_assert(FR * WR * 32 == BM && FC * WC * 32 == BN, "whole results");
+    constexpr int kLoads = kRows / 16;  // of a stage, 16 rows each
+    constexpr int L = kLoads / kWaves;
+    static_assert(L * kWaves == kLoads, "the waves share the loads evenly");
+    constexpr int kStageBytes = kRows * kStep;
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kStages * kStageBytes];
+    __shared__ uint32_t s_scales[kScaleBlocks / 4][kRows];
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+    const int wr = wave / WC, wc = wave % WC;
+    const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) uint8_t *)s_ring));
+    const int64_t depth = static_cast<int64_t>(a.blocks) * kF8Block;
+    const int64_t col_tiles = (a.cols + BN - 1) / BN, row_tiles = count_tiles(a, BM), tiles = row_tiles * col_tiles;
+    // this lane's part of a fragment of 32 rows: bytes [32 half, 32 half + 32) of row lane % 32
+    const int first = lane % 32 * kStep + ((lane / 32 * 2) ^ turn_of(lane % 16)) * 16;
+
+    for (int64_t turn = 0; turn < tiles; turn += gridDim.x) {
+        Place at;
+        if (!place_of(turn, tiles, row_tiles, col_tiles, at)) return;
+        const Run run = find_tile(a, BM, at.row_tile);
+        const int col0 = static_cast<int>(at.col_tile) * BN;
+        f32x16 acc[FR][FC] = {};
+        if (run.expert < a.experts) {
+            // rows past the run's end repeat its last and are not stored
+            const uint8_t *src[L];
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int row = (wave * L + i) * 16 + lane / 4, chunk = lane % 4 ^ turn_of(row % 16);
+                src[i] = (row < BM ? a.x + x_row(a, run, row) * depth : a.w + w_row(a, run, col0 + row - BM) * depth) +
+                         chunk * 16;
+            }
+            for (int block0 = 0; block0 < a.blocks; block0 += kScaleBlocks) {
+                const int blocks = a.blocks - block0 < kScaleBlocks ? a.blocks - block0 : kScaleBlocks;
+                __syncthreads();  // the last products' scales are read
+                for (int i = threadIdx.x; i < kRows * (kScaleBlocks / 4); i += kThreads) {
+                    const int row = i % kRows, quad = i / kRows;
+                    if (quad * 4 >= blocks) break;
+                    const uint8_t *from = row < BM ? a.x_scales + x_row(a, run, row) * a.blocks
+                                                   : a.w_scales + w_row(a, run, col0 + row - BM) * a.blocks;
+                    uint32_t four = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (quad * 4 + k < blocks) four |= static_cast<uint32_t>(from[block0 + quad * 4 + k]) << (8 * k);
+                    s_scales[quad][row] = four;
+                }
+                const int stages = blocks * 2;
+                int issued = 0;
+                const auto issue = [&](int i) {
+                    load_slots(src[i], ring + (issued % kStages) * kStageBytes + (wave * L + i) * 1024);
+                    // past the end of k the last stage is loaded again, unused
+                    if (issued + 1 < stages) src[i] += kStep;
+                };
+                i32x8 frag[2][FR + FC];
+                const auto fetch = [&](int stage, int turn, int r) {
+                    const uint8_t *at = s_ring + (stage % kStages) * kStageBytes + first +
+                                        (r < FR ? wr * FR + r : BM / 32 + wc * FC + r - FR) * (32 * kStep);
+                    const i32x4 low = *reinterpret_cast<const i32x4 *>(at);
+                    const i32x4 high = *reinterpret_cast<const i32x4 *>(s_ring + ((at - s_ring) ^ 16));
+                    frag[turn][r] = __builtin_shufflevector(low, high, 0, 1, 2, 3, 4, 5, 6, 7);
+                };
+                int scale[FR + FC];
+                const auto multiply = [&](int turn, int next) {
+                    constexpr int M = FR * FC, R = FR + FC;
+#pragma unroll
+                    for (int m = 0; m < M; ++m) {
+#pragma unroll
+                        for (int r = m * R / M; r < (m + 1) * R / M; ++r) fetch(next, 1 - turn, r);
+#pragma unroll
+                        for (int i = m * L / M; i < (m + 1) * L / M; ++i) issue(i);
+                        const int i = m / FC, k = m % FC;
+                        acc[i][k] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            frag[turn][FR + k], frag[turn][i], acc[i][k], 0, 0, 0, scale[FR + k], 0, scale[i]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    ++issued;
+                };
+                for (; issued < kStages - 1; ++issued)
+#pragma unroll
+                    for (int i = 0; i < L; ++i) issue(i);
+                wait_and_meet<(kStages - 2) * L>();
+#pragma unroll
+                for (int r = 0; r < FR + FC; ++r) fetch(0, 0, r);
+                for (int b = 0; b < blocks; ++b) {
+                    // At each meeting the next stage is there and all waves are done with the one before this, whose
+                    // place the loads then take.
+                    wait_and_meet<(kStages - 3) * L>();
+#pragma unroll
+                    for (int r = 0; r < FR + FC; ++r)
+                        scale[r] = b % 4 ? scale[r] >> 8
+                                         : static_cast<int>(s_scales[b / 4][(r < FR ? wr * FR + r : BM / 32 + wc * FC +
+                                                                             r - FR) * 32 + lane % 32]);
+                    multiply(0, 2 * b + 1);
+                    wait_and_meet<(kStages - 3) * L>();
+                    multiply(1, 2 * b + 2);
+                }
+                wait_and_meet<0>();
+#pragma unroll
+                for (int i = 0; i < L; ++i) src[i] += kStep;  // the step that the last stage did not take
+            }
+        }
+        store_tile<FR, FC>(a, run, acc, wr * FR * 32, col0 + wc * FC * 32);
+    }
+}
+
+// The same for float32 results. The 8-bit instructions align the products of 8 neighbours along k to the largest of them and
+// cut what lies 2^-13 below it: about 2^-16 of a result, next to nothing beside a 16-bit rounding (2^-9, 2^-12) but not
+// beside float32's. So here both operands become bfloat16 on their way to LDS, which loses nothing (e4m3 has 4 bits, the
+// scale none), and the bfloat16 instructions' products are summed in float32. Half the rate.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// 16 held values as bfloat16.
+__device__ __forceinline__ void widen16(u32x4 held, float step, bf16x8 (&out)[2]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const bf16x2 low = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(held[k], step, false);
+        const bf16x2 high = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(held[k], step, true);
+        out[k / 2][k % 2 * 4] = low[0];
+        out[k / 2][k % 2 * 4 + 1] = low[1];
+        out[k / 2][k % 2 * 4 + 2] = high[0];
+        out[k / 2][k % 2 * 4 + 3] = high[1];
+    }
+}
+
+constexpr int kWideTile = 128, kWideThreads = 256;
+
+// 16 bytes (8 columns of k) of a row of a stage.
+__device__ __forceinline__ int wide_at(int row, int chunk) { return row * (kStep * 2) + (chunk ^ (row >> 1 & 7)) * 16; }
+
+__global__ __launch_bounds__(kWideThreads, 2) void product_wide_kernel(ProductArgs a) {
+    constexpr int kStage = 2 * kWideTile * kStep * 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t s_stages[2 * kStage];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+    const int wr = wave / 2, wc = wave % 2;
+    const int64_t depth = static_cast<int64_t>(a.blocks) * kF8Block;
+    const int64_t col_tiles = (a.cols + kWideTile - 1) / kWideTile, row_tiles = count_tiles(a, kWideTile);
+    const int64_t tiles = row_tiles * col_tiles;
+    const int my_row = threadIdx.x / 2, my_half = threadIdx.x % 2;  // 32 columns of a row of x and of one of the weight
+    for (int64_t turn = 0; turn < tiles; turn += gridDim.x) {
+        Place at;
+        if (!place_of(turn, tiles, row_tiles, col_tiles, at)) return;
+        const Run run = find_tile(a, kWideTile, at.row_tile);
+        const int col0 = static_cast<int>(at.col_tile) * kWideTile;
+        f32x16 acc[2][2] = {};
+        if (run.expert < a.experts) {
+            const int64_t r = x_row(a, run, my_row), n = w_row(a, run, col0 + my_row);
+            const uint8_t *x = a.x + r * depth + my_half * 32, *w = a.w + n * depth + my_half * 32;
+            const uint8_t *xs = a.x_scales + r * a.blocks, *ws = a.w_scales + n * a.blocks;
+            u32x4 held[2][2];
+            float step[2];
+            const auto load = [&](int stage) {
+                const int64_t col = static_cast<int64_t>(stage) * kStep;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    held[0][k] = *reinterpret_cast<const u32x4 *>(x + col + k * 16);
+                    held[1][k] = *reinterpret_cast<const u32x4 *>(w + col + k * 16);
+                }
+                step[0] = f8_step(xs[stage / 2]);
+                step[1] = f8_step(ws[stage / 2]);
+            };
+            const int stages = a.blocks * 2;
+            __syncthreads();  // the last tile's operands are read
+            load(0);
+            for (int stage = 0; stage < stages; ++stage) {
+                uint8_t *planes = s_stages + stage % 2 * kStage;
+#pragma unroll
+                for (int op = 0; op < 2; ++op)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        bf16x8 v[2];
+                        widen16(held[op][k], step[op], v);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            *reinterpret_cast<bf16x8 *>(planes + op * (kStage / 2) +
+                                                        wide_at(my_row, my_half * 4 + k * 2 + h)) = v[h];
+                    }
+                __syncthreads();
+                if (stage + 1 < stages) load(stage + 1);
+#pragma unroll
+                for (int deep = 0; deep < kStep / 16; ++deep) {
+                    bf16x8 frag[2][2];
+#pragma unroll
+                    for (int op = 0; op < 2; ++op)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            frag[op][i] = *reinterpret_cast<const bf16x8 *>(
+                                planes + op * (kStage / 2) +
+                                wide_at((op ? wc : wr) * 64 + i * 32 + lane % 32, deep * 2 + lane / 32));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            acc[i][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag[1][k], frag[0][i], acc[i][k], 0,
+                                                                                0, 0);
+                }
+            }
+        }
+        store_tile<2, 2>(a, run, acc, wr * 64, col0 + wc * 64);
+    }
+}
+
+constexpr int64_t kLimit = int64_t(1) << 31;
+constexpr int kMaxExperts = 4096;
+constexpr int kUnits = 256;
+
+}  // namespace
+}  // namespace gs
+
+using namespace gs;
+
+extern "C" gs_status gs_expert_product(const void *x, const void *x_scales, const void *weight,
+                                          const void *weight_scales, const int32_t *offsets, const int32_t *pairs,
+                                          int64_t rows, int64_t x_rows, int64_t choices, int experts, int64_t dim,
+                                          int64_t cols, int relu, int dtype, void *out, void *stream_handle) {
+    const char *name = "gs_expert_product";
+    if (rows < 0 || rows >= kLimit || x_rows < 0 || x_rows >= kLimit)
+        return fail(GS_ERR_INVALID_ARG, "%s: need 0 <= rows, x_rows < 2^31", name);
+    if (experts < 1 || experts > kMaxExperts)
+        return fail(GS_ERR_INVALID_ARG, "%s: experts = %d outside [1, %d]", name, experts, kMaxExperts);
+    if (!offsets && experts != 1) return fail(GS_ERR_INVALID_ARG, "%s: offsets may be NULL for one expert only", name);
+    if (dim < 1 || dim >= kLimit || cols < 1 || cols >= kLimit)
+        return fail(GS_ERR_INVALID_ARG, "%s: need 1 <= dim, cols < 2^31", name);
+    if (!known_dtype(dtype)) return fail(GS_ERR_INVALID_ARG, "%s: dtype = %d is no gs_dtype", name, dtype);
+    if (choices < 1 || choices >= kLimit) return fail(GS_ERR_INVALID_ARG, "%s: need 1 <= choices < 2^31", name);
+    if (pairs ? x_rows * choices != rows : x_rows != rows)
+        return fail(GS_ERR_INVALID_ARG, "%s: x_rows = %lld do not go with rows = %lld", name,
+                    static_cast<long long>(x_rows), static_cast<long long>(rows));
+    if (rows == 0) return ok();
+    if (!x || !x_scales || !weight || !weight_scales || !out)
+        return fail(GS_ERR_INVALID_ARG, "%s: a required pointer is NULL", name);
+    if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(weight)) % 16)
+        return fail(GS_ERR_INVALID_ARG, "%s: values must start at a multiple of 16 bytes", name);
+    const size_t blocks = static_cast<size_t>(f8_blocks(dim));
+    const size_t wide = static_cast<size_t>(experts) * static_cast<size_t>(cols) * blocks;
+    const gs_status over = check_apart(
+        name, {{"out", out, static_cast<size_t>(rows) * cols * dtype_size(dtype)}},
+        {{"x", x, x_rows * blocks * kF8Block}, {"x_scales", x_scales, x_rows * blocks},
+         {"weight", weight, wide * kF8Block}, {"weight_scales", weight_scales, wide},
+         {"offsets", offsets, (experts + size_t(1)) * 4}, {"pairs", pairs, static_cast<size_t>(rows) * 4}});
+    if (over != GS_OK) return over;
+    hipStream_t stream = static_cast<hipStream_t>(stream_handle);
+    ProductArgs a = {static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(x_scales),
+                     static_cast<const uint8_t *>(weight), static_cast<const uint8_t *>(weight_scales), offsets, pairs,
+                     rows, x_rows, static_cast<int>(choices), experts, static_cast<int>(cols),
+                     static_cast<int>(blocks), relu ? 1 : 0, dtype, out};
+    // at most these tiles, whatever the offsets
+    const auto most = [&](int bm, int bn) { return (rows / bm + experts + 1) * ((cols + bn - 1) / bn); };
+    const auto grid = [&](int64_t tiles, int per_unit) {
+        const int64_t full = static_cast<int64_t>(kUnits) * per_unit, whole = (tiles + kDies - 1) / kDies * kDies;
+        return dim3(static_cast<unsigned>(whole < full ? whole : full));
+    };
+    if (dtype == GS_F32) {
+        hipLaunchKernelGGL(product_wide_kernel, grid(most(kWideTile, kWideTile), 2), dim3(kWideThreads), 0, stream, a);
+        GS_LAUNCH_TRY("product_wide_kernel");
+    } else if (rows / experts >= 256 && rows / 256 * ((cols + 255) / 256) >= kUnits) {
+        hipLaunchKernelGGL((product_kernel<256, 256, 2, 4>), grid(most(256, 256), 1), dim3(512), 0, stream, a);
+        GS_LAUNCH_TRY("product_kernel");
+    } else {
+        hipLaunchKernelGGL((product_kernel<128, 128, 2, 2>), grid(most(128, 128), 2), dim3(256), 0, stream, a);
+        GS_LAUNCH_TRY("product_kernel");
+    }
+    return ok();
+}
