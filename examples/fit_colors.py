@@ -6,7 +6,8 @@ and that its gradients are right, not what can be learned from less.
 Each step: features -> expert layer -> colour head -> gs_rasterize_fwd; the image's squared error against the scene's
 own rendering goes back through gs_rasterize_bwd, the head and the layer, and the weights take orthogonalised updates.
 
-    python examples/fit_colors.py [--steps 60] [--scene tiny|200k] [--dtype bf16|f32]
+    python examples/fit_colors.py [--steps 60] [--scene tiny|200k] [--dtype bf16|f32] [--products library|f8]
+                                  [--balance 0.01]
 """
 import argparse
 import os
@@ -28,13 +29,15 @@ def features(ds, dim, seed=0):
                      6.3 * torch.rand(dim, generator=g, device="cuda"))
 
 
-def fit(scene, steps, dim=128, hidden=256, experts=8, choices=2, dtype=torch.bfloat16, rate=1e-3, tell=None):
+def fit(scene, steps, dim=128, hidden=256, experts=8, choices=2, dtype=torch.bfloat16, rate=1e-3, tell=None,
+        products="library", balance=0.0):
     """The loss of every step."""
     ds = frame.to_device(scene)
     want = frame.render_frame(ds)
     target, isect, offsets = want.render.render_colors, want.isect, want.isect_offsets
     x = features(ds, dim).to(dtype)
-    layer, head = ExpertLayer(dim, hidden, experts, choices, dtype=dtype), ColorHead(dim)
+    layer = ExpertLayer(dim, hidden, experts, choices, dtype=dtype, products=products, balance=balance)
+    head = ColorHead(dim)
     losses = []
     for step in range(steps):
         y, saved = layer.forward(x)
@@ -64,9 +67,12 @@ def main():
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--scene", choices=("tiny", "200k"), default="200k")
     ap.add_argument("--dtype", choices=("bf16", "f32"), default="bf16")
+    ap.add_argument("--products", choices=("library", "f8"), default="library")
+    ap.add_argument("--balance", type=float, default=0.0, help="weight of the experts' balance loss")
     a = ap.parse_args()
     scene = synth.tiny() if a.scene == "tiny" else synth.config2()
-    losses = fit(scene, a.steps, dtype=torch.bfloat16 if a.dtype == "bf16" else torch.float32, tell=print)
+    losses = fit(scene, a.steps, dtype=torch.bfloat16 if a.dtype == "bf16" else torch.float32, tell=print,
+                 products=a.products, balance=a.balance)
     print(f"loss {losses[0]:.6f} -> {losses[-1]:.6f}")
 
 
