@@ -40,4 +40,21 @@ __device__ __forceinline__ uint32_t f8_pack(float a, float b, float c, float d, 
     return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(scaled(c), scaled(d), w, true));
 }
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// 8 held values as bfloat16, which loses nothing: e4m3 has 4 bits and the scale none.
+__device__ __forceinline__ bf16x8 widen8(uint32_t first, uint32_t second, float step) {
+    bf16x8 out;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t w = k < 2 ? first : second;
+        const bf16x2 two = k % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, step, true)
+                                 : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, step, false);
+        out[2 * k] = two[0];
+        out[2 * k + 1] = two[1];
+    }
+    return out;
+}
+
 }  // namespace gs

@@ -283,22 +283,6 @@ __global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (BM <= 128 ? 2 : 1)) vo
 // cut what lies 2^-13 below it: about 2^-16 of a result, next to nothing beside a 16-bit rounding (2^-9, 2^-12) but not
 // beside float32's. So here both operands become bfloat16 on their way to LDS, which loses nothing (e4m3 has 4 bits, the
 // scale none), and the bfloat16 instructions' products are summed in float32. Half the rate.
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-// 16 held values as bfloat16.
-__device__ __forceinline__ void widen16(u32x4 held, float step, bf16x8 (&out)[2]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const bf16x2 low = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(held[k], step, false);
-        const bf16x2 high = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(held[k], step, true);
-        out[k / 2][k % 2 * 4] = low[0];
-        out[k / 2][k % 2 * 4 + 1] = low[1];
-        out[k / 2][k % 2 * 4 + 2] = high[0];
-        out[k / 2][k % 2 * 4 + 3] = high[1];
-    }
-}
-
 constexpr int kWideTile = 128, kWideThreads = 256;
 
 // 16 bytes (8 columns of k) of a row of a stage.
@@ -344,12 +328,11 @@ __global__ __launch_bounds__(kWideThreads, 2) void product_wide_kernel(ProductAr
                 for (int op = 0; op < 2; ++op)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        bf16x8 v[2];
-                        widen16(held[op][k], step[op], v);
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             *reinterpret_cast<bf16x8 *>(planes + op * (kStage / 2) +
-                                                        wide_at(my_row, my_half * 4 + k * 2 + h)) = v[h];
+                                                        wide_at(my_row, my_half * 4 + k * 2 + h)) =
+                                widen8(held[op][k][2 * h], held[op][k][2 * h + 1], step[op]);
                     }
                 __syncthreads();
                 if (stage + 1 < stages) load(stage + 1);

@@ -11,17 +11,16 @@
 namespace gs {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kTile = 128;      // columns of x and of grad
+constexpr int kBand = 8;        // tiles of x's columns that are worked on together
+constexpr int kSmall = 128, kLarge = 256;  // columns of a tile, of x and of grad
 constexpr int kDeep = 32;       // rows of a step
+constexpr int kSegment = 1024;  // rows whose places in x are looked up at once
 constexpr int kThreads = 256;
 constexpr int kDies = 8;
 constexpr int kUnits = 256;
-constexpr int kPlaneBytes = kDeep * kTile * 2;
 
 struct GradArgs {
     const uint8_t *x, *x_scales;
@@ -73,9 +72,12 @@ __device__ __forceinline__ Run find_part(const GradArgs &a, int64_t item) {
     return {a.experts, 0, 0};
 }
 
-// Bytes from a plane's start to 16 columns (unit of 8) of a row: so placed that the four rows which a transposing load
-// takes at once lie in different banks.
-__device__ __forceinline__ int unit_at(int row, int unit) { return row * (kTile * 2) + (unit ^ (row % 4 * 2)) * 32; }
+// Bytes from a plane's start to 8 columns (a chunk) of a row of TILE: so placed that the four rows which a transposing load
+// takes at once lie in different banks, and the even or odd chunks of two neighbouring rows too, which are written at once.
+template <int TILE>
+__device__ __forceinline__ int chunk_at(int row, int chunk) {
+    return row * (TILE * 2) + (chunk ^ (row % 4 * 4) ^ (row % 2)) * 16;
+}
 
 __device__ __forceinline__ float leading8(float v) {
     return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xffff0000u);
@@ -88,139 +90,231 @@ constexpr int kPlanes = sizeof(T) == 4 ? 3 : 2;
 template <>
 constexpr int kPlanes<__bf16> = 1;
 
-template <int P>
-__device__ __forceinline__ void split16(const float *v, bf16x8 (&out)[P][2]) {
+// 8 values as P planes.
+template <int P, typename V>
+__device__ __forceinline__ void split8(const V *packs, bf16x8 (&out)[P]) {
+    constexpr int N = sizeof(V) / sizeof((*packs)[0]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (P == 1) {
+            out[0][j] = packs[j / N][j % N];
+        } else {
+            float rest = static_cast<float>(packs[j / N][j % N]);
+            const bool number = finite_bits(rest) != 0 || rest == 0.0f;
+            out[0][j] = static_cast<__bf16>(number ? leading8(rest) : rest);
+            rest = number ? rest - leading8(rest) : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float rest = v[h * 8 + j];
-            if constexpr (P > 1) {
-                const bool number = finite_bits(rest) != 0 || rest == 0.0f;
-                out[0][h][j] = static_cast<__bf16>(number ? leading8(rest) : rest);
-                rest = number ? rest - leading8(rest) : 0.0f;
-#pragma unroll
-                for (int p = 1; p < P; ++p) {
-                    out[p][h][j] = static_cast<__bf16>(leading8(rest));
-                    rest -= leading8(rest);
-                }
-            } else {
-                out[0][h][j] = static_cast<__bf16>(rest);
+            for (int p = 1; p < P; ++p) {
+                out[p][j] = static_cast<__bf16>(leading8(rest));
+                rest -= leading8(rest);
             }
         }
+    }
 }
 
-// One tile of one part: 4 waves of 64 x 64 results.
-template <typename T>
-__global__ __launch_bounds__(kThreads, 2) void weight_grad_kernel(GradArgs a, int64_t items) {
-    constexpr int P = kPlanes<T>, kBytes = (1 + P) * kPlaneBytes;
-    __shared__ __attribute__((aligned(1024))) uint8_t s_planes[2 * kBytes];
+// One tile of one part: 4 waves of 32 F x 32 F results. A step's rows go from memory to registers two steps ahead, from
+// there as bfloat16 to LDS one step ahead. CUT: rows of
+// grad end inside a pack. NARROW: they are shorter than one.
+template <typename T, int F, bool CUT, bool NARROW>
+__global__ __launch_bounds__(kThreads, F == 2 ? 2 : 1) void weight_grad_kernel(GradArgs a, int64_t items) {
+    constexpr int P = kPlanes<T>, kTile = 64 * F, kRuns = F / 2;  // columns of a tile; a thread's runs of 16 of a row
+    constexpr int kPlaneBytes = kDeep * kTile * 2, kBytes = (1 + P) * kPlaneBytes;
+    // steps whose rows are in LDS beside the current one's: two where there is room, so that no step begins with a wait
+    constexpr int kAhead = 3 * kBytes + kSegment * 8 <= 159 * 1024 / (F == 2 ? 2 : 1) ? 2 : 1;
+    __shared__ __attribute__((aligned(1024))) uint8_t s_planes[(kAhead + 1) * kBytes];
+    __shared__ int64_t s_rows[kSegment];  // first blocks of the rows of x
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
     const int wr = wave / 2, wc = wave % 2;
-    const int64_t down = f8_blocks(a.dim), across = (a.cols + kTile - 1) / kTile;
-    const int64_t tiles = items * down * across;
-    const int my_row = threadIdx.x / 8, my_unit = threadIdx.x % 8;
-    const int my_place = unit_at(my_row, my_unit);
+    const int64_t down = (a.dim + kTile - 1) / kTile, across = (a.cols + kTile - 1) / kTile, each = down * across;
+    const int64_t tiles = items * each;
+    const int my_row = threadIdx.x / 8, my_col = threadIdx.x % 8 * 16;  // and 128 on
+    const int my_place = chunk_at<kTile>(my_row, threadIdx.x % 8 * 2);
     // a transposing load: lane p of 16 reads 4 of the 16 columns of row p / 4
-    const int p = lane % 16, from = unit_at(lane / 32 * 8 + p / 4, lane / 16 % 2) + p % 4 * 8;
+    const int p = lane % 16, from = chunk_at<kTile>(lane / 32 * 8 + p / 4, lane / 16 % 2 * 2 + p / 2 % 2) + p % 2 * 8;
 
     for (int64_t turn = 0; turn < tiles; turn += gridDim.x) {
-        const int64_t now = tiles - turn < gridDim.x ? tiles - turn : gridDim.x;
-        const int64_t share = (now + kDies - 1) / kDies;
-        const int64_t j = blockIdx.x / kDies, place = blockIdx.x % kDies * share + j;
+        // of each 256 tiles, which run at about the same time, every die takes neighbouring ones: its L2 holds their rows
+        const int64_t group = turn + blockIdx.x / kUnits * kUnits;
+        const int64_t now = tiles - group < kUnits ? tiles - group : kUnits, share = (now + kDies - 1) / kDies;
+        const int64_t j = blockIdx.x % kUnits / kDies, place = blockIdx.x % kDies * share + j;
         if (j >= share || place >= now) return;
-        const int64_t tile = turn + place, item = tile / (down * across), rest = tile - item * down * across;
-        const int d0 = static_cast<int>(rest / across) * kTile, n0 = static_cast<int>(rest % across) * kTile;
+        const int64_t tile = group + place, item = tile / each, of = tile - item * each;
+        const int64_t band = of / (kBand * across), rest = of - band * kBand * across;
+        const int64_t height = down - band * kBand < kBand ? down - band * kBand : kBand;
+        const int d0 = static_cast<int>(band * kBand + rest % height) * kTile;
+        const int n0 = static_cast<int>(rest / height) * kTile;
         Run run;
         if (a.parted) run = find_part(a, item);
         else run = run_of(a, static_cast<int>(item));
         if (run.expert >= a.experts) return;  // fewer parts than there could be
-        f32x16 acc[2][2] = {};
+        f32x16 acc[F][F] = {};
 
-        u32x4 x_now = {};
-        float step = 0.0f, g_now[16];
-        const auto load = [&](int64_t first) {
-            const int64_t r = first + my_row;
-            x_now = u32x4{0, 0, 0, 0};
-            step = 1.0f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) g_now[k] = 0.0f;
-            if (r < run.end) {
-                int64_t s = r;
-                if (a.pairs) s = within(a.pairs[r] / a.choices, 0, a.x_rows - 1);
-                x_now = *reinterpret_cast<const u32x4 *>(a.x + (s * a.blocks + d0 / kTile) * kF8Block + my_unit * 16);
-                step = f8_step(a.x_scales[s * a.blocks + d0 / kTile]);
-                load_floats<16>(static_cast<const T *>(a.grad) + r * a.cols, n0 + my_unit * 16, a.cols, g_now);
+        // Rows and columns past the ends are read at the last one: no load waits for a branch. The rows become zeros on
+        // their way to LDS, the columns belong to results that are not stored.
+        constexpr int kPacks = 16 / Pack<T>::kN;
+        u32x4 x[2][kRuns];
+        int step[2][kRuns];
+        typename Pack<T>::V g[2][kRuns][kPacks];
+        bf16x8 d[2][F], n[2][F];
+        for (int64_t start = run.begin; start < run.end; start += kSegment) {
+            const int64_t end = start + kSegment < run.end ? start + kSegment : run.end;
+            const int count = static_cast<int>(end - start);
+            __syncthreads();  // the last rows' operands and places are read
+            for (int i = threadIdx.x; i < count; i += kThreads) {
+                const int64_t r = start + i;
+                s_rows[i] = (a.pairs ? within(a.pairs[r] / a.choices, 0, a.x_rows - 1) : r) * a.blocks;
             }
-        };
-        const auto keep = [&](uint8_t *planes) {
-            bf16x8 v[2];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const int w = static_cast<int>(x_now[k / 4]);
-                const float f = k % 4 == 0   ? __builtin_amdgcn_cvt_f32_fp8(w, 0)
-                                : k % 4 == 1 ? __builtin_amdgcn_cvt_f32_fp8(w, 1)
-                                : k % 4 == 2 ? __builtin_amdgcn_cvt_f32_fp8(w, 2)
-                                             : __builtin_amdgcn_cvt_f32_fp8(w, 3);
-                v[k / 8][k % 8] = static_cast<__bf16>(f * step);
-            }
-            *reinterpret_cast<bf16x8 *>(planes + my_place) = v[0];
-            *reinterpret_cast<bf16x8 *>(planes + my_place + 16) = v[1];
-            bf16x8 g[P][2];
-            split16<P>(g_now, g);
-#pragma unroll
-            for (int q = 0; q < P; ++q) {
-                *reinterpret_cast<bf16x8 *>(planes + (1 + q) * kPlaneBytes + my_place) = g[q][0];
-                *reinterpret_cast<bf16x8 *>(planes + (1 + q) * kPlaneBytes + my_place + 16) = g[q][1];
-            }
-        };
-        const auto operand = [&](const uint8_t *plane, int unit, int deep) {
-            typedef __attribute__((address_space(3))) s16x4 *LdsPtr;
-            // the unit's number is even: its place is that of unit 0 or 1, moved
-            const uint8_t *at = plane + deep * (kTile * 2) + (from ^ (unit * 32));
-            const s16x4 low = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at));
-            const s16x4 high = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at + 4 * (kTile * 2)));
-            typedef short s16x8 __attribute__((ext_vector_type(8)));
-            const s16x8 both = __builtin_shufflevector(low, high, 0, 1, 2, 3, 4, 5, 6, 7);
-            return __builtin_bit_cast(bf16x8, both);
-        };
-
-        __syncthreads();
-        load(run.begin);
-        int at = 0;
-        for (int64_t first = run.begin; first < run.end; first += kDeep, at ^= 1) {
-            uint8_t *planes = s_planes + at * kBytes;
-            keep(planes);
             __syncthreads();
-            load(first + kDeep);  // zeros past the end
+            // where the step that is loaded next has this thread's row, and the last row there is
+            const T *row = static_cast<const T *>(a.grad) + (start + (my_row < count ? my_row : count - 1)) * a.cols;
+            const T *const last_row = static_cast<const T *>(a.grad) + (end - 1) * a.cols;
+            const int64_t row_step = static_cast<int64_t>(kDeep) * a.cols;
+            int64_t source = s_rows[my_row < count ? my_row : count - 1];
+            const auto load = [&](int at, int j) {
+                const int64_t b = source + (d0 / kF8Block + j < a.blocks ? d0 / kF8Block + j : a.blocks - 1);
+                step[at][j] = a.x_scales[b];
+                x[at][j] = *reinterpret_cast<const u32x4 *>(a.x + b * kF8Block + my_col);
 #pragma unroll
-            for (int deep = 0; deep < kDeep; deep += 16) {
-                bf16x8 d[2], n[2];
+                for (int k = 0; k < kPacks; ++k) {
+                    const int col = n0 + j * 128 + my_col + k * Pack<T>::kN;
+                    if constexpr (NARROW) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) d[i] = operand(planes, wr * 4 + i * 2, deep);
+                        for (int q = 0; q < Pack<T>::kN; ++q)
+                            g[at][j][k][q] = row[col + q < a.cols ? col + q : a.cols - 1];
+                    } else {
+                        g[at][j][k] = read_pack(row, col, a.cols);
+                    }
+                }
+            };
+            const auto seek = [&](int next) {  // the step from row `next` on is loaded next
+                row = row + row_step < last_row ? row + row_step : last_row;
+                const int i = next + my_row;
+                source = s_rows[i < count ? i : count - 1];
+            };
+            const auto load_all = [&](int next, int at) {
 #pragma unroll
-                for (int q = P - 1; q >= 0; --q) {
+                for (int j = 0; j < kRuns; ++j) load(at, j);
+                seek(next);
+            };
+            // Piece 0, 2, ...: 8 columns of x; 1, 3, ...: of grad. A row past the end is the last one again, with zeros for
+            // its grad: its x then adds zeros, or the NaN that it added itself.
+            constexpr int kPieces = 2 * F;
+            const auto keep = [&](int first, int at, uint8_t *planes, int piece) {
+                const int j = piece / 4, h = piece / 2 % 2;
+                // the first chunk's number is even: the second one's place differs in one bit
+                uint8_t *to = planes + (my_place ^ (h * 16)) + j * 256;
+                if (piece % 2 == 0) {
+                    *reinterpret_cast<bf16x8 *>(to) =
+                        widen8(x[at][j][2 * h], x[at][j][2 * h + 1], f8_step(step[at][j]));
+                    return;
+                }
+                const uint32_t there = first + my_row < count ? 0xffffffffu : 0u;
+                typename Pack<T>::V packs[8 / Pack<T>::kN];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) n[i] = operand(planes + (1 + q) * kPlaneBytes, wc * 4 + i * 2, deep);
+                for (int q = 0; q < 8 / Pack<T>::kN; ++q) {
+                    const int k = h * 8 / Pack<T>::kN + q;
+                    packs[q] = g[at][j][k];
+                    if constexpr (CUT) packs[q] = end_pack<T>(packs[q], n0 + j * 128 + my_col + k * Pack<T>::kN, a.cols);
+                }
+                bf16x8 s[P];
+                split8<P>(packs, s);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                for (int q = 0; q < P; ++q)
+                    *reinterpret_cast<u32x4 *>(to + (1 + q) * kPlaneBytes) = __builtin_bit_cast(u32x4, s[q]) & there;
+            };
+            const auto keep_all = [&](int first, int at, uint8_t *planes) {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            acc[i][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d[i], n[k], acc[i][k], 0, 0, 0);
+                for (int piece = 0; piece < kPieces; ++piece) keep(first, at, planes, piece);
+            };
+            const auto operand = [&](const uint8_t *plane, int unit, int deep) {
+                typedef __attribute__((address_space(3))) s16x4 *LdsPtr;
+                typedef short s16x8 __attribute__((ext_vector_type(8)));
+                // of 16 columns each; the unit's number is even: its place is that of the first two, moved
+                const uint8_t *at = plane + deep * (kTile * 2) + (from ^ (unit * 32));
+                const s16x4 low = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at));
+                const s16x4 high = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(at + 4 * (kTile * 2)));
+                const s16x8 both = __builtin_shufflevector(low, high, 0, 1, 2, 3, 4, 5, 6, 7);
+                return __builtin_bit_cast(bf16x8, both);
+            };
+            // A step is 2 P phases: 16 rows and one plane of grad each, the smallest plane first. Operand r of a phase: the
+            // plane's, and where the rows are new x's.
+            constexpr int kPhases = 2 * P;
+            const auto operands = [](int phase) { return phase % P == 0 ? 2 * F : F; };
+            const auto fetch = [&](const uint8_t *planes, int phase, int r) {
+                const int deep = phase / P * 16, q = P - 1 - phase % P;
+                if (r < F) n[phase % 2][r] = operand(planes + (1 + q) * kPlaneBytes, wc * 2 * F + r * 2, deep);
+                else d[phase / P % 2][r - F] = operand(planes, wr * 2 * F + (r - F) * 2, deep);
+            };
+            const auto fetch_all = [&](const uint8_t *planes, int phase) {
+#pragma unroll
+                for (int r = 0; r < operands(phase); ++r) fetch(planes, phase, r);
+            };
+            // One step, whose first operands are there. Between its products, in this order: the reads of the next phase's
+            // operands, the loads of the rows kAhead + 1 steps on, and the rows kAhead steps on to LDS.
+            const auto work = [&](int first, int at, const uint8_t *now, const uint8_t *next, uint8_t *after) {
+                constexpr int M = F * F;
+                __syncthreads();
+                if constexpr (kAhead == 1) fetch_all(now, 0);
+#pragma unroll
+                for (int phase = 0; phase < kPhases; ++phase) {
+                    const bool last = phase + 1 == kPhases;
+                    const int reads = !last ? operands(phase + 1) : kAhead == 2 ? operands(0) : 0;
+#pragma unroll
+                    for (int m = 0; m < M; ++m) {
+                        // the reads end early enough to be done at the next phase
+#pragma unroll
+                        for (int r = m * reads * 4 / (M * 3); r < (m + 1) * reads * 4 / (M * 3) && r < reads; ++r)
+                            fetch(last ? next : now, last ? 0 : phase + 1, r);
+                        const int i = m / F, k = m % F;
+                        acc[i][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d[phase / P % 2][i], n[phase % 2][k],
+                                                                            acc[i][k], 0, 0, 0);
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (phase == 0 && m % (M / 4) == 0 && m / (M / 4) < kRuns) load(1 - at, m / (M / 4));
+                        if (phase == 0 && m == M * 3 / 4) seek(first + (kAhead + 2) * kDeep);
+                        if (last)
+#pragma unroll
+                            for (int piece = m * kPieces / M; piece < (m + 1) * kPieces / M; ++piece)
+                                keep(first + kAhead * kDeep, at, after, piece);
+                    }
+                }
+            };
+            load_all(kDeep, 0);
+            load_all(2 * kDeep, 1);
+            keep_all(0, 0, s_planes);
+            if constexpr (kAhead == 2) {
+                load_all(3 * kDeep, 0);
+                keep_all(kDeep, 1, s_planes + kBytes);
+                __syncthreads();
+                fetch_all(s_planes, 0);
+            }
+            // six steps a turn: registers two deep and LDS kAhead + 1 deep are then the same in every turn
+            for (int first = 0; first < count;) {
+#pragma unroll
+                for (int u = 0; u < 6; ++u) {
+                    constexpr int kPlaces = kAhead + 1;
+                    work(first, (u + kAhead) % 2, s_planes + u % kPlaces * kBytes,
+                         s_planes + (u + 1) % kPlaces * kBytes, s_planes + (u + kAhead) % kPlaces * kBytes);
+                    first += kDeep;
+                    if (first >= count) break;
                 }
             }
         }
         float *out = a.out + (a.parted ? item : run.expert) * static_cast<int64_t>(a.dim) * a.cols;
+        // one pointer that walks the lane's results, so that no address is kept from before
+        const int n1 = n0 + wc * F * 32 + lane % 32, d1 = d0 + wr * F * 32 + lane / 32 * 4;
+        float *to = out + static_cast<int64_t>(d1) * a.cols + n1;
+        const bool inside = d0 + kTile <= a.dim && n0 + kTile <= a.cols;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < F; ++i)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int n = n0 + wc * 64 + k * 32 + lane % 32;
+            for (int g = 0; g < 16; ++g) {
+                const int d = d1 + i * 32 + g / 4 * 8 + g % 4;
 #pragma unroll
-                for (int g = 0; g < 16; ++g) {
-                    const int d = d0 + wr * 64 + i * 32 + g / 4 * 8 + lane / 32 * 4 + g % 4;
-                    if (d < a.dim && n < a.cols) out[static_cast<int64_t>(d) * a.cols + n] = acc[i][k][g];
-                }
+                for (int k = 0; k < F; ++k)
+                    if (inside || (d < a.dim && n1 + k * 32 < a.cols))
+                        to[k * 32] = acc[i][k][g];
+                to += (g % 4 == 3 ? 5 : 1) * static_cast<int64_t>(a.cols);
+                asm volatile("" : "+v"(to));
             }
     }
 }
@@ -253,16 +347,22 @@ constexpr int kMaxExperts = 4096;
 // Rows of a part and the parts that there can be; one part an expert where its tiles alone fill the chip.
 struct Parts {
     int64_t chunk, items;
+    int tile;
     bool parted;
 };
+inline int64_t tiles_of(int64_t dim, int64_t cols, int tile) {
+    return ((dim + tile - 1) / tile) * ((cols + tile - 1) / tile);
+}
 Parts parts_for(int64_t rows, int experts, int64_t dim, int64_t cols) {
-    const int64_t tiles = f8_blocks(dim) * ((cols + kTile - 1) / kTile);
+    const int64_t all = rows > 0 ? rows : 1;
+    if (cols >= 8 && experts * tiles_of(dim, cols, kLarge) >= 2 * kUnits) return {all, experts, kLarge, false};
+    const int64_t tiles = tiles_of(dim, cols, kSmall);
     const int64_t want = 4 * kUnits / tiles;  // parts in all, for four tiles a compute unit
     int64_t chunk = want > 0 ? (rows + want - 1) / want : rows;
     chunk = (chunk + kDeep - 1) / kDeep * kDeep;
     chunk = chunk < 8 * kDeep ? 8 * kDeep : chunk;
-    if (experts * tiles >= 2 * kUnits || chunk >= rows) return {rows > 0 ? rows : 1, experts, false};
-    return {chunk, rows / chunk + experts, true};
+    if (experts * tiles >= 2 * kUnits || chunk >= rows) return {all, experts, kSmall, false};
+    return {chunk, rows / chunk + experts, kSmall, true};
 }
 
 }  // namespace
@@ -318,15 +418,24 @@ extern "C" gs_status gs_expert_weight_grad(const void *x, const void *x_scales, 
                   x_rows, static_cast<int>(choices), experts, static_cast<int>(dim), static_cast<int>(cols),
                   static_cast<int>(blocks), parts.chunk, parts.parted ? 1 : 0,
                   parts.parted ? static_cast<float *>(workspace) : out};
-    const int64_t tiles = parts.items * f8_blocks(dim) * ((cols + kTile - 1) / kTile);
+    const int64_t tiles = parts.items * tiles_of(dim, cols, parts.tile);
     const int64_t whole = (tiles + kDies - 1) / kDies * kDies, most = 1 << 20;
     const dim3 grid(static_cast<unsigned>(whole < most ? whole : most));
-    if (dtype == GS_F32)
-        hipLaunchKernelGGL((weight_grad_kernel<float>), grid, dim3(kThreads), 0, stream, a, parts.items);
-    else if (dtype == GS_BF16)
-        hipLaunchKernelGGL((weight_grad_kernel<__bf16>), grid, dim3(kThreads), 0, stream, a, parts.items);
-    else
-        hipLaunchKernelGGL((weight_grad_kernel<_Float16>), grid, dim3(kThreads), 0, stream, a, parts.items);
+#define GS_WEIGHT_GRAD_F(T, F, CUT, NARROW)                                                                           \
+    hipLaunchKernelGGL((weight_grad_kernel<T, F, CUT, NARROW>), grid, dim3(kThreads), 0, stream, a, parts.items)
+#define GS_WEIGHT_GRAD(T)                                                                  \
+    do {                                                                                   \
+        if (cols < Pack<T>::kN) GS_WEIGHT_GRAD_F(T, 2, false, true);                       \
+        else if (cols % Pack<T>::kN != 0 && parts.tile == kLarge) GS_WEIGHT_GRAD_F(T, 4, true, false); \
+        else if (cols % Pack<T>::kN != 0) GS_WEIGHT_GRAD_F(T, 2, true, false);             \
+        else if (parts.tile == kLarge) GS_WEIGHT_GRAD_F(T, 4, false, false);               \
+        else GS_WEIGHT_GRAD_F(T, 2, false, false);                                         \
+    } while (0)
+    if (dtype == GS_F32) GS_WEIGHT_GRAD(float);
+    else if (dtype == GS_BF16) GS_WEIGHT_GRAD(__bf16);
+    else GS_WEIGHT_GRAD(_Float16);
+#undef GS_WEIGHT_GRAD
+#undef GS_WEIGHT_GRAD_F
     GS_LAUNCH_TRY("weight_grad_kernel");
     if (parts.parted) {
         const int64_t groups = (dim * cols + kThreads - 1) / kThreads, joins = groups * experts;
