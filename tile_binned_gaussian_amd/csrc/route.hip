@@ -5,6 +5,8 @@
 // once: the largest gives the softmax, K rounds of the largest that is left give the choices. Each lane counts its own
 // experts' choices and sums their probabilities over all tokens of its workgroup in registers; the workgroups' sums go to
 // a workspace and a second kernel adds them in a fixed order, in float64. A single workgroup (few tokens) finishes alone.
+#include <type_traits>
+
 #include "gs_types.hpp"
 
 namespace gs {
@@ -15,9 +17,8 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxExperts = 4096;
 constexpr int kBlocks = 1024;      // workgroups of the first kernel, at most
 constexpr int64_t kPartials = 1 << 20;  // partial sums of each kind, at most
-constexpr int kJoinCols = 64;      // experts of a workgroup of the second kernel
+constexpr int kJoinCols = 64;      // experts of a workgroup of the second kernel, at most
 constexpr int kJoinThreads = 1024;
-constexpr int kJoinSlices = kJoinThreads / kJoinCols;
 
 // Workgroups for this many tokens with `rows` of them a turn: enough to fill the chip, few enough that their sums are
 // soon added.
@@ -37,17 +38,60 @@ __device__ __forceinline__ uint32_t order_of(float v) {
 }
 constexpr uint32_t kOrderOfNone = 0x007fffffu;  // minus infinity's: an expert that may not be chosen
 
+// The value of the lane that differs in one bit of its number, or in a whole run of them: once the lanes of each half
+// agree, any of the other half will do, and within 16 lanes the mirrored one costs no LDS instruction.
+template <int D>
+__device__ __forceinline__ uint32_t across(uint32_t v) {
+    if constexpr (D == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);
+    else if constexpr (D == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);
+    else if constexpr (D == 4) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);
+    else if constexpr (D == 8) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);
+    else return __shfl_xor(v, D, kWave);
+}
+// Folds f over the group's lanes, from neighbours on: every lane gets the same.
+template <int G, int D = 1, typename F>
+__device__ __forceinline__ void fold(const F &f) {
+    if constexpr (D < G) {
+        f(std::integral_constant<int, D>());
+        fold<G, D * 2>(f);
+    }
+}
+template <int G>
+__device__ __forceinline__ float sum_of(float v) {
+    fold<G>([&](auto d) {
+        v += __builtin_bit_cast(float, across<decltype(d)::value>(__builtin_bit_cast(uint32_t, v)));
+    });
+    return v;
+}
+
 // The largest of the group's values, and its expert: the lowest among equal ones.
 template <int G>
-__device__ __forceinline__ void group_best(uint32_t &key, int &expert) {
+__device__ __forceinline__ void group_best(uint32_t &key, uint32_t &expert) {
+    fold<G>([&](auto d) {
+        const uint32_t k = across<decltype(d)::value>(key), e = across<decltype(d)::value>(expert);
+        const bool take = k > key || (k == key && e < expert);
+        key = take ? k : key;
+        expert = take ? e : expert;
+    });
+}
+
+// Lane l of the group has experts l * V to l * V + V - 1. WHOLE: there are G * V of them.
+template <int G, int V, bool WHOLE, typename T>
+__device__ __forceinline__ void load_row(const T *row, int lane, int experts, float (&x)[V]) {
+    if constexpr (WHOLE) {
+        typedef T P __attribute__((ext_vector_type(V)));
+        typedef P U __attribute__((aligned(sizeof(T))));
+        const P p = *reinterpret_cast<const U *>(row + lane * V);
 #pragma unroll
-    for (int d = G / 2; d > 0; d >>= 1) {
-        const uint32_t k = __shfl_xor(key, d, kWave);
-        const int e = __shfl_xor(expert, d, kWave);
-        if (k > key || (k == key && e < expert)) {
-            key = k;
-            expert = e;
+        for (int v = 0; v < V; ++v) x[v] = static_cast<float>(p[v]);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = lane * V + v;
+            x[v] = static_cast<float>(row[e < experts ? e : experts - 1]);
         }
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = lane * V + v < experts ? x[v] : -__builtin_inff();
     }
 }
 
@@ -70,11 +114,12 @@ __device__ __forceinline__ float balance_loss(int experts, double dot, int64_t p
     return static_cast<float>(experts * dot / static_cast<double>(pairs > 0 ? pairs : 1));
 }
 
-template <typename T, int G, int V>
+template <typename T, int G, int V, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
     constexpr int kRows = kThreads / G;
-    __shared__ float s_shares[kThreads];
-    __shared__ int32_t s_counts[kThreads];
+    constexpr int kHold = G == 1 ? 4 : 1;  // choices that a lane holds until their sum is known
+    __shared__ float s_shares[kWaves][G * V];
+    __shared__ int32_t s_counts[kWaves][G * V];
     __shared__ int32_t s_kept[kWaves];
     __shared__ double s_dot[kWaves];
     __shared__ int32_t s_pairs[kWaves];
@@ -89,31 +134,40 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
         count[v] = 0;
     }
     // all lanes of a wave take as many turns: a token past the end is one that is left out and not written
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < a.tokens;
-         first += static_cast<int64_t>(gridDim.x) * kRows) {
-        const int64_t t = first + group;
-        const bool there = t < a.tokens;
-        const T *row = logits + (there ? t : a.tokens - 1) * E;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + group;
+    float next[V];
+    uint8_t next_in = 1;
+    const auto fetch = [&](int64_t at) {
+        at = at < a.tokens ? at : a.tokens - 1;
+        load_row<G, V, WHOLE>(logits + at * E, lane, E, next);
+        if (a.mask) next_in = a.mask[at];
+    };
+    fetch(t);
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < a.tokens; first += step, t += step) {
+        const bool there = t < a.tokens, in = there && next_in != 0;
         float x[V];
         uint32_t key[V];
-        const bool in = there && (!a.mask || a.mask[t] != 0);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = v * G + lane;
-            x[v] = e < E ? static_cast<float>(row[e]) : -__builtin_inff();
-            key[v] = e < E && in ? order_of(x[v]) : 0u;
+            x[v] = next[v];
+            key[v] = in ? order_of(x[v]) : 0u;
+            if (!WHOLE && lane * V + v >= E) key[v] = 0u;
         }
+        if (first + step < a.tokens) fetch(t + step);
         float largest = 0.0f, total = 0.0f, sum = 0.0f;
         bool takes = in;
-        for (int k = 0; k < K; ++k) {
-            uint32_t best = 0;
-            int expert = 0x7fffffff;
+        int32_t my_id[kHold];
+        float my_e[kHold];
+        const bool held = K <= G * kHold;
+        const auto choose = [&](int k, int slot) {
+            uint32_t best = key[0], expert = static_cast<uint32_t>(lane * V);
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (key[v] > best) {
-                    best = key[v];
-                    expert = v * G + lane;
-                }
+            for (int v = 1; v < V; ++v) {
+                const bool take = key[v] > best;
+                best = take ? key[v] : best;
+                expert = take ? static_cast<uint32_t>(lane * V + v) : expert;
+            }
             group_best<G>(best, expert);
             takes = takes && best > kOrderOfNone;
             const uint32_t bits = best & 0x80000000u ? best & 0x7fffffffu : ~best;
@@ -123,31 +177,57 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
                 float p[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    p[v] = v * G + lane < E ? expf(x[v] - largest) : 0.0f;
+                    p[v] = expf(x[v] - largest);  // 0 past the last expert
+                    if (!WHOLE && lane * V + v >= E) p[v] = 0.0f;
                     sum += p[v];
                 }
-                sum = group_sum<G>(sum);
-                if (takes) {
-                    const float scale = 1.0f / sum;
+                sum = sum_of<G>(sum);
+                const float scale = takes ? 1.0f / sum : 0.0f;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) share[v] = __builtin_fmaf(p[v], scale, share[v]);
-                    kept += lane == 0;
-                }
+                for (int v = 0; v < V; ++v) share[v] = takes ? __builtin_fmaf(p[v], scale, share[v]) : share[v];
+                kept += takes && lane == 0;
             }
             const float e = takes ? expf(value - largest) : 0.0f;
             total += e;
-            if (takes) {
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (v * G + lane == expert) {
-                        ++count[v];
-                        key[v] = 0;
-                    }
+            for (int v = 0; v < V; ++v) {
+                const bool mine = takes && static_cast<uint32_t>(lane * V + v) == expert;
+                count[v] += mine;
+                key[v] = mine ? 0u : key[v];
             }
-            if (there && lane == 0) {
-                a.ids[t * K + k] = takes ? expert : -1;
-                a.weights[t * K + k] = takes ? a.renormalize ? e : e / sum : 0.0f;
+            const int32_t id = takes ? static_cast<int32_t>(expert) : -1;
+            if (held) {
+                if (G == 1 || k == lane) {
+                    my_id[slot] = id;
+                    my_e[slot] = e;
+                }
+            } else if (there && lane == 0) {
+                a.ids[t * K + k] = id;
+                a.weights[t * K + k] = e;
             }
+        };
+        if constexpr (G == 1) {
+#pragma unroll
+            for (int k = 0; k < kHold; ++k)
+                if (k < K) choose(k, k);
+            for (int k = kHold; k < K; ++k) choose(k, 0);
+        } else {
+            for (int k = 0; k < K; ++k) choose(k, 0);
+        }
+        // divided by the sum of the chosen or of all: no token has an empty sum but one that is left out
+        const float divisor = a.renormalize ? total : sum;
+        if (held) {
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) {
+                const int k = G == 1 ? i : lane;
+                if (there && k < K) {
+                    a.ids[t * K + k] = my_id[i];
+                    a.weights[t * K + k] = my_id[i] >= 0 ? my_e[i] / divisor : 0.0f;
+                }
+            }
+        } else if (there && lane == 0) {  // read back by the lane that wrote them
+            for (int k = 0; k < K; ++k)
+                a.weights[t * K + k] = a.ids[t * K + k] >= 0 ? a.weights[t * K + k] / divisor : 0.0f;
         }
         if (++turn % 64 == 0) {
 #pragma unroll
@@ -156,47 +236,51 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
                 share[v] = 0.0f;
             }
         }
-        // read back by the lane that wrote them
-        if (a.renormalize && in && there && lane == 0 && total != 0.0f)
-            for (int k = 0; k < K; ++k) a.weights[t * K + k] /= total;
     }
-    // the workgroup's sums: its groups' in order
+    // the workgroup's sums: over the wave's groups, then the waves in order
     const bool alone = gridDim.x == 1;
+    const int wave = threadIdx.x / kWave;
     double dot = 0.0;
     int32_t pairs = 0;
 #pragma unroll
     for (int d = kWave / 2; d > 0; d >>= 1) kept += __shfl_xor(kept, d, kWave);
-    if (threadIdx.x % kWave == 0) s_kept[threadIdx.x / kWave] = kept;
+    if (threadIdx.x % kWave == 0) s_kept[wave] = kept;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float s = shares[v] + share[v];
+        int32_t c = count[v];
+#pragma unroll
+        for (int d = G; d < kWave; d <<= 1) {
+            s += __shfl_xor(s, d, kWave);
+            c += __shfl_xor(c, d, kWave);
+        }
+        if (threadIdx.x % kWave < G) {
+            s_shares[wave][lane * V + v] = s;
+            s_counts[wave][lane * V + v] = c;
+        }
+    }
     __syncthreads();
     kept = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) kept += s_kept[w];
     const float inverse = 1.0f / static_cast<float>(kept > 0 ? kept : 1);
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+        float s = 0.0f;
+        int32_t c = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        __syncthreads();
-        s_shares[threadIdx.x] = shares[v] + share[v];
-        s_counts[threadIdx.x] = count[v];
-        __syncthreads();
-        for (int l = threadIdx.x; l < G; l += kThreads) {
-            const int e = v * G + l;
-            if (e >= E) continue;
-            float s = 0.0f;
-            int32_t c = 0;
-            for (int r = 0; r < kRows; ++r) {
-                s += s_shares[r * G + l];
-                c += s_counts[r * G + l];
-            }
-            if (alone) {
-                s *= inverse;
-                a.shares[e] = s;
-                a.counts[e] = c;
-                dot += static_cast<double>(s) * c;
-                pairs += c;
-            } else {
-                a.part_shares[static_cast<int64_t>(blockIdx.x) * E + e] = s;
-                a.part_counts[static_cast<int64_t>(blockIdx.x) * E + e] = c;
-            }
+        for (int w = 0; w < kWaves; ++w) {
+            s += s_shares[w][e];
+            c += s_counts[w][e];
+        }
+        if (alone) {
+            s *= inverse;
+            a.shares[e] = s;
+            a.counts[e] = c;
+            dot += static_cast<double>(s) * c;
+            pairs += c;
+        } else {
+            a.part_shares[static_cast<int64_t>(blockIdx.x) * E + e] = s;
+            a.part_counts[static_cast<int64_t>(blockIdx.x) * E + e] = c;
         }
     }
     if (!alone) {
@@ -239,11 +323,12 @@ __device__ __forceinline__ S workgroup_sum(S v, S *slots) {
     return s;
 }
 
-// Adds the workgroups' sums of kJoinCols experts; where that is all of them, the loss too.
+// Adds the workgroups' sums of `cols` experts (a power of two); where that is all of them, the loss too. The threads of an
+// expert share its sums and are added pair by pair.
 __global__ __launch_bounds__(kJoinThreads) void route_join_kernel(const int32_t *__restrict__ part_counts,
                                                                   const float *__restrict__ part_shares,
                                                                   const int32_t *__restrict__ part_kept, int parts,
-                                                                  int experts, int32_t *__restrict__ counts,
+                                                                  int experts, int cols, int32_t *__restrict__ counts,
                                                                   float *__restrict__ shares,
                                                                   int32_t *__restrict__ kept_out,
                                                                   float *__restrict__ loss) {
@@ -254,24 +339,28 @@ __global__ __launch_bounds__(kJoinThreads) void route_join_kernel(const int32_t 
     int32_t kept = 0;
     for (int b = threadIdx.x; b < parts; b += kJoinThreads) kept += part_kept[b];
     kept = workgroup_sum<kJoinThreads>(kept, s_sum);
-    const int col = threadIdx.x % kJoinCols, slice = threadIdx.x / kJoinCols, e = blockIdx.x * kJoinCols + col;
+    const int col = threadIdx.x % cols, slice = threadIdx.x / cols, slices = kJoinThreads / cols;
+    const int e = blockIdx.x * cols + col;
     double s = 0.0;
     int32_t c = 0;
     if (e < experts)
-        for (int b = slice; b < parts; b += kJoinSlices) {
+#pragma unroll 4
+        for (int b = slice; b < parts; b += slices) {
             s += static_cast<double>(part_shares[static_cast<int64_t>(b) * experts + e]);
             c += part_counts[static_cast<int64_t>(b) * experts + e];
         }
     s_share[threadIdx.x] = s;
     s_count[threadIdx.x] = c;
-    __syncthreads();
+    for (int n = slices / 2; n > 0; n >>= 1) {
+        __syncthreads();
+        if (slice < n) {
+            s_share[threadIdx.x] = s += s_share[threadIdx.x + n * cols];
+            s_count[threadIdx.x] = c += s_count[threadIdx.x + n * cols];
+        }
+    }
     double dot = 0.0;
     int32_t pairs = 0;
     if (slice == 0 && e < experts) {
-        for (int i = 1; i < kJoinSlices; ++i) {
-            s += s_share[i * kJoinCols + col];
-            c += s_count[i * kJoinCols + col];
-        }
         s /= kept > 0 ? kept : 1;
         shares[e] = static_cast<float>(s);
         counts[e] = c;
@@ -326,11 +415,33 @@ struct RouteBwdArgs {
 // The gradient of a token's logits, formed again from them:
 //   through the weights  [j = ids_k] w_k (g_k - sum_i g_i w_i), or, not renormalised, the sum's part times p_j,
 //   through the loss     grad_loss * experts / kept * p_j (f_j - sum_e f_e p_e),  f_e = counts_e / sum of counts.
-template <typename T, int G, int V>
+// Lane k of the group has the token's choice k (and k + G, ...), and gives it to the others in turn.
+template <typename T, int G, int V, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
     constexpr int kRows = kThreads / G;
     __shared__ int32_t s_sum[kWaves];
     const int lane = threadIdx.x % G, group = threadIdx.x / G, E = a.experts, K = a.choices;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + group;
+    struct Choice {
+        int32_t id;
+        float w, g;
+    };
+    float next[V];
+    Choice next_choice;
+    const auto choice = [&](int64_t at, int k) {
+        const int64_t i = at * K + (k < K ? k : K - 1);
+        Choice c = {a.ids[i], a.weights[i], 0.0f};
+        if (a.grad_weights) c.g = a.grad_weights[i];
+        if (k >= K) c.id = -1;
+        return c;
+    };
+    const auto fetch = [&](int64_t at) {
+        at = at < a.tokens ? at : a.tokens - 1;
+        load_row<G, V, WHOLE>(static_cast<const T *>(a.logits) + at * E, lane, E, next);
+        next_choice = choice(at, G == 1 ? 0 : lane);
+    };
+    fetch(t);
     float f[V], scale = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) f[v] = 0.0f;
@@ -343,59 +454,72 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdArgs a) {
         const float inverse = 1.0f / static_cast<float>(pairs > 0 ? pairs : 1);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (v * G + lane < E) f[v] = static_cast<float>(a.counts[v * G + lane]) * inverse;
+            if (lane * V + v < E) f[v] = static_cast<float>(a.counts[lane * V + v]) * inverse;
     }
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < a.tokens;
-         first += static_cast<int64_t>(gridDim.x) * kRows) {
-        const int64_t t = first + group;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < a.tokens; first += step, t += step) {
         const bool there = t < a.tokens;
         const int64_t at = there ? t : a.tokens - 1;
-        const T *row = static_cast<const T *>(a.logits) + at * E;
-        const int32_t *ids = a.ids + at * K;
-        const bool in = ids[0] >= 0;
         float p[V], most = -__builtin_inff(), sum = 0.0f;
+        const Choice mine = next_choice;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            p[v] = v * G + lane < E ? static_cast<float>(row[v * G + lane]) : -__builtin_inff();
+            p[v] = next[v];
             most = fmaxf(most, p[v]);
         }
-#pragma unroll
-        for (int d = G / 2; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor(most, d, kWave));
+        if (first + step < a.tokens) fetch(t + step);
+        fold<G>([&](auto d) {
+            most = fmaxf(most, __builtin_bit_cast(float, across<decltype(d)::value>(__builtin_bit_cast(uint32_t, most))));
+        });
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            p[v] = v * G + lane < E ? expf(p[v] - most) : 0.0f;
+            p[v] = expf(p[v] - most);
+            if (!WHOLE && lane * V + v >= E) p[v] = 0.0f;
             sum += p[v];
         }
-        const float inverse = 1.0f / group_sum<G>(sum);
-        float mean = 0.0f, total = 0.0f;
+        const float inverse = 1.0f / sum_of<G>(sum);
+        float mean = 0.0f, total = mine.id >= 0 ? mine.g * mine.w : 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             p[v] *= inverse;
             mean = __builtin_fmaf(p[v], f[v], mean);
         }
-        mean = group_sum<G>(mean);
-        if (a.grad_weights)
-            for (int k = 0; k < K; ++k)
-                if (ids[k] >= 0) total = __builtin_fmaf(a.grad_weights[at * K + k], a.weights[at * K + k], total);
+        mean = sum_of<G>(mean);
+        for (int k = G; k < K; k += G) {
+            const Choice c = choice(at, k + lane);
+            total += c.id >= 0 ? c.g * c.w : 0.0f;
+        }
+        total = sum_of<G>(total);
+        // a token that was left out has no first choice
+        const bool in = __shfl(mine.id, threadIdx.x % kWave - lane, kWave) >= 0;
         float g[V];
         const float through = a.renormalize ? 0.0f : total;
 #pragma unroll
         for (int v = 0; v < V; ++v) g[v] = p[v] * __builtin_fmaf(scale, f[v] - mean, -through);
-        if (a.grad_weights)
-            for (int k = 0; k < K; ++k) {
-                const int e = ids[k];
-                if (e < 0) continue;
-                const float w = a.weights[at * K + k], gw = a.grad_weights[at * K + k];
-                const float add = a.renormalize ? w * (gw - total) : w * gw;
+        const auto add = [&](const Choice &c, int from) {
+            const float part = a.renormalize ? c.w * (c.g - total) : c.w * c.g;
+            const int32_t id = G == 1 ? c.id : __shfl(c.id, threadIdx.x % kWave - lane + from, kWave);
+            const float of = G == 1 ? part : __shfl(part, threadIdx.x % kWave - lane + from, kWave);
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (v * G + lane == e) g[v] += add;
-            }
-        if (there) {
-            T *out = static_cast<T *>(a.grad_logits) + t * E;
+            for (int v = 0; v < V; ++v) g[v] += id == lane * V + v ? of : 0.0f;
+        };
+        for (int k = 0; k < K && k < G; ++k) add(mine, k);
+        for (int k = G; k < K; k += G) {
+            const Choice c = choice(at, k + lane);
+            for (int i = 0; i < G && k + i < K; ++i) add(c, i);
+        }
+        T *out = static_cast<T *>(a.grad_logits) + at * E;
+        if (!there) continue;
+        if constexpr (WHOLE) {
+            typedef T P __attribute__((ext_vector_type(V)));
+            typedef P U __attribute__((aligned(sizeof(T))));
+            P o;
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = static_cast<T>(in ? g[v] : 0.0f);
+            *reinterpret_cast<U *>(out + lane * V) = o;
+        } else {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (v * G + lane < E) out[v * G + lane] = static_cast<T>(in ? g[v] : 0.0f);
+                if (lane * V + v < E) out[lane * V + v] = static_cast<T>(in ? g[v] : 0.0f);
         }
     }
 }
@@ -414,11 +538,12 @@ gs_status check_route(const char *name, int64_t tokens, int experts, int64_t cho
     return GS_OK;
 }
 
-// Lanes that share a token: as many as it has experts, up to a wave.
-inline int route_lanes(int experts) {
-    int g = 1;
-    while (g < experts && g < kWave) g *= 2;
-    return g;
+// Lanes that share a token, and a lane's experts. Up to 16 experts a lane has a token of its own and no value crosses
+// lanes; up to 256 they are 16 lanes, within which values cross without LDS.
+constexpr int route_lanes(int experts) { return experts <= 16 ? 1 : experts <= 32 ? 8 : experts <= 256 ? 16 : 64; }
+constexpr int route_columns(int experts) {
+    return experts <= 4 ? 4 : experts <= 8 ? 8 : experts <= 16 ? 16 : experts <= 64 ? 4 : experts <= 128 ? 8
+           : experts <= 1024 ? 16 : 64;
 }
 
 struct RouteRoom {
@@ -441,23 +566,26 @@ RouteRoom route_room(int64_t tokens, int experts) {
 
 using namespace gs;
 
-// Launches kernel<T, G, V> for the type code and the number of experts.
-#define GS_ROUTE_LAUNCH_GV(kernel, T, G, V) \
-    hipLaunchKernelGGL((kernel<T, G, V>), grid, dim3(kThreads), 0, stream, a)
-#define GS_ROUTE_LAUNCH_T(kernel, T)                                    \
-    do {                                                                \
-        if (experts <= 1) GS_ROUTE_LAUNCH_GV(kernel, T, 1, 1);          \
-        else if (experts <= 2) GS_ROUTE_LAUNCH_GV(kernel, T, 2, 1);     \
-        else if (experts <= 4) GS_ROUTE_LAUNCH_GV(kernel, T, 4, 1);     \
-        else if (experts <= 8) GS_ROUTE_LAUNCH_GV(kernel, T, 8, 1);     \
-        else if (experts <= 16) GS_ROUTE_LAUNCH_GV(kernel, T, 16, 1);   \
-        else if (experts <= 32) GS_ROUTE_LAUNCH_GV(kernel, T, 32, 1);   \
-        else if (experts <= 64) GS_ROUTE_LAUNCH_GV(kernel, T, 64, 1);   \
-        else if (experts <= 128) GS_ROUTE_LAUNCH_GV(kernel, T, 64, 2);  \
-        else if (experts <= 256) GS_ROUTE_LAUNCH_GV(kernel, T, 64, 4);  \
-        else if (experts <= 1024) GS_ROUTE_LAUNCH_GV(kernel, T, 64, 16); \
-        else GS_ROUTE_LAUNCH_GV(kernel, T, 64, 64);                     \
-        GS_LAUNCH_TRY(#kernel);                                         \
+// Launches kernel<T, G, V, WHOLE> for the type code and the number of experts.
+#define GS_ROUTE_LAUNCH_V(kernel, T, MOST, WHOLE)                                                              \
+    hipLaunchKernelGGL((kernel<T, route_lanes(MOST), route_columns(MOST), WHOLE>), grid, dim3(kThreads), 0, stream, a)
+#define GS_ROUTE_LAUNCH_W(kernel, T, MOST)                                 \
+    do {                                                                   \
+        if (experts == MOST) GS_ROUTE_LAUNCH_V(kernel, T, MOST, true);     \
+        else GS_ROUTE_LAUNCH_V(kernel, T, MOST, false);                    \
+    } while (0)
+#define GS_ROUTE_LAUNCH_T(kernel, T)                                \
+    do {                                                            \
+        if (experts <= 4) GS_ROUTE_LAUNCH_W(kernel, T, 4);          \
+        else if (experts <= 8) GS_ROUTE_LAUNCH_W(kernel, T, 8);     \
+        else if (experts <= 16) GS_ROUTE_LAUNCH_W(kernel, T, 16);   \
+        else if (experts <= 32) GS_ROUTE_LAUNCH_W(kernel, T, 32);   \
+        else if (experts <= 64) GS_ROUTE_LAUNCH_W(kernel, T, 64);   \
+        else if (experts <= 128) GS_ROUTE_LAUNCH_W(kernel, T, 128); \
+        else if (experts <= 256) GS_ROUTE_LAUNCH_W(kernel, T, 256); \
+        else if (experts <= 1024) GS_ROUTE_LAUNCH_V(kernel, T, 1024, false); \
+        else GS_ROUTE_LAUNCH_V(kernel, T, 4096, false);             \
+        GS_LAUNCH_TRY(#kernel);                                     \
     } while (0)
 #define GS_ROUTE_LAUNCH(kernel)                                   \
     do {                                                          \
@@ -511,9 +639,11 @@ extern "C" gs_status gs_expert_route(const void *logits, const uint8_t *mask, in
     const dim3 grid(static_cast<unsigned>(room.blocks));
     GS_ROUTE_LAUNCH(route_kernel);
     if (room.blocks == 1) return ok();
-    const int joins = (experts + kJoinCols - 1) / kJoinCols;
+    int cols = 1;
+    while (cols < experts && cols < kJoinCols) cols *= 2;
+    const int joins = (experts + cols - 1) / cols;
     hipLaunchKernelGGL(route_join_kernel, dim3(static_cast<unsigned>(joins)), dim3(kJoinThreads), 0, stream,
-                       a.part_counts, a.part_shares, a.part_kept, room.blocks, experts, counts, shares, kept, loss);
+                       a.part_counts, a.part_shares, a.part_kept, room.blocks, experts, cols, counts, shares, kept, loss);
     GS_LAUNCH_TRY("route_join_kernel");
     if (joins > 1) {
         hipLaunchKernelGGL(route_loss_kernel, dim3(1), dim3(kJoinThreads), 0, stream, counts, shares, experts, loss);
@@ -542,7 +672,7 @@ extern "C" gs_status gs_expert_route_bwd(const void *logits, const int32_t *ids,
     RouteBwdArgs a = {logits, ids, counts, kept, weights, grad_weights, grad_loss, tokens, experts,
                       static_cast<int>(choices), renormalize ? 1 : 0, grad_logits};
     const int64_t rows = kThreads / route_lanes(experts), want = (tokens + rows - 1) / rows;
-    const dim3 grid(static_cast<unsigned>(want < 8 * kBlocks ? want : 8 * kBlocks));
+    const dim3 grid(static_cast<unsigned>(want < 2 * kBlocks ? want : 2 * kBlocks));
     GS_ROUTE_LAUNCH(route_bwd_kernel);
     return ok();
 }
