@@ -902,11 +902,10 @@ def gs_expert_route(logits, choices, mask=None, renormalize=True, out=None, stre
     code, dev, T, E, pl = _logits(logits, K)
     pm = None if mask is None else _arg(mask, "mask", torch.bool, dev, (T,))
     if out is None:
-        floats, ints = torch.empty((E + 1,), dtype=torch.float32, device=dev), \
-            torch.empty((E + 1,), dtype=torch.int32, device=dev)
-        out = ExpertRoute(torch.empty((T, K), dtype=torch.int32, device=dev),
-                          torch.empty((T, K), dtype=torch.float32, device=dev), ints[:E], floats[:E],
-                          floats[E], ints[E:])
+        ids = torch.empty((T, K), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, K), dtype=torch.float32, device=dev)
+        out = ExpertRoute(ids, weights, ids.new_empty(E), weights.new_empty(E), weights.new_empty(()),
+                          ids.new_empty(1))
         po = [t.data_ptr() for t in (out.ids, out.weights, out.counts, out.shares, out.loss, out.kept)]
     else:
         po = [_arg(out.ids, "ids", torch.int32, dev, (T, K)), _arg(out.weights, "weights", torch.float32, dev, (T, K)),

@@ -81,28 +81,6 @@ __device__ __forceinline__ Run find_tile(const ProductArgs &a, int height, int64
     return {a.experts, 0, 0};
 }
 
-// Four results of a row from column n on.
-template <typename T>
-__device__ __forceinline__ void store_four(T *row, int n, int cols, const float *v) {
-    typedef T V __attribute__((ext_vector_type(4)));
-    typedef V VU __attribute__((aligned(sizeof(T))));
-    V o;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = static_cast<T>(v[k]);
-    if (n + 4 <= cols) {
-        *reinterpret_cast<VU *>(row + n) = o;
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (n + k < cols) row[n + k] = o[k];
-}
-__device__ __forceinline__ void store_four(const ProductArgs &a, int64_t row, int n, const float *v) {
-    if (a.out_type == GS_F32) store_four(static_cast<float *>(a.out) + row * a.cols, n, a.cols, v);
-    else if (a.out_type == GS_BF16) store_four(static_cast<__bf16 *>(a.out) + row * a.cols, n, a.cols, v);
-    else store_four(static_cast<_Float16 *>(a.out) + row * a.cols, n, a.cols, v);
-}
-
 // The row of x that row i of a run's tile is: rows past the run's end repeat its last and are not stored.
 __device__ __forceinline__ int64_t x_row(const ProductArgs &a, const Run &run, int i) {
     const int64_t r = run.begin + i < run.end ? run.begin + i : run.end - 1;
@@ -129,28 +107,88 @@ __device__ __forceinline__ bool place_of(int64_t turn, int64_t tiles, int64_t ro
     return true;
 }
 
+// 16 columns of a row of results: lane l has columns l / 32 * 4 on of each 8, and of another 8. to: the row's first of them.
+// `room`: columns up to the row's end, if WHOLE is not to hold.
+template <bool WHOLE>
+__device__ __forceinline__ void store_sixteen(float *to, int room, const float *v) {
+    typedef float V __attribute__((ext_vector_type(4)));
+    typedef V VU __attribute__((aligned(4)));
+    const int half = threadIdx.x % kWave / 32;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int n = h * 8 + half * 4;
+        if (WHOLE || n + 4 <= room) {
+            *reinterpret_cast<VU *>(to + n) = V{v[h * 4], v[h * 4 + 1], v[h * 4 + 2], v[h * 4 + 3]};
+            continue;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (n + k < room) to[n + k] = v[h * 4 + k];
+    }
+}
+// In 16 bits the lanes of a row exchange halves first, so that each stores 8 neighbours.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void store_sixteen(T *to, int room, const float *v) {
+    typedef T V __attribute__((ext_vector_type(8)));
+    typedef V VU __attribute__((aligned(sizeof(T))));
+    V own;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) own[k] = static_cast<T>(v[k]);
+    const u32x4 w = __builtin_bit_cast(u32x4, own);
+    const auto first = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    const auto second = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    const V o = __builtin_bit_cast(V, u32x4{first[0], second[0], first[1], second[1]});
+    const int n = threadIdx.x % kWave / 32 * 8;
+    if (WHOLE || n + 8 <= room) {
+        *reinterpret_cast<VU *>(to + n) = o;
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (n + k < room) to[n + k] = o[k];
+}
+
+template <typename T, bool WHOLE, int FR, int FC>
+__device__ __forceinline__ void store_rows(const ProductArgs &a, const Run &run, const f32x16 (&acc)[FR][FC], int row0,
+                                           int col0) {
+    const float low = a.relu ? 0.0f : -__builtin_inff();
+    const int64_t row = run.begin + row0 + threadIdx.x % 32;
+    T *to = static_cast<T *>(a.out) + row * a.cols + col0;
+#pragma unroll
+    for (int i = 0; i < FR; ++i) {
+        if (row + i * 32 < run.end) {  // lanes l and l + 32 have the same row: both or neither
+#pragma unroll
+            for (int k = 0; k < FC; ++k)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float v[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        v[q] = acc[i][k][g * 8 + q];
+                        v[q] = v[q] < low ? low : v[q];  // NaN stays
+                    }
+                    store_sixteen<WHOLE>(to + k * 32 + g * 16, a.cols - col0 - k * 32 - g * 16, v);
+                }
+        }
+        to += 32 * static_cast<int64_t>(a.cols);
+        asm volatile("" : "+v"(to));  // formed here, not kept from before the products
+    }
+}
+
 // A wave's results: lane l has row l % 32 of each 32 x 32, and of its columns four from l / 32 * 4 on of every eight.
 template <int FR, int FC>
 __device__ __forceinline__ void store_tile(const ProductArgs &a, const Run &run, const f32x16 (&acc)[FR][FC], int row0,
                                            int col0) {
-    const int lane = threadIdx.x % kWave;
-#pragma unroll
-    for (int i = 0; i < FR; ++i) {
-        const int64_t row = run.begin + row0 + i * 32 + lane % 32;
-        if (row >= run.end) continue;
-#pragma unroll
-        for (int k = 0; k < FC; ++k)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float v[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    v[q] = acc[i][k][g * 4 + q];
-                    if (a.relu) v[q] = v[q] < 0.0f ? 0.0f : v[q];  // NaN stays
-                }
-                const int n = col0 + k * 32 + g * 8 + lane / 32 * 4;
-                if (n < a.cols) store_four(a, row, n, v);
-            }
+    const bool whole = col0 + FC * 32 <= a.cols;
+    if (a.out_type == GS_F32) {
+        if (whole) store_rows<float, true>(a, run, acc, row0, col0);
+        else store_rows<float, false>(a, run, acc, row0, col0);
+    } else if (a.out_type == GS_BF16) {
+        if (whole) store_rows<__bf16, true>(a, run, acc, row0, col0);
+        else store_rows<__bf16, false>(a, run, acc, row0, col0);
+    } else {
+        if (whole) store_rows<_Float16, true>(a, run, acc, row0, col0);
+        else store_rows<_Float16, false>(a, run, acc, row0, col0);
     }
 }
 
@@ -161,7 +199,7 @@ __device__ __forceinline__ void load_slots(const uint8_t *src, uint32_t lds) {
 }
 template <int OUTSTANDING>
 __device__ __forceinline__ void wait_and_meet() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(OUTSTANDING) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(OUTSTANDING) : "memory");
 }
 
 // Where the 16-byte chunk c (of four) of a row of a stage lies among the row's four places: so that both 8 and 16 rows
@@ -170,8 +208,9 @@ __device__ __forceinline__ int turn_of(int row) { return ((row >> 1) ^ (row >> 3
 
 // Tile of BM rows and BN columns by WR x WC waves. A stage is 64 columns of k of all the tile's rows and of its weights'
 // rows; four stages are in LDS, loaded without registers in between while the products of the one before run.
+// An operand's registers are filled with the next stage's as soon as its last product of this one has begun.
 template <int BM, int BN, int WR, int WC>
-__global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (BM <= 128 ? 2 : 1)) void product_kernel(ProductArgs a) {
+__global__ __launch_bounds__(WR *WC *kWave, BM <= 128 ? 2 : 1) void product_kernel(ProductArgs a) {
     constexpr int kStages = 4, kRows = BM + BN, kWaves = WR * WC, kThreads = kWaves * kWave;
     constexpr int FR = BM / 32 / WR, FC = BN / 32 / WC;
     static_assert(FR * WR * 32 == BM && FC * WC * 32 == BN, "whole results");
@@ -198,7 +237,6 @@ __global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (BM <= 128 ? 2 : 1)) vo
         const int col0 = static_cast<int>(at.col_tile) * BN;
         f32x16 acc[FR][FC] = {};
         if (run.expert < a.experts) {
-            // rows past the run's end repeat its last and are not stored
             const uint8_t *src[L];
 #pragma unroll
             for (int i = 0; i < L; ++i) {
@@ -208,69 +246,88 @@ __global__ __launch_bounds__(WR *WC *kWave, WR *WC / 4 * (BM <= 128 ? 2 : 1)) vo
             }
             for (int block0 = 0; block0 < a.blocks; block0 += kScaleBlocks) {
                 const int blocks = a.blocks - block0 < kScaleBlocks ? a.blocks - block0 : kScaleBlocks;
-                __syncthreads();  // the last products' scales are read
-                for (int i = threadIdx.x; i < kRows * (kScaleBlocks / 4); i += kThreads) {
-                    const int row = i % kRows, quad = i / kRows;
-                    if (quad * 4 >= blocks) break;
-                    const uint8_t *from = row < BM ? a.x_scales + x_row(a, run, row) * a.blocks
-                                                   : a.w_scales + w_row(a, run, col0 + row - BM) * a.blocks;
-                    uint32_t four = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (quad * 4 + k < blocks) four |= static_cast<uint32_t>(from[block0 + quad * 4 + k]) << (8 * k);
-                    s_scales[quad][row] = four;
-                }
                 const int stages = blocks * 2;
+                __syncthreads();  // the last products' scales and operands are read
                 int issued = 0;
                 const auto issue = [&](int i) {
                     load_slots(src[i], ring + (issued % kStages) * kStageBytes + (wave * L + i) * 1024);
                     // past the end of k the last stage is loaded again, unused
                     if (issued + 1 < stages) src[i] += kStep;
                 };
-                i32x8 frag[2][FR + FC];
-                const auto fetch = [&](int stage, int turn, int r) {
-                    const uint8_t *at = s_ring + (stage % kStages) * kStageBytes + first +
-                                        (r < FR ? wr * FR + r : BM / 32 + wc * FC + r - FR) * (32 * kStep);
+                for (; issued < kStages - 1; ++issued)
+#pragma unroll
+                    for (int i = 0; i < L; ++i) issue(i);
+#pragma unroll
+                for (int row = threadIdx.x; row < kRows; row += kThreads) {
+                    const uint8_t *from = (row < BM ? a.x_scales + x_row(a, run, row) * a.blocks
+                                                    : a.w_scales + w_row(a, run, col0 + row - BM) * a.blocks) + block0;
+                    uint32_t four[kScaleBlocks / 4];
+                    if (blocks >= 4) {
+                        // the last four end with the row; what lies before is shifted out
+#pragma unroll
+                        for (int quad = 0; quad < kScaleBlocks / 4; ++quad) {
+                            const int b = quad * 4 + 4 <= blocks ? quad * 4 : blocks - 4;
+                            uint32_t word;
+                            __builtin_memcpy(&word, from + b, 4);
+                            four[quad] = quad * 4 - b < 4 ? word >> (quad * 4 - b) * 8 : 0;
+                        }
+                    } else {
+                        four[0] = 0;
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) four[0] |= (k < blocks ? from[k] : 0u) << 8 * k;
+#pragma unroll
+                        for (int quad = 1; quad < kScaleBlocks / 4; ++quad) four[quad] = 0;
+                    }
+#pragma unroll
+                    for (int quad = 0; quad < kScaleBlocks / 4; ++quad) s_scales[quad][row] = four[quad];
+                }
+                i32x8 fx[FR], fw[FC];
+                const auto fetch = [&](int stage, int row) {
+                    const uint8_t *at = s_ring + (stage % kStages) * kStageBytes + first + row * kStep;
                     const i32x4 low = *reinterpret_cast<const i32x4 *>(at);
                     const i32x4 high = *reinterpret_cast<const i32x4 *>(s_ring + ((at - s_ring) ^ 16));
-                    frag[turn][r] = __builtin_shufflevector(low, high, 0, 1, 2, 3, 4, 5, 6, 7);
+                    return __builtin_shufflevector(low, high, 0, 1, 2, 3, 4, 5, 6, 7);
                 };
-                int scale[FR + FC];
-                const auto multiply = [&](int turn, int next) {
-                    constexpr int M = FR * FC, R = FR + FC;
+                const auto fetch_x = [&](int stage, int i) { fx[i] = fetch(stage, (wr * FR + i) * 32); };
+                const auto fetch_w = [&](int stage, int k) { fw[k] = fetch(stage, BM + (wc * FC + k) * 32); };
+                int sx[FR], sw[FC];
+                const auto multiply = [&](int stage) {
+                    constexpr int M = FR * FC;
 #pragma unroll
                     for (int m = 0; m < M; ++m) {
-#pragma unroll
-                        for (int r = m * R / M; r < (m + 1) * R / M; ++r) fetch(next, 1 - turn, r);
-#pragma unroll
-                        for (int i = m * L / M; i < (m + 1) * L / M; ++i) issue(i);
                         const int i = m / FC, k = m % FC;
-                        acc[i][k] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                            frag[turn][FR + k], frag[turn][i], acc[i][k], 0, 0, 0, scale[FR + k], 0, scale[i]);
+                        acc[i][k] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[k], fx[i], acc[i][k], 0, 0, 0,
+                                                                                    sw[k], 0, sx[i]);
+                        if (k == FC - 1) fetch_x(stage + 1, i);
+                        if (i == FR - 1) fetch_w(stage + 1, k);
+#pragma unroll
+                        for (int l = m * L / M; l < (m + 1) * L / M; ++l) issue(l);
                         __builtin_amdgcn_sched_barrier(0);
                     }
                     ++issued;
                 };
-                for (; issued < kStages - 1; ++issued)
-#pragma unroll
-                    for (int i = 0; i < L; ++i) issue(i);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's scales are in LDS
                 wait_and_meet<(kStages - 2) * L>();
 #pragma unroll
-                for (int r = 0; r < FR + FC; ++r) fetch(0, 0, r);
+                for (int i = 0; i < FR; ++i) fetch_x(0, i);
+#pragma unroll
+                for (int k = 0; k < FC; ++k) fetch_w(0, k);
                 for (int b = 0; b < blocks; ++b) {
-                    // At each meeting the next stage is there and all waves are done with the one before this, whose
-                    // place the loads then take.
+                    // At each meeting the next stage is there and all waves have the operands of the one before this,
+                    // whose place the loads then take.
                     wait_and_meet<(kStages - 3) * L>();
 #pragma unroll
-                    for (int r = 0; r < FR + FC; ++r)
-                        scale[r] = b % 4 ? scale[r] >> 8
-                                         : static_cast<int>(s_scales[b / 4][(r < FR ? wr * FR + r : BM / 32 + wc * FC +
-                                                                             r - FR) * 32 + lane % 32]);
-                    multiply(0, 2 * b + 1);
+                    for (int i = 0; i < FR; ++i)
+                        sx[i] = b % 4 ? sx[i] >> 8 : static_cast<int>(s_scales[b / 4][(wr * FR + i) * 32 + lane % 32]);
+#pragma unroll
+                    for (int k = 0; k < FC; ++k)
+                        sw[k] = b % 4 ? sw[k] >> 8
+                                      : static_cast<int>(s_scales[b / 4][BM + (wc * FC + k) * 32 + lane % 32]);
+                    multiply(2 * b);
                     wait_and_meet<(kStages - 3) * L>();
-                    multiply(1, 2 * b + 2);
+                    multiply(2 * b + 1);
                 }
-                wait_and_meet<0>();
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 #pragma unroll
                 for (int i = 0; i < L; ++i) src[i] += kStep;  // the step that the last stage did not take
             }
@@ -413,7 +470,7 @@ extern "C" gs_status gs_expert_product(const void *x, const void *x_scales, cons
         hipLaunchKernelGGL(product_wide_kernel, grid(most(kWideTile, kWideTile), 2), dim3(kWideThreads), 0, stream, a);
         GS_LAUNCH_TRY("product_wide_kernel");
     } else if (rows / experts >= 256 && rows / 256 * ((cols + 255) / 256) >= kUnits) {
-        hipLaunchKernelGGL((product_kernel<256, 256, 2, 4>), grid(most(256, 256), 1), dim3(512), 0, stream, a);
+        hipLaunchKernelGGL((product_kernel<256, 256, 2, 2>), grid(most(256, 256), 1), dim3(256), 0, stream, a);
         GS_LAUNCH_TRY("product_kernel");
     } else {
         hipLaunchKernelGGL((product_kernel<128, 128, 2, 2>), grid(most(128, 128), 2), dim3(256), 0, stream, a);
