@@ -958,6 +958,8 @@ def _held(q, name, device=None):
     if dim < 1:
         raise ValueError(f"{name} must have at least one column")
     blocks, dev = (dim + 127) // 128, q.values.device if device is None else device
+    if not isinstance(q.scales, torch.Tensor) or tuple(q.scales.shape) != lead + (blocks,):
+        raise ValueError(f"{name} scales must have shape {lead + (blocks,)}")
     pv = _arg(q.values, f"{name} values", torch.float8_e4m3fn, dev, lead + (blocks * 128,))
     return dev, lead, dim, pv, _arg(q.scales, f"{name} scales", torch.uint8, dev, lead + (blocks,))
 
