@@ -210,7 +210,7 @@ __device__ __forceinline__ int turn_of(int row) { return ((row >> 1) ^ (row >> 3
 // rows; four stages are in LDS, loaded without registers in between while the products of the one before run.
 // An operand's registers are filled with the next stage's as soon as its last product of this one has begun.
 template <int BM, int BN, int WR, int WC>
-__global__ __launch_bounds__(WR *WC *kWave, BM <= 128 ? 2 : 1) void product_kernel(ProductArgs a) {
+__global__ __launch_bounds__(WR *WC *kWave, BM <= 64 ? 4 : BM <= 128 ? 2 : 1) void product_kernel(ProductArgs a) {
     constexpr int kStages = 4, kRows = BM + BN, kWaves = WR * WC, kThreads = kWaves * kWave;
     constexpr int FR = BM / 32 / WR, FC = BN / 32 / WC;
     static_assert(FR * WR * 32 == BM && FC * WC * 32 == BN, "whole results");
@@ -355,32 +355,37 @@ __global__ __launch_bounds__(kWideThreads, 2) void product_wide_kernel(ProductAr
     const int64_t tiles = row_tiles * col_tiles;
     const int my_row = threadIdx.x / 2, my_half = threadIdx.x % 2;  // 32 columns of a row of x and of one of the weight
     for (int64_t turn = 0; turn < tiles; turn += gridDim.x) {
-        Place at;
-        if (!place_of(turn, tiles, row_tiles, col_tiles, at)) return;
-        const Run run = find_tile(a, kWideTile, at.row_tile);
-        const int col0 = static_cast<int>(at.col_tile) * kWideTile;
+        Place place;
+        if (!place_of(turn, tiles, row_tiles, col_tiles, place)) return;
+        const Run run = find_tile(a, kWideTile, place.row_tile);
+        const int col0 = static_cast<int>(place.col_tile) * kWideTile;
         f32x16 acc[2][2] = {};
         if (run.expert < a.experts) {
             const int64_t r = x_row(a, run, my_row), n = w_row(a, run, col0 + my_row);
             const uint8_t *x = a.x + r * depth + my_half * 32, *w = a.w + n * depth + my_half * 32;
             const uint8_t *xs = a.x_scales + r * a.blocks, *ws = a.w_scales + n * a.blocks;
-            u32x4 held[2][2];
-            float step[2];
-            const auto load = [&](int stage) {
+            u32x4 held[2][2][2];  // two stages on their way
+            int step[2][2];
+            const int stages = a.blocks * 2;
+            const auto load = [&](int stage, int at) {
+                stage = stage < stages ? stage : stages - 1;  // past the end the last one again, unused
                 const int64_t col = static_cast<int64_t>(stage) * kStep;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    held[0][k] = *reinterpret_cast<const u32x4 *>(x + col + k * 16);
-                    held[1][k] = *reinterpret_cast<const u32x4 *>(w + col + k * 16);
+                    held[at][0][k] = *reinterpret_cast<const u32x4 *>(x + col + k * 16);
+                    held[at][1][k] = *reinterpret_cast<const u32x4 *>(w + col + k * 16);
                 }
-                step[0] = f8_step(xs[stage / 2]);
-                step[1] = f8_step(ws[stage / 2]);
+                step[at][0] = xs[stage / 2];
+                step[at][1] = ws[stage / 2];
             };
-            const int stages = a.blocks * 2;
             __syncthreads();  // the last tile's operands are read
-            load(0);
-            for (int stage = 0; stage < stages; ++stage) {
-                uint8_t *planes = s_stages + stage % 2 * kStage;
+            load(0, 0);
+            load(1, 1);
+            for (int pair = 0; pair < stages; pair += 2)
+#pragma unroll
+            for (int at = 0; at < 2; ++at) {
+                const int stage = pair + at;
+                uint8_t *planes = s_stages + at * kStage;
 #pragma unroll
                 for (int op = 0; op < 2; ++op)
 #pragma unroll
@@ -389,10 +394,12 @@ __global__ __launch_bounds__(kWideThreads, 2) void product_wide_kernel(ProductAr
                         for (int h = 0; h < 2; ++h)
                             *reinterpret_cast<bf16x8 *>(planes + op * (kStage / 2) +
                                                         wide_at(my_row, my_half * 4 + k * 2 + h)) =
-                                widen8(held[op][k][2 * h], held[op][k][2 * h + 1], step[op]);
+                                widen8(held[at][op][k][2 * h], held[at][op][k][2 * h + 1],
+                                       f8_step(step[at][op]));
                     }
                 __syncthreads();
-                if (stage + 1 < stages) load(stage + 1);
+                load(stage + 2, at);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int deep = 0; deep < kStep / 16; ++deep) {
                     bf16x8 frag[2][2];
@@ -471,6 +478,9 @@ extern "C" gs_status gs_expert_product(const void *x, const void *x_scales, cons
         GS_LAUNCH_TRY("product_wide_kernel");
     } else if (rows / experts >= 256 && rows / 256 * ((cols + 255) / 256) >= kUnits) {
         hipLaunchKernelGGL((product_kernel<256, 256, 2, 2>), grid(most(256, 256), 1), dim3(256), 0, stream, a);
+        GS_LAUNCH_TRY("product_kernel");
+    } else if (rows / 128 * ((cols + 127) / 128) < 2 * kUnits) {
+        hipLaunchKernelGGL((product_kernel<64, 64, 2, 2>), grid(most(64, 64), 4), dim3(256), 0, stream, a);
         GS_LAUNCH_TRY("product_kernel");
     } else {
         hipLaunchKernelGGL((product_kernel<128, 128, 2, 2>), grid(most(128, 128), 2), dim3(256), 0, stream, a);

@@ -336,7 +336,15 @@ __global__ __launch_bounds__(kThreads) void weight_grad_join_kernel(GradArgs a, 
         if (i >= size) continue;
         const float *from = parts + first * size + i;
         float s = 0.0f;
-        for (int64_t k = 0; k < count; ++k) s += from[k * size];
+        int64_t k = 0;
+        for (; k + 8 <= count; k += 8) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = from[(k + j) * size];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += v[j];
+        }
+        for (; k < count; ++k) s += from[k * size];
         out[expert * size + i] = s;
     }
 }
@@ -357,7 +365,10 @@ Parts parts_for(int64_t rows, int experts, int64_t dim, int64_t cols) {
     const int64_t all = rows > 0 ? rows : 1;
     if (cols >= 8 && experts * tiles_of(dim, cols, kLarge) >= 2 * kUnits) return {all, experts, kLarge, false};
     const int64_t tiles = tiles_of(dim, cols, kSmall);
-    const int64_t want = 4 * kUnits / tiles;  // parts in all, for four tiles a compute unit
+    // the parts' tiles fill the chip once (two workgroups a unit), each expert's last part being a shorter one; twice
+    // where that leaves fewer parts than experts
+    int64_t want = 2 * kUnits / tiles - experts;
+    if (want < experts) want = 4 * kUnits / tiles - experts;
     int64_t chunk = want > 0 ? (rows + want - 1) / want : rows;
     chunk = (chunk + kDeep - 1) / kDeep * kDeep;
     chunk = chunk < 8 * kDeep ? 8 * kDeep : chunk;
