@@ -2,6 +2,9 @@
 //
 // A power of two costs no bits (e4m3 rounds relative to the value, whatever the scale) and is what the matrix cores apply
 // by themselves. A block's largest magnitude is exact, so is the division by its scale: each value is rounded once.
+//
+// Bound by memory: 65536 x 4096 bf16 held in 153 us and restored in 129 (5.3 and 6.3 TB/s, part of it from the last-level
+// cache); the smallest calls are a launch of 4 us.
 #include "gs_f8.hpp"
 
 namespace gs {

@@ -5,6 +5,10 @@
 // once: the largest gives the softmax, K rounds of the largest that is left give the choices. Each lane counts its own
 // experts' choices and sums their probabilities over all tokens of its workgroup in registers; the workgroups' sums go to
 // a workspace and a second kernel adds them in a fixed order, in float64. A single workgroup (few tokens) finishes alone.
+//
+// 1000000 x 8 float32, 2 choices: 19.5 us (2.5 TB/s: a token a lane, so rounds of comparisons, exponentials and stores of
+// 8 bytes a token fill the time) and 5.1 for the second kernel; the gradient of 32768 x 64, 8 choices 8.7 us (2.3 TB/s).
+// Eight lanes a token instead took 99 us with the second kernel, 64 lanes the gradient 30: values crossed lanes by LDS.
 #include <type_traits>
 
 #include "gs_types.hpp"
