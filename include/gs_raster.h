@@ -510,7 +510,8 @@ gs_status gs_dequantize(const void *values, const void *scales, int64_t rows, in
  * x values and scales of [x_rows, dim]; weight of [experts, cols, dim]; out [rows, cols] of dtype. offsets as
  * gs_expert_plan wrote them, or NULL: one expert has all rows. pairs NULL: x holds the sorted rows, x_rows = rows. pairs
  * as gs_expert_plan wrote them: x holds the tokens, rows = x_rows * choices, and row r is token pairs[r] / choices.
- * A byte 255 of scales makes its block NaN. Offsets and pairs out of range are taken to its ends.
+ * Bytes 0 and 255 stand for no scale (gs_quantize writes neither): results of their blocks are not defined. Offsets and
+ * pairs out of range are taken to its ends.
  * Limits: 0 <= rows < 2^31, 1 <= dim, cols < 2^31, 1 <= experts <= 4096. Asynchronous.
  */
 gs_status gs_expert_product(const void *x, const void *x_scales, const void *weight, const void *weight_scales,
