@@ -1031,7 +1031,9 @@ def gs_expert_product(x, weight, plan=None, gather=False, relu=False, dtype=torc
     the plan's kept ones; relu=True: max(0, .).
 
     x: Quantized rows in the plan's order, [tokens * choices, dim], or with gather=True the tokens themselves,
-    [tokens, dim]. weight: Quantized [experts, cols, dim]. plan=None: one weight [cols, dim] for all rows."""
+    [tokens, dim]. weight: Quantized [experts, cols, dim]. plan=None: one weight [cols, dim] for all rows. float32 results
+    are summed in float32; for 16-bit ones the products of each 8 neighbours along dim are first cut off 2^-13 below the
+    largest of them, so that results of large products that cancel keep fewer bits."""
     lib = load_library()
     dev, lead, dim, px, pxs = _held(x, "x")
     rows, x_rows, K, E, po, pp = _plan_rows(lead, plan, gather, dev)
