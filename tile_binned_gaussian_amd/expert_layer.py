@@ -126,8 +126,9 @@ class ExpertLayer(_Momentum):
 
     def _backward_held(self, s, grad_y):
         """The experts' results are formed again from the hidden values kept. Gradients of 8-bit values are those of the
-        values that they stand for; the output gradients of both products are held in 8 bits too, for the gradients of
-        their inputs."""
+        values that they stand for (a hidden value that rounds to 0 passes none on); the output gradients of both products
+        are held in 8 bits too, for the gradients of their inputs. The router's logits are of the tokens themselves, and so
+        is its weight's gradient: they are normalised again."""
         p, t = self.parameters, s.x.dtype
         rows = binding.gs_expert_product(s.hidden, s.weights.down, s.plan, dtype=t)
         combine = binding.gs_expert_combine_bwd(rows, s.plan, s.route.weights, grad_y)
@@ -138,7 +139,8 @@ class ExpertLayer(_Momentum):
         grads["up"] = binding.gs_expert_weight_grad(s.tokens, grad_hidden, s.plan, gather=True)
         grad_sent = binding.gs_expert_product(binding.gs_quantize(grad_hidden), s.weights.up_back, s.plan, dtype=t)
         grad_logits = binding.gs_expert_route_bwd(s.logits, s.route, combine.weights, self._grad_loss)
-        grads["router"] = binding.gs_expert_weight_grad(s.tokens, grad_logits)
+        again = binding.gs_layer_norm_fwd(s.x, p["norm_weight"], p["norm_bias"], stats=False)
+        grads["router"] = again.y.float().t() @ grad_logits
         grad_norm = binding.gs_expert_combine(grad_sent, s.plan).float() + grad_logits @ p["router"].t()
         norm = binding.gs_layer_norm_bwd(s.x, p["norm_weight"], s.mean, s.rstd, grad_norm.to(t))
         grads["norm_weight"], grads["norm_bias"] = norm.weight, norm.bias
