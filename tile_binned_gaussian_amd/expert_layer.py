@@ -51,8 +51,8 @@ class _Saved:
     sent: torch.Tensor
     hidden: torch.Tensor  # the experts' hidden values after the rectifier, in sorted rows
     rows: torch.Tensor  # the experts' results, in sorted rows
-    logits: torch.Tensor
-    route: binding.ExpertRoute | None  # with a balance loss
+    logits: torch.Tensor | None  # with a balance loss, as the route
+    route: binding.ExpertRoute | None
 
 
 @dataclass
@@ -79,7 +79,8 @@ class _SavedHeld:
 
 class ExpertLayer(_Momentum):
     """products: "library" or "f8". balance: the weight of the balance loss, whose gradient the backward adds to that of
-    the result; the forward's loss is saved.route.loss."""
+    the result; the forward's loss is then saved.route.loss (library products without a balance loss route in plain torch
+    operations: saved.route is None)."""
 
     def __init__(self, dim, hidden, experts, choices, seed=0, device="cuda", dtype=torch.bfloat16, products="library",
                  balance=0.0):
@@ -170,7 +171,7 @@ class ExpertLayer(_Momentum):
         hidden = self._of_experts(sent, p["up"].to(x.dtype), bounds, x.new_empty(T * K, self.hidden)).relu_()
         rows = self._of_experts(hidden, p["down"].to(x.dtype), bounds, torch.empty_like(sent))
         y = x + binding.gs_expert_combine(rows, plan, weights)
-        return y, _Saved(x, norm, plan, bounds, ids, weights, sent, hidden, rows, logits, route)
+        return y, _Saved(x, norm, plan, bounds, ids, weights, sent, hidden, rows, None if route is None else logits, route)
 
     def backward(self, s, grad_y):
         """(gradient of x, gradients of the parameters by name) of sum(grad_y * y) + balance * balance loss."""
