@@ -630,9 +630,15 @@ def _int32(v, name):
     return v
 
 
-def _stream_int(stream):
+def _stream_int(stream, device):
+    """The stream's handle. It has to be one of the tensors' device: a kernel on another one would read memory that is
+    not its own, in no order with the work that fills it."""
+    current = torch.cuda.current_device()  # a given stream's, where there is one
+    if device.index != current:
+        raise ValueError(f"the tensors are on {device}, the call's stream is on cuda:{current}: make theirs the "
+                         "current device or pass one of its streams")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(current)
     return stream.cuda_stream
 
 
@@ -694,7 +700,7 @@ def gs_layer_norm_fwd(x, weight, bias=None, eps=1e-5, stats=True, out=None, stre
         if out.mean is not None:
             pm = _arg(out.mean, "mean", torch.float32, dev, shape)
             pr = _arg(out.rstd, "rstd", torch.float32, dev, shape)
-    _check(lib.gs_layer_norm_fwd(px, pw, pb, rows, dim, eps, code, wcode, py, pm, pr, _stream_int(stream)))
+    _check(lib.gs_layer_norm_fwd(px, pw, pb, rows, dim, eps, code, wcode, py, pm, pr, _stream_int(stream, dev)))
     return out
 
 
@@ -726,7 +732,7 @@ def gs_layer_norm_bwd(x, weight, mean, rstd, grad_y, grad_bias=True, out=None, s
     ws, pws, room = _room(lib.gs_layer_norm_bwd_workspace_bytes(rows, dim), dev) if workspace is None \
         else _given_room(workspace, dev)
     _check(lib.gs_layer_norm_bwd(px, pw, pm, pr, pg, rows, dim, code, wcode, ox, ow, ob, pws, room,
-                                 _stream_int(stream)))
+                                 _stream_int(stream, dev)))
     return out
 
 
@@ -771,7 +777,7 @@ def gs_expert_plan(ids, experts, out=None, stream=None, workspace=None) -> Exper
         pr, pp = _arg(out.rows, "rows", torch.int32, dev, (T, K)), _arg(out.pairs, "pairs", torch.int32, dev, (T * K,))
     ws, pws, room = _room(lib.gs_expert_plan_workspace_bytes(T, K, E), dev) if workspace is None \
         else _given_room(workspace, dev)
-    _check(lib.gs_expert_plan(pi, T, K, E, po, pr, pp, pws, room, _stream_int(stream)))
+    _check(lib.gs_expert_plan(pi, T, K, E, po, pr, pp, pws, room, _stream_int(stream, dev)))
     return out
 
 
@@ -789,7 +795,7 @@ def gs_expert_dispatch(x, plan, out=None, stream=None):
         out = x.new_empty((T * K, D))
     else:
         _arg(out, "sent", x.dtype, dev, (T * K, D))
-    _check(lib.gs_expert_dispatch(px, po, pr, T, K, E, D, code, out.data_ptr(), _stream_int(stream)))
+    _check(lib.gs_expert_dispatch(px, po, pr, T, K, E, D, code, out.data_ptr(), _stream_int(stream, dev)))
     return out
 
 
@@ -813,7 +819,7 @@ def gs_expert_combine(source, plan, weights=None, out=None, stream=None):
         out = source.new_empty((T, D))
     else:
         _arg(out, "y", source.dtype, dev, (T, D))
-    _check(lib.gs_expert_combine(ps, pr, pw, T, K, D, code, out.data_ptr(), _stream_int(stream)))
+    _check(lib.gs_expert_combine(ps, pr, pw, T, K, D, code, out.data_ptr(), _stream_int(stream, dev)))
     return out
 
 
@@ -840,7 +846,7 @@ def gs_expert_combine_bwd(source, plan, weights, grad_y, out=None, stream=None) 
         _arg(out.rows, "grad_rows", source.dtype, dev, (T * K, D))
         _arg(out.weights, "grad_weights", torch.float32, dev, (T, K))
     _check(lib.gs_expert_combine_bwd(ps, po, pr, pw, pg, T, K, E, D, code, out.rows.data_ptr(),
-                                     out.weights.data_ptr(), _stream_int(stream)))
+                                     out.weights.data_ptr(), _stream_int(stream, dev)))
     return out
 
 
@@ -864,7 +870,7 @@ def gs_orthogonalize(update, steps=5, coefficients=(3.4445, -4.7750, 2.0315), ep
     ws, pws, room = _room(lib.gs_orthogonalize_workspace_bytes(B, m, n), dev) if workspace is None \
         else _given_room(workspace, dev)
     _check(lib.gs_orthogonalize(pu, B, m, n, steps, a, b, c, eps, code, out.data_ptr(), pws, room,
-                                _stream_int(stream)))
+                                _stream_int(stream, dev)))
     return out
 
 
@@ -913,7 +919,7 @@ def gs_expert_route(logits, choices, mask=None, renormalize=True, out=None, stre
               _arg(out.loss, "loss", torch.float32, dev, ()), _arg(out.kept, "kept", torch.int32, dev, (1,))]
     ws, pws, room = _room(lib.gs_expert_route_workspace_bytes(T, E), dev) if workspace is None \
         else _given_room(workspace, dev)
-    _check(lib.gs_expert_route(pl, pm, T, E, K, int(bool(renormalize)), code, *po, pws, room, _stream_int(stream)))
+    _check(lib.gs_expert_route(pl, pm, T, E, K, int(bool(renormalize)), code, *po, pws, room, _stream_int(stream, dev)))
     return out
 
 
@@ -933,7 +939,7 @@ def gs_expert_route_bwd(logits, route, grad_weights=None, grad_loss=None, renorm
     else:
         _arg(out, "grad_logits", logits.dtype, dev, (T, E))
     _check(lib.gs_expert_route_bwd(pl, pi, pw, pc, pk, pg, ps, T, E, K, int(bool(renormalize)), code, out.data_ptr(),
-                                   _stream_int(stream)))
+                                   _stream_int(stream, dev)))
     return out
 
 
@@ -989,7 +995,7 @@ def gs_quantize(x, transpose=False, out=None, stream=None) -> Quantized:
         _, got, got_dim, pv, ps = _held(out, "out", dev)
         if got != tuple(lead) or got_dim != along:
             raise ValueError(f"out must hold {tuple(lead) + (along,)} (got {got + (got_dim,)})")
-    _check(lib.gs_quantize(px, batch, rows, dim, int(bool(transpose)), code, pv, ps, _stream_int(stream)))
+    _check(lib.gs_quantize(px, batch, rows, dim, int(bool(transpose)), code, pv, ps, _stream_int(stream, dev)))
     return out
 
 
@@ -1005,7 +1011,7 @@ def gs_dequantize(q, dtype=torch.float32, out=None, stream=None):
     else:
         _arg(out, "out", dtype, dev, lead + (dim,))
     _check(lib.gs_dequantize(pv, ps, q.scales.numel() // q.scales.shape[-1], dim, _DTYPES[dtype], out.data_ptr(),
-                                _stream_int(stream)))
+                                _stream_int(stream, dev)))
     return out
 
 
@@ -1048,7 +1054,7 @@ def gs_expert_product(x, weight, plan=None, gather=False, relu=False, dtype=torc
     else:
         _arg(out, "out", dtype, dev, (rows, cols))
     _check(lib.gs_expert_product(px, pxs, pw, pws, po, pp, rows, x_rows, K, E, dim, cols, int(bool(relu)),
-                                    _DTYPES[dtype], out.data_ptr(), _stream_int(stream)))
+                                    _DTYPES[dtype], out.data_ptr(), _stream_int(stream, dev)))
     return out
 
 
@@ -1072,5 +1078,5 @@ def gs_expert_weight_grad(x, grad, plan=None, gather=False, out=None, stream=Non
     ws, pws, room = _room(lib.gs_expert_weight_grad_workspace_bytes(rows, E, dim, cols), dev) if workspace is None \
         else _given_room(workspace, dev)
     _check(lib.gs_expert_weight_grad(px, pxs, pg, po, pp, rows, x_rows, K, E, dim, cols, code, out.data_ptr(), pws,
-                                        room, _stream_int(stream)))
+                                        room, _stream_int(stream, dev)))
     return out
