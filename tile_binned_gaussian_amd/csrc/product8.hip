@@ -186,7 +186,7 @@ __device__ __forceinline__ void store_rows(const ProductArgs &a, const Run &run,
 template <int FR, int FC>
 __device__ __forceinline__ void store_tile(const ProductArgs &a, const Run &run, const f32x16 (&acc)[FR][FC], int row0,
                                            int col0) {
-    const bool whole = col0 + FC * 32 <= a.cols;
+    const bool whole = a.cols - col0 >= FC * 32;
     if (a.out_type == GS_F32) {
         if (whole) store_rows<float, true>(a, run, acc, row0, col0);
         else store_rows<float, false>(a, run, acc, row0, col0);
@@ -233,7 +233,8 @@ __global__ __launch_bounds__(WR *WC *kWave, BM <= 64 ? 4 : BM <= 128 ? 2 : 1) vo
     const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) uint8_t *)s_ring));
     const int64_t depth = static_cast<int64_t>(a.blocks) * kF8Block;
-    const int64_t col_tiles = (a.cols + BN - 1) / BN, row_tiles = count_tiles(a, BM), tiles = row_tiles * col_tiles;
+    const int64_t col_tiles = (int64_t{a.cols} + BN - 1) / BN, row_tiles = count_tiles(a, BM);
+    const int64_t tiles = row_tiles * col_tiles;
     // this lane's part of a fragment of 32 rows: bytes [32 half, 32 half + 32) of row lane % 32
     const int first = lane % 32 * kStep + ((lane / 32 * 2) ^ turn_of(lane % 16)) * 16;
 
@@ -357,7 +358,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void product_wide_kernel(ProductAr
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
     const int wr = wave / 2, wc = wave % 2;
     const int64_t depth = static_cast<int64_t>(a.blocks) * kF8Block;
-    const int64_t col_tiles = (a.cols + kWideTile - 1) / kWideTile, row_tiles = count_tiles(a, kWideTile);
+    const int64_t col_tiles = (int64_t{a.cols} + kWideTile - 1) / kWideTile, row_tiles = count_tiles(a, kWideTile);
     const int64_t tiles = row_tiles * col_tiles;
     const int my_row = threadIdx.x / 2, my_half = threadIdx.x % 2;  // 32 columns of a row of x and of one of the weight
     for (int64_t turn = 0; turn < tiles; turn += gridDim.x) {

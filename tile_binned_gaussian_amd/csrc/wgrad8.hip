@@ -129,8 +129,8 @@ __global__ __launch_bounds__(kThreads, F == 2 ? 2 : 1) void weight_grad_kernel(G
     __shared__ int64_t s_rows[kSegment];  // first blocks of the rows of x
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
     const int wr = wave / 2, wc = wave % 2;
-    const int64_t down = (a.dim + kTile - 1) / kTile, across = (a.cols + kTile - 1) / kTile, each = down * across;
-    const int64_t tiles = items * each;
+    const int64_t down = (int64_t{a.dim} + kTile - 1) / kTile, across = (int64_t{a.cols} + kTile - 1) / kTile;
+    const int64_t each = down * across, tiles = items * each;
     const int my_row = threadIdx.x / 8, my_col = threadIdx.x % 8 * 16;  // and 128 on
     const int my_place = chunk_at<kTile>(my_row, threadIdx.x % 8 * 2);
     // a transposing load: lane p of 16 reads 4 of the 16 columns of row p / 4
@@ -307,7 +307,7 @@ __global__ __launch_bounds__(kThreads, F == 2 ? 2 : 1) void weight_grad_kernel(G
         // one pointer that walks the lane's results, so that no address is kept from before
         const int n1 = n0 + wc * F * 32 + lane % 32, d1 = d0 + wr * F * 32 + lane / 32 * 4;
         float *to = out + static_cast<int64_t>(d1) * a.cols + n1;
-        const bool inside = d0 + kTile <= a.dim && n0 + kTile <= a.cols;
+        const bool inside = a.dim - d0 >= kTile && a.cols - n0 >= kTile;
 #pragma unroll
         for (int i = 0; i < F; ++i)
 #pragma unroll
