@@ -16,11 +16,12 @@ CALIB_SOURCES = [os.path.join(HERE, "csrc", "calib", "valu_calib.hip")]
 HEADERS = sorted(glob.glob(os.path.join(HERE, "csrc", "*.hpp"))) + [os.path.join(ROOT, "include", "gs_raster.h")]
 
 # -ffp-contract=off: the composite's float32 operation order is part of its definition (no fused multiply-adds
-# except the ones the source writes). Packed FP32 instructions are disabled for the whole library.
+# except the ones the source writes). Packed FP32 instructions are disabled for the whole library. -Werror=pass-failed: a
+# loop that asks to be unrolled and is not keeps what it indexes in memory instead of registers.
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-ffp-contract=off",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    "-Wall", "-Wno-unused-result",
+    "-Wall", "-Wno-unused-result", "-Werror=pass-failed",
 ]
 
 

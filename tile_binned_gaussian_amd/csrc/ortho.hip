@@ -779,7 +779,6 @@ __device__ __forceinline__ void small_step(f32x16 (&x)[kSmallTurns], int col_blo
         const int blocks = col_blocks * 2, to = blocks * (part + 1) / kParts;
         const int across = l.across + l.half * col_blocks * kBlock, across4 = across ^ 32;
         const int pi = ti * 2 * col_blocks * kBlock, pj = tj * 2 * col_blocks * kBlock;
-#pragma unroll 2
         for (int k = blocks * part / kParts; k < to; ++k) {
             const h16x8 ph = small_operand_turned(xh + pi, k, across, across4);
             const h16x8 qh = small_operand_turned(xh + pj, k, across, across4);

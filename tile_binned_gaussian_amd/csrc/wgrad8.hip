@@ -10,6 +10,8 @@
 // 16384 tokens, 2 choices of 16 experts, 4096 x 4096 bf16 1175 to 1236 us: 1.1 to 1.2 PFLOP/s inside a tile (a bfloat16
 // library product of one such matrix 1.38), and 18 us a tile for its start and its 256 KB of results, during which its unit
 // has no other. 200000 tokens, 2 of 8, 128 x 256 bf16: 50 us at 4.5 TB/s and 8.5 for the parts' join.
+#include <utility>
+
 #include "gs_f8.hpp"
 
 namespace gs {
@@ -116,9 +118,20 @@ __device__ __forceinline__ void split8(const V *packs, bf16x8 (&out)[P]) {
     }
 }
 
-// One tile of one part: 4 waves of 32 F x 32 F results. A step's rows go from memory to registers two steps ahead, from
-// there as bfloat16 to LDS one step ahead. CUT: rows of
-// grad end inside a pack. NARROW: they are shorter than one.
+// f(0) to f(N - 1), each with its number as a constant: the compiler's own unrolling gives up on a step as long as that of
+// a large tile of float32 rows that end inside a pack, and what it does not unroll keeps its accumulators in memory
+// (16 x 2048 rows 4096 x 4095: 132 ms, so 4.1).
+template <int... I, typename F>
+__device__ __forceinline__ void unrolled(std::integer_sequence<int, I...>, const F &f) {
+    (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(const F &f) {
+    unrolled(std::make_integer_sequence<int, N>(), f);
+}
+
+// One tile of one part: 4 waves of 32 F x 32 F results. A step's rows go as bfloat16 to LDS kAhead steps ahead, and from
+// memory to registers one step before that. CUT: rows of grad end inside a pack. NARROW: they are shorter than one.
 template <typename T, int F, bool CUT, bool NARROW>
 __global__ __launch_bounds__(kThreads, F == 2 ? 2 : 1) void weight_grad_kernel(GradArgs a, int64_t items) {
     constexpr int P = kPlanes<T>, kTile = 64 * F, kRuns = F / 2;  // columns of a tile; a thread's runs of 16 of a row
@@ -243,7 +256,7 @@ __global__ __launch_bounds__(kThreads, F == 2 ? 2 : 1) void weight_grad_kernel(G
             // A step is 2 P phases: 16 rows and one plane of grad each, the smallest plane first. Operand r of a phase: the
             // plane's, and where the rows are new x's.
             constexpr int kPhases = 2 * P;
-            const auto operands = [](int phase) { return phase % P == 0 ? 2 * F : F; };
+            constexpr auto operands = [](int phase) { return phase % P == 0 ? 2 * F : F; };
             const auto fetch = [&](const uint8_t *planes, int phase, int r) {
                 const int deep = phase / P * 16, q = P - 1 - phase % P;
                 if (r < F) n[phase % 2][r] = operand(planes + (1 + q) * kPlaneBytes, wc * 2 * F + r * 2, deep);
@@ -259,28 +272,24 @@ __global__ __launch_bounds__(kThreads, F == 2 ? 2 : 1) void weight_grad_kernel(G
                 constexpr int M = F * F;
                 __syncthreads();
                 if constexpr (kAhead == 1) fetch_all(now, 0);
+                unrolled<kPhases * M>([&](auto turn) {
+                    constexpr int phase = turn / M, m = turn % M, i = m / F, k = m % F;
+                    constexpr bool last = phase + 1 == kPhases;
+                    constexpr int reads = !last ? operands(phase + 1) : kAhead == 2 ? operands(0) : 0;
+                    // the reads end early enough to be done at the next phase
 #pragma unroll
-                for (int phase = 0; phase < kPhases; ++phase) {
-                    const bool last = phase + 1 == kPhases;
-                    const int reads = !last ? operands(phase + 1) : kAhead == 2 ? operands(0) : 0;
+                    for (int r = m * reads * 4 / (M * 3); r < (m + 1) * reads * 4 / (M * 3) && r < reads; ++r)
+                        fetch(last ? next : now, last ? 0 : phase + 1, r);
+                    acc[i][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d[phase / P % 2][i], n[phase % 2][k], acc[i][k],
+                                                                        0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (phase == 0 && m % (M / 4) == 0 && m / (M / 4) < kRuns) load(1 - at, m / (M / 4));
+                    if (phase == 0 && m == M * 3 / 4) seek(first + (kAhead + 2) * kDeep);
+                    if (last)
 #pragma unroll
-                    for (int m = 0; m < M; ++m) {
-                        // the reads end early enough to be done at the next phase
-#pragma unroll
-                        for (int r = m * reads * 4 / (M * 3); r < (m + 1) * reads * 4 / (M * 3) && r < reads; ++r)
-                            fetch(last ? next : now, last ? 0 : phase + 1, r);
-                        const int i = m / F, k = m % F;
-                        acc[i][k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d[phase / P % 2][i], n[phase % 2][k],
-                                                                            acc[i][k], 0, 0, 0);
-                        __builtin_amdgcn_sched_barrier(0);
-                        if (phase == 0 && m % (M / 4) == 0 && m / (M / 4) < kRuns) load(1 - at, m / (M / 4));
-                        if (phase == 0 && m == M * 3 / 4) seek(first + (kAhead + 2) * kDeep);
-                        if (last)
-#pragma unroll
-                            for (int piece = m * kPieces / M; piece < (m + 1) * kPieces / M; ++piece)
-                                keep(first + kAhead * kDeep, at, after, piece);
-                    }
-                }
+                        for (int piece = m * kPieces / M; piece < (m + 1) * kPieces / M; ++piece)
+                            keep(first + kAhead * kDeep, at, after, piece);
+                });
             };
             load_all(kDeep, 0);
             load_all(2 * kDeep, 1);
@@ -291,10 +300,11 @@ __global__ __launch_bounds__(kThreads, F == 2 ? 2 : 1) void weight_grad_kernel(G
                 __syncthreads();
                 fetch_all(s_planes, 0);
             }
-            // six steps a turn: registers two deep and LDS kAhead + 1 deep are then the same in every turn
+            // so many steps a turn that registers two deep and LDS kAhead + 1 deep are then the same in every turn
+            constexpr int kSteps = kAhead == 2 ? 6 : 2;
             for (int first = 0; first < count;) {
 #pragma unroll
-                for (int u = 0; u < 6; ++u) {
+                for (int u = 0; u < kSteps; ++u) {
                     constexpr int kPlaces = kAhead + 1;
                     work(first, (u + kAhead) % 2, s_planes + u % kPlaces * kBytes,
                          s_planes + (u + 1) % kPlaces * kBytes, s_planes + (u + kAhead) % kPlaces * kBytes);
