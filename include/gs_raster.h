@@ -507,7 +507,9 @@ gs_status gs_dequantize(const void *values, const void *scales, int64_t rows, in
 /* Products of rows sorted by expert with the experts' weights, both held in 8 bits along the sum's axis:
  *   out[r, n] = sum_k x[r, k] * weight[e, n, k] for the rows [offsets[e], offsets[e + 1]) of expert e;
  *   relu != 0: max(0, .) of it; the rows from offsets[experts] on become zeros.
- * float32 results: exact products, summed in float32. 16-bit results: the products of each 8 neighbours along k (k / 8 the
+ * float32 results: exact products, summed in float32, of both operands as bfloat16: they are exact as that but for numbers
+ * that are no multiples of 2^-133 (scale bytes 1 and 2), which are rounded to those, and numbers beyond its largest, which
+ * become it (bytes from 247 on; of gs_quantize's, inputs of 3.3e38 and more). 16-bit results: the products of each 8 neighbours along k (k / 8 the
  * same) are cut off 2^-13 below the power of two of their largest before they are summed in float32. That is at most
  * 7 * 2^-13 of that product (2^-16 of a typical result), beside half steps of 2^-8 (bfloat16) and 2^-11 (float16) of the
  * result: where large products cancel, or float16's last bit counts, take float32 results.
@@ -526,7 +528,8 @@ gs_status gs_expert_product(const void *x, const void *x_scales, const void *wei
 /* Gradient of the experts' weights, with the activations held in 8 bits:
  *   out[e, k, n] = sum over the rows r of expert e of x[r, k] * grad[r, n], in float32; zeros for an expert without rows.
  * x, offsets, pairs, rows, x_rows and choices as in gs_expert_product; grad [rows, cols] of dtype, whose rows from
- * offsets[experts] on are not read; out [experts, dim, cols] float32. Every product is exact.
+ * offsets[experts] on are not read; out [experts, dim, cols] float32. Every product is exact for x as bfloat16, as for
+ * gs_expert_product's float32 results, and grad; but of a float32 grad, what lies below 2^-133 is cut off.
  * workspace: gs_expert_weight_grad_workspace_bytes(rows, experts, dim, cols) bytes (0 for sizes out of range and where
  * the experts' matrices alone fill the chip). Limits as gs_expert_product's. Asynchronous.
  */

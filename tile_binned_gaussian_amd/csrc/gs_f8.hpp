@@ -43,7 +43,10 @@ __device__ __forceinline__ uint32_t f8_pack(float a, float b, float c, float d, 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// 8 held values as bfloat16, which loses nothing: e4m3 has 4 bits and the scale none.
+// 8 held values as bfloat16. That loses nothing (e4m3 has 4 bits and the scale none) of multiples of 2^-133, which those of
+// scale bytes from 3 on are; smaller multiples are rounded to one of 2^-133. From kF8Beyond on a value may be beyond
+// bfloat16's largest: rounding up makes one of a finite value next to it.
+constexpr int kF8Beyond = 247;
 __device__ __forceinline__ bf16x8 widen8(uint32_t first, uint32_t second, float step) {
     bf16x8 out;
 #pragma unroll
@@ -55,6 +58,18 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t first, uint32_t second, float 
         out[2 * k + 1] = two[1];
     }
     return out;
+}
+
+// The largest in place of infinities, as where a value is restored: an infinity would make NaN of every zero that it meets.
+// NaN stays.
+__device__ __forceinline__ bf16x8 finite8(bf16x8 v) {
+    u32x4 bits = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if ((bits[k] & 0x7fffu) == 0x7f80u) --bits[k];
+        if ((bits[k] & 0x7fff0000u) == 0x7f800000u) bits[k] -= 0x10000u;
+    }
+    return __builtin_bit_cast(bf16x8, bits);
 }
 
 }  // namespace gs

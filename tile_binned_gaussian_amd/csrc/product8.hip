@@ -12,6 +12,8 @@
 // Bound by the tile's start and end and by the loads' latency: 16384 tokens, 2 choices of 16 experts, 4096 -> 4096 bf16
 // 570 to 610 us, 1.8 PFLOP/s, of which 13 us a tile are spent outside its products; inside them 2.5 PFLOP/s (an 8-bit
 // library product 3.1 to 3.3). Few rows are bound by a tile's chain of stages: 32 rows of 8 experts, 1024 -> 2048, 7.8 us.
+#include <type_traits>
+
 #include "gs_f8.hpp"
 
 namespace gs {
@@ -345,8 +347,8 @@ __global__ __launch_bounds__(WR *WC *kWave, BM <= 64 ? 4 : BM <= 128 ? 2 : 1) vo
 }
 
 // The same for float32 results, beside whose half step of 2^-24 the 8-bit instructions' cut is large. So here both operands
-// become bfloat16 on their way to LDS, which loses nothing (e4m3 has 4 bits, the scale none), and the bfloat16
-// instructions' products are summed in float32. Half the rate.
+// become bfloat16 on their way to LDS, which loses nothing between 2^-133 and its largest (e4m3 has 4 bits, the scale
+// none), and the bfloat16 instructions' products are summed in float32. Half the rate.
 constexpr int kWideTile = 128, kWideThreads = 256;
 
 // 16 bytes (8 columns of k) of a row of a stage.
@@ -393,17 +395,22 @@ __global__ __launch_bounds__(kWideThreads, 2) void product_wide_kernel(ProductAr
             for (int at = 0; at < 2; ++at) {
                 const int stage = pair + at;
                 uint8_t *planes = s_stages + at * kStage;
+                const auto widen = [&](auto beyond) {
 #pragma unroll
-                for (int op = 0; op < 2; ++op)
+                    for (int op = 0; op < 2; ++op)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                        for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            *reinterpret_cast<bf16x8 *>(planes + op * (kStage / 2) +
-                                                        wide_at(my_row, my_half * 4 + k * 2 + h)) =
-                                widen8(held[at][op][k][2 * h], held[at][op][k][2 * h + 1],
-                                       f8_step(step[at][op]));
-                    }
+                            for (int h = 0; h < 2; ++h) {
+                                const bf16x8 v = widen8(held[at][op][k][2 * h], held[at][op][k][2 * h + 1],
+                                                        f8_step(step[at][op]));
+                                *reinterpret_cast<bf16x8 *>(planes + op * (kStage / 2) +
+                                                            wide_at(my_row, my_half * 4 + k * 2 + h)) =
+                                    beyond ? finite8(v) : v;
+                            }
+                };
+                if (__ballot(step[at][0] >= kF8Beyond || step[at][1] >= kF8Beyond)) widen(std::true_type());
+                else widen(std::false_type());
                 __syncthreads();
                 load(stage + 2, at);
                 __builtin_amdgcn_sched_barrier(0);

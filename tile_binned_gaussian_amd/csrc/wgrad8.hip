@@ -1,9 +1,9 @@
 // Gradient of the experts' weights from activations kept in 8 bits on gfx950:
 // out[e][k][n] = sum over the rows r of expert e of x[r, k] grad[r, n].
 //
-// An e4m3 value times its block's power of two is a bfloat16 without rounding, and float16 and float32 gradients are the
-// sums of two and three bfloat16 (11 and 24 bits), so the products run on the bfloat16 matrix cores and lose nothing; they
-// are summed in float32. The rows are the sum's own axis: both operands lie in LDS as they come, row by row, and the
+// An e4m3 value times its block's power of two is a bfloat16 without rounding (from multiples of 2^-133 to its largest), and
+// float16 and float32 gradients are the sums of two and three bfloat16 (11 bits, and 24 down to 2^-133), so the products run
+// on the bfloat16 matrix cores and lose nothing; they are summed in float32. The rows are the sum's own axis: both operands lie in LDS as they come, row by row, and the
 // transposing LDS load turns them. Few matrices with many rows each are summed in parts of some rows, which a second
 // kernel adds in order.
 //
@@ -239,9 +239,25 @@ __global__ __launch_bounds__(kThreads, F == 2 ? 2 : 1) void weight_grad_kernel(G
                 for (int q = 0; q < P; ++q)
                     *reinterpret_cast<u32x4 *>(to + (1 + q) * kPlaneBytes) = __builtin_bit_cast(u32x4, s[q]) & there;
             };
+            // What this thread kept of x, once more where a block may hold values beyond bfloat16's largest: looked at after
+            // the step, not between its products (5% there)
+            const auto keep_finite = [&](int at, uint8_t *planes) {
+                int most = step[at][0];
+#pragma unroll
+                for (int j = 1; j < kRuns; ++j) most = most > step[at][j] ? most : step[at][j];
+                if (!__ballot(most >= kF8Beyond)) return;
+#pragma unroll
+                for (int j = 0; j < kRuns; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        auto *to = reinterpret_cast<bf16x8 *>(planes + (my_place ^ (h * 16)) + j * 256);
+                        *to = finite8(*to);
+                    }
+            };
             const auto keep_all = [&](int first, int at, uint8_t *planes) {
 #pragma unroll
                 for (int piece = 0; piece < kPieces; ++piece) keep(first, at, planes, piece);
+                keep_finite(at, planes);
             };
             const auto operand = [&](const uint8_t *plane, int unit, int deep) {
                 typedef __attribute__((address_space(3))) s16x4 *LdsPtr;
@@ -290,6 +306,7 @@ __global__ __launch_bounds__(kThreads, F == 2 ? 2 : 1) void weight_grad_kernel(G
                         for (int piece = m * kPieces / M; piece < (m + 1) * kPieces / M; ++piece)
                             keep(first + kAhead * kDeep, at, after, piece);
                 });
+                keep_finite(at, after);
             };
             load_all(kDeep, 0);
             load_all(2 * kDeep, 1);
