@@ -509,10 +509,11 @@ gs_status gs_dequantize(const void *values, const void *scales, int64_t rows, in
  *   relu != 0: max(0, .) of it; the rows from offsets[experts] on become zeros.
  * float32 results: exact products, summed in float32, of both operands as bfloat16: they are exact as that but for numbers
  * that are no multiples of 2^-133 (scale bytes 1 and 2), which are rounded to those, and numbers beyond its largest, which
- * become it (bytes from 247 on; of gs_quantize's, inputs of 3.3e38 and more). 16-bit results: the products of each 8 neighbours along k (k / 8 the
- * same) are cut off 2^-13 below the power of two of their largest before they are summed in float32. That is at most
- * 7 * 2^-13 of that product (2^-16 of a typical result), beside half steps of 2^-8 (bfloat16) and 2^-11 (float16) of the
- * result: where large products cancel, or float16's last bit counts, take float32 results.
+ * become it (bytes from 247 on; of gs_quantize's, inputs of 3.3e38 and more).
+ * 16-bit results: the products of each 8 neighbours along k (k / 8 the same) are cut off 2^-13 below the power of two of
+ * their largest before they are summed in float32. That is at most 7 * 2^-13 of that product (2^-16 of a typical result),
+ * beside half steps of 2^-8 (bfloat16) and 2^-11 (float16) of the result: where large products cancel, or float16's last
+ * bit counts, take float32 results.
  * x values and scales of [x_rows, dim]; weight of [experts, cols, dim]; out [rows, cols] of dtype. offsets as
  * gs_expert_plan wrote them, or NULL: one expert has all rows. pairs NULL: x holds the sorted rows, x_rows = rows. pairs
  * as gs_expert_plan wrote them: x holds the tokens, rows = x_rows * choices, and row r is token pairs[r] / choices.

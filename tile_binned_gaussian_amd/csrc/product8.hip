@@ -10,8 +10,11 @@
 // token, so the rows are never copied into sorted order.
 //
 // Bound by the tile's start and end and by the loads' latency: 16384 tokens, 2 choices of 16 experts, 4096 -> 4096 bf16
-// 570 to 610 us, 1.8 PFLOP/s, of which 13 us a tile are spent outside its products; inside them 2.5 PFLOP/s (an 8-bit
-// library product 3.1 to 3.3). Few rows are bound by a tile's chain of stages: 32 rows of 8 experts, 1024 -> 2048, 7.8 us.
+// 570 to 620 us, 1.8 PFLOP/s, of which 13 us a tile are spent outside its products (from the times of two depths; 54
+// registers of a lane of the largest tiles are spilled there); inside them 2.5 PFLOP/s (an 8-bit library product 3.1 to
+// 3.3). They are some 2048 tiles for 256 units: eight turns, and a ninth where an expert's rows begin another tile. Few
+// rows are bound by a tile's chain of stages: 32 rows of 8 experts, 1024 -> 2048, 7.8 us. 400000 rows of 8 experts 128 ->
+// 256 71 us (3.6 TB/s), 256 -> 128 52.
 #include <type_traits>
 
 #include "gs_f8.hpp"
@@ -496,7 +499,8 @@ extern "C" gs_status gs_expert_product(const void *x, const void *x_scales, cons
         hipLaunchKernelGGL((product_kernel<256, 256, 2, 2>), grid(most(256, 256), 1), dim3(256), 0, stream, a);
         GS_LAUNCH_TRY("product_kernel");
     } else if (rows / 128 * ((cols + 127) / 128) < kUnits) {
-        // few rows: 32 of 8 experts, 1024 -> 2048, the kernel 7.8 us, by tiles of 128 10.2; 2048 rows 18.5 and 16.2
+        // few rows: 32 of 8 experts, 1024 -> 2048, the kernel 7.8 us, by tiles of 128 10.2; 2048 rows of 8 experts 11.6 and
+        // 14.2; but 4500 rows of 60 experts, 768 -> 1024, 20.7 and 15.8, 4096 of 16, 2048 -> 2048, 40.6 and 28.1
         hipLaunchKernelGGL((product_kernel<64, 64, 2, 2>), grid(most(64, 64), 4), dim3(256), 0, stream, a);
         GS_LAUNCH_TRY("product_kernel");
     } else {

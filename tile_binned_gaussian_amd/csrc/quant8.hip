@@ -4,7 +4,8 @@
 // by themselves. A block's largest magnitude is exact, so is the division by its scale: each value is rounded once.
 //
 // Bound by memory: 65536 x 4096 bf16 held in 153 us and restored in 129 (5.3 and 6.3 TB/s, part of it from the last-level
-// cache); the smallest calls are a launch of 4 us.
+// cache); the smallest calls are a launch of 4 us. Transposed 16 x 4096 x 4096 float32 375 us (straight 231): 3.6
+// TB/s, read 32 columns of a row at a time.
 #include "gs_f8.hpp"
 
 namespace gs {

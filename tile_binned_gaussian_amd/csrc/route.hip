@@ -1,8 +1,8 @@
 // The router of a layer of experts on gfx950: each token's best experts and their weights, how many tokens every expert
 // got, the balance loss of both, and the gradient of the logits.
 //
-// A group of G lanes holds a token's logits in registers, lane l the experts l, l + G, l + 2 G, ..., so they are read
-// once: the largest gives the softmax, K rounds of the largest that is left give the choices. Each lane counts its own
+// A group of G lanes holds a token's logits in registers, lane l the experts l V to l V + V - 1, so they are read once:
+// the largest gives the softmax, K rounds of the largest that is left give the choices. Each lane counts its own
 // experts' choices and sums their probabilities over all tokens of its workgroup in registers; the workgroups' sums go to
 // a workspace and a second kernel adds them in a fixed order, in float64. A single workgroup (few tokens) finishes alone.
 //
@@ -543,7 +543,14 @@ gs_status check_route(const char *name, int64_t tokens, int experts, int64_t cho
 }
 
 // Lanes that share a token, and a lane's experts. Up to 16 experts a lane has a token of its own and no value crosses
-// lanes; up to 256 they are 16 lanes, within which values cross without LDS.
+// lanes; up to 256 they are 16 lanes, within which values cross without LDS. Float32, 2 choices, forward / gradient in us:
+//   1000000 x 8    one lane 24 / 19, eight 56 / 28           300000 x 64   16 lanes 55 / 31, eight 43 / 30, 64 162 / 68
+//   1000000 x 16   one lane 37 / 36, eight 61 / 34           200000 x 128  16 lanes 56 / 40, eight 57 / 47, 64 123 / 56
+//   500000 x 32    eight lanes 44 / 25, one 50 / 38,         100000 x 256  16 lanes 57 / 52, eight 90 / 68, 64 79 / 40
+//                  16 66 / 35                                20000 x 1024  64 lanes 67 / 130
+// A number of experts that fills no lane's load costs more: 12 for 16 46 / 57, 100 for 128 65 / 73, 200 for 256 76 / 117.
+// Each further choice is a round: 8 of 8 79 / 92, 8 of 64 121 / 38, 8 of 256 99 / 55. The largest lane, 64 experts of more
+// than 1024, leaves 226 registers to scratch.
 constexpr int route_lanes(int experts) { return experts <= 16 ? 1 : experts <= 32 ? 8 : experts <= 256 ? 16 : 64; }
 constexpr int route_columns(int experts) {
     return experts <= 4 ? 4 : experts <= 8 ? 8 : experts <= 16 ? 16 : experts <= 64 ? 4 : experts <= 128 ? 8

@@ -1,15 +1,17 @@
 // Gradient of the experts' weights from activations kept in 8 bits on gfx950:
 // out[e][k][n] = sum over the rows r of expert e of x[r, k] grad[r, n].
 //
-// An e4m3 value times its block's power of two is a bfloat16 without rounding (from multiples of 2^-133 to its largest), and
-// float16 and float32 gradients are the sums of two and three bfloat16 (11 bits, and 24 down to 2^-133), so the products run
-// on the bfloat16 matrix cores and lose nothing; they are summed in float32. The rows are the sum's own axis: both operands lie in LDS as they come, row by row, and the
-// transposing LDS load turns them. Few matrices with many rows each are summed in parts of some rows, which a second
-// kernel adds in order.
+// An e4m3 value times its block's power of two is a bfloat16 without rounding (a multiple of 2^-133 up to its largest is),
+// and float16 and float32 gradients are the sums of two and three bfloat16 (11 bits, and 24 down to 2^-133), so the products
+// run on the bfloat16 matrix cores and lose nothing; they are summed in float32. The rows are the sum's own axis: both
+// operands lie in LDS as they come, row by row, and the transposing LDS load turns them. Few matrices with many rows each
+// are summed in parts of some rows, which a second kernel adds in order.
 //
-// 16384 tokens, 2 choices of 16 experts, 4096 x 4096 bf16 1175 to 1236 us: 1.1 to 1.2 PFLOP/s inside a tile (a bfloat16
+// 16384 tokens, 2 choices of 16 experts, 4096 x 4096: bf16 1175 to 1236 us, 1.1 to 1.2 PFLOP/s inside a tile (a bfloat16
 // library product of one such matrix 1.38), and 18 us a tile for its start and its 256 KB of results, during which its unit
-// has no other. 200000 tokens, 2 of 8, 128 x 256 bf16: 50 us at 4.5 TB/s and 8.5 for the parts' join.
+// has no other (both from the times of two numbers of rows); the 91 to 120 registers that a lane of these tiles spills are
+// written and read there. 16 x 2048 rows float16 3150 us, float32 3590, 4080 for 4095 columns. 200000 tokens, 2 of 8,
+// 128 x 256 bf16: 50 us at 4.5 TB/s and 8.5 for the parts' join.
 #include <utility>
 
 #include "gs_f8.hpp"
@@ -239,8 +241,8 @@ __global__ __launch_bounds__(kThreads, F == 2 ? 2 : 1) void weight_grad_kernel(G
                 for (int q = 0; q < P; ++q)
                     *reinterpret_cast<u32x4 *>(to + (1 + q) * kPlaneBytes) = __builtin_bit_cast(u32x4, s[q]) & there;
             };
-            // What this thread kept of x, once more where a block may hold values beyond bfloat16's largest: looked at after
-            // the step, not between its products (5% there)
+            // What this thread kept of x, once more where a block may hold values beyond bfloat16's largest: looked at
+            // after the step, not between its products (5% there)
             const auto keep_finite = [&](int at, uint8_t *planes) {
                 int most = step[at][0];
 #pragma unroll
