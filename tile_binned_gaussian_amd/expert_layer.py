@@ -5,9 +5,9 @@ tokens are sorted by expert, every expert is a two-layer perceptron on its own r
 to their tokens. The backward is written out call by call; weight matrices move by their orthogonalised momentum.
 The experts' own products are plain library products, one per expert and direction, or with ``products="f8"`` the
 library's own on values held in 8 bits: the tokens and the hidden values are then kept for the backward in 8 bits, no row
-is copied into sorted order, and nothing waits for the host, so the layer can be captured into a graph. ``ColorHead`` maps
-features to colours in (0, 1). Both keep float32 parameters; the layer computes in the type it is made for, the head in
-float32.
+is copied into sorted order, and nothing waits for the host, so the layer can be captured into a graph. The router's
+projection and its gradients are plain products of the tokens as they are either way. ``ColorHead`` maps features to
+colours in (0, 1). Both keep float32 parameters; the layer computes in the type it is made for, the head in float32.
 """
 from __future__ import annotations
 
